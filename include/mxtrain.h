@@ -1,0 +1,93 @@
+/*
+ * mxtrain.h -- C ABI of libmxtrain.so: the operators of a mixture-of-experts
+ * layer's training step that stay in 16 or 32 bits next to the MXFP8 casts
+ * and products of mxfp8.h, on MI355X (gfx950).
+ *
+ * Conventions shared by every call (those of mxfp8.h):
+ *  - All data pointers are DEVICE pointers.  bf16 values are raw 16-bit
+ *    patterns.  Dimensions, strides and leading dimensions (ld_*) are int64
+ *    element counts.  Every matrix is row-major with unit column stride and
+ *    the given row stride.
+ *  - The caller owns and allocates every buffer, workspaces among them; the
+ *    library never allocates, frees, synchronizes or reads device memory
+ *    from the host.
+ *  - Work is enqueued asynchronously on `stream` (a hipStream_t; NULL is the
+ *    default stream), with the stream's device current.  A call that launches
+ *    several kernels orders them on that stream.
+ *  - Every argument is checked before any launch; a failed check returns a
+ *    status and enqueues nothing.
+ *  - Outputs and workspaces must not alias inputs or each other (not
+ *    checked).  Equal inputs give equal bits: nothing is summed in an order
+ *    that changes from call to call.
+ *  - Calls are thread-safe; the library keeps no mutable global state.
+ */
+#ifndef MXTRAIN_H
+#define MXTRAIN_H
+
+#include <stdint.h>
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum mxtrain_status {
+    MXTRAIN_OK = 0,
+    MXTRAIN_ERR_NULL = 1,      /* a required pointer is NULL                        */
+    MXTRAIN_ERR_SHAPE = 2,     /* a dimension is negative or out of its range       */
+    MXTRAIN_ERR_STRIDE = 3,    /* ld smaller than the row, or not the multiple asked */
+    MXTRAIN_ERR_ALIGN = 4,     /* a pointer lacks the alignment asked               */
+    MXTRAIN_ERR_TYPE = 5,      /* a type code is not one the call takes             */
+    MXTRAIN_ERR_OVERFLOW = 6,  /* an extent or the launch grid is too large         */
+    MXTRAIN_ERR_LAUNCH = 7,    /* the HIP runtime refused the launch                */
+    MXTRAIN_ERR_WORKSPACE = 8, /* the workspace is smaller than the call needs      */
+    MXTRAIN_ERR_VALUE = 9      /* a scalar argument is not one the call takes       */
+} mxtrain_status;
+
+/* Element types. */
+enum { MXTRAIN_BF16 = 0, MXTRAIN_F32 = 1 };
+
+/*
+ * Layer norm over the last axis, row i of x [M, N]:
+ *   mean = sum_j x_ij / N,  rstd = 1 / sqrt(sum_j (x_ij - mean)^2 / N + eps),
+ *   y_ij = (x_ij - mean) rstd weight_j + bias_j.
+ *   x, y       : dtype (MXTRAIN_BF16 or MXTRAIN_F32), row strides ld_x, ld_y.
+ *   weight, bias : param_dtype [N] each, either may be NULL (ones, zeros).
+ *   mean, rstd : fp32 [M], what the backward pass reads; either may be NULL.
+ * Computed in fp32, rounded once into y.  Pointers aligned to their element
+ * size; rows that all start 16-byte aligned with N a multiple of 16 bytes'
+ * worth of elements move 16 bytes at a time, others by element.  eps >= 0 and
+ * finite (MXTRAIN_ERR_VALUE).  N >= 1 when M > 0; M, N < 2^31.
+ * M == 0 returns MXTRAIN_OK and enqueues nothing.
+ */
+mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *weight, const void *bias,
+                                      int param_dtype, int64_t M, int64_t N, int dtype, float eps,
+                                      void *y, int64_t ld_y, float *mean, float *rstd, void *stream);
+
+/*
+ * Gradients of the above for upstream dy [M, N], with xh = (x - mean) rstd
+ * and g = dy weight:
+ *   dx = rstd (g - sum_j g / N - xh sum_j (g xh) / N),
+ *   dweight_j = sum_i dy_ij xh_ij,  dbias_j = sum_i dy_ij.
+ *   dy, x, dx : dtype, row strides ld_dy, ld_x, ld_dx.
+ *   mean, rstd : fp32 [M], as the forward pass wrote them.
+ *   weight    : param_dtype [N] or NULL (ones).
+ *   dweight, dbias : fp32 [N]; either may be NULL (not wanted).
+ *   workspace : at least mxtrain_layer_norm_bwd_workspace(M, N) bytes, 4-byte
+ *               aligned; may be NULL where dweight and dbias both are.
+ * M == 0 writes zeros into dweight and dbias.
+ */
+int64_t mxtrain_layer_norm_bwd_workspace(int64_t M, int64_t N);
+mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x,
+                                      const float *mean, const float *rstd, const void *weight, int param_dtype,
+                                      int64_t M, int64_t N, int dtype, void *dx, int64_t ld_dx,
+                                      float *dweight, float *dbias,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
+
+/* Static, NUL-terminated description of a status code (never NULL). */
+const char *mxtrain_status_str(mxtrain_status status);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MXTRAIN_H */

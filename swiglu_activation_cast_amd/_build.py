@@ -1,6 +1,8 @@
 """Compiles the gfx950 HIP libraries in-tree with hipcc: libmxfp8.so (the
-casts and their consumer, behind include/mxfp8.h) and libmxstream.so (the
-streaming bandwidth probe behind include/mxstream.h, measurement only)."""
+casts and their consumer, behind include/mxfp8.h), libmxtrain.so (the 16- and
+32-bit operators of a training step beside them, behind include/mxtrain.h) and
+libmxstream.so (the streaming bandwidth probe behind include/mxstream.h,
+measurement only)."""
 from __future__ import annotations
 
 import hashlib
@@ -16,12 +18,15 @@ LIB_PATH = os.path.join(PKG_DIR, "libmxfp8.so")
 SOURCES = [os.path.join(CSRC, "mxfp8.hip")]
 STREAM_LIB_PATH = os.path.join(PKG_DIR, "libmxstream.so")
 STREAM_SOURCES = [os.path.join(CSRC, "mx_stream.hip")]
+TRAIN_LIB_PATH = os.path.join(PKG_DIR, "libmxtrain.so")
+TRAIN_SOURCES = [os.path.join(CSRC, "train", "mxtrain.hip")]
 ARCH = "gfx950"
 
 
 def kernel_source_hash() -> str:
-    """Short hash of the kernel sources (the .hip/.hpp/.h files under
-    csrc/): ties a recorded profile to the code it measured."""
+    """Short hash of the kernel sources of libmxfp8.so and libmxstream.so
+    (the .hip/.hpp/.h files directly under csrc/): ties a recorded profile
+    to the code it measured."""
     h = hashlib.sha256()
     for name in sorted(os.listdir(CSRC)):
         if not name.endswith((".hip", ".hpp", ".h")):
@@ -72,6 +77,7 @@ def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bo
 
 def build_all(verbose: bool = False) -> None:
     build(verbose=verbose)
+    build(TRAIN_LIB_PATH, verbose=verbose, sources=TRAIN_SOURCES)
     build(STREAM_LIB_PATH, verbose=verbose, sources=STREAM_SOURCES)
 
 

@@ -1,0 +1,201 @@
+"""ctypes binding of libmxtrain.so (argument marshalling only).
+
+The training operators beside the MXFP8 casts: layer norm, the experts' bf16
+products and the orthogonalised weight update.  As in the casts' binding,
+every function takes torch tensors that live on the GPU, checks shapes,
+dtypes and devices (the C ABI sees bare pointers), allocates outputs and
+workspaces with torch where the caller passes none, and calls the C entry
+point of the same name on torch's current stream, or on `stream`.  There is no
+CPU or PyTorch fallback.
+
+A workspace that a call allocates itself may be handed out again by torch as
+soon as the call returns, while its kernels still run: on `stream` other than
+the current one it is recorded there, so that it is not reused too early.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+from typing import Optional, Tuple
+
+import torch
+
+_PKG_DIR = os.path.dirname(os.path.abspath(__file__))
+TRAIN_LIB_PATH = os.path.join(_PKG_DIR, "libmxtrain.so")
+
+_i64 = ctypes.c_int64
+_p = ctypes.c_void_p
+_int = ctypes.c_int
+_f32 = ctypes.c_float
+
+_SIGNATURES = {
+    "mxtrain_layer_norm_fwd": (_int, [_p, _i64, _p, _p, _int, _i64, _i64, _int, _f32, _p, _i64, _p, _p, _p]),
+    "mxtrain_layer_norm_bwd_workspace": (_i64, [_i64, _i64]),
+    "mxtrain_layer_norm_bwd": (_int, [_p, _i64, _p, _i64, _p, _p, _p, _int, _i64, _i64, _int, _p, _i64, _p, _p, _p,
+                                      _i64, _p]),
+    "mxtrain_status_str": (ctypes.c_char_p, [_int]),
+}
+
+# element types (MXTRAIN_* in mxtrain.h)
+_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+
+_train_lib = None
+
+
+class MxtrainError(RuntimeError):
+    def __init__(self, fn: str, status: int, text: str):
+        super().__init__(f"{fn} failed with status {status}: {text}")
+        self.status = status
+
+
+def train_lib() -> ctypes.CDLL:
+    """The loaded libmxtrain.so with argument types set (raises if not built)."""
+    global _train_lib
+    if _train_lib is not None:
+        return _train_lib
+    if not os.path.exists(TRAIN_LIB_PATH):
+        raise RuntimeError(
+            f"{TRAIN_LIB_PATH} is not built; run `python -m swiglu_activation_cast_amd._build` "
+            "(or __graft_entry__.build()) first"
+        )
+    handle = ctypes.CDLL(TRAIN_LIB_PATH)
+    for name, (restype, argtypes) in _SIGNATURES.items():
+        fn = getattr(handle, name)
+        fn.argtypes = argtypes
+        fn.restype = restype
+    _train_lib = handle
+    return handle
+
+
+def train_status_str(status: int) -> str:
+    return train_lib().mxtrain_status_str(int(status)).decode()
+
+
+def _call(name: str, device: torch.device, *args) -> None:
+    """The C call with `device` current; raises on a status."""
+    fn = getattr(train_lib(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args)
+    if status != 0:
+        raise MxtrainError(name, status, train_status_str(status))
+
+
+def _stream_of(device: torch.device, stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _workspace(nbytes: int, given: Optional[torch.Tensor], device: torch.device, stream) -> torch.Tensor:
+    """`given`, checked, or a new workspace that is safe on `stream`."""
+    if given is not None:
+        if given.device != device or not given.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+        if given.numel() * given.element_size() < nbytes:
+            raise ValueError(f"workspace must hold at least {nbytes} bytes")
+        return given
+    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
+    if stream is not None:
+        handle = _stream_of(device, stream)
+        if handle != torch.cuda.current_stream(device).cuda_stream:
+            ws.record_stream(torch.cuda.ExternalStream(handle, device=device))
+    return ws
+
+
+def _gpu(t, name: str, dtypes, dim: int, device=None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
+        want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
+        raise TypeError(f"{name} must be a {want} tensor, got {getattr(t, 'dtype', type(t).__name__)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(t.shape)}")
+    return t
+
+
+def _ld(t: torch.Tensor, name: str) -> int:
+    """Row stride of the last two dimensions, whose columns must be adjacent."""
+    rows, cols = t.shape[-2:]
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
+
+
+def _param(t: Optional[torch.Tensor], name: str, n: int, device, dtype=None):
+    if t is None:
+        return None
+    _gpu(t, name, (torch.bfloat16, torch.float32) if dtype is None else (dtype,), 1, device)
+    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must hold {n} adjacent elements")
+    return t.data_ptr()
+
+
+def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _gpu(t, name, (dtype,), len(shape), device)
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+def mxtrain_layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None,
+                           bias: Optional[torch.Tensor] = None, *, eps: float = 1e-5,
+                           out: Optional[torch.Tensor] = None, mean: Optional[torch.Tensor] = None,
+                           rstd: Optional[torch.Tensor] = None, stream=None
+                           ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Layer norm of the rows of x [M, N] (bf16 or fp32); returns (y, mean, rstd).
+
+    y = (x - mean) * rstd * weight + bias in x's dtype, with the fp32 row
+    statistics [M] that the backward pass reads.  weight and bias: [N], bf16
+    or fp32 (the same), or None."""
+    _gpu(x, "x", _FLOATS, 2)
+    M, N = x.shape
+    dev = x.device
+    if weight is not None and bias is not None and weight.dtype != bias.dtype:
+        raise TypeError("weight and bias must have the same dtype")
+    pw, pb = _param(weight, "weight", N, dev), _param(bias, "bias", N, dev)
+    param = weight if weight is not None else bias
+    y = _out(out, "out", (M, N), x.dtype, dev)
+    mean = _out(mean, "mean", (M,), torch.float32, dev)
+    rstd = _out(rstd, "rstd", (M,), torch.float32, dev)
+    _call("mxtrain_layer_norm_fwd", dev, x.data_ptr(), _ld(x, "x"), pw, pb,
+          _TYPES[param.dtype] if param is not None else 0, M, N, _TYPES[x.dtype], eps, y.data_ptr(), _ld(y, "out"),
+          _param(mean, "mean", M, dev), _param(rstd, "rstd", M, dev), _stream_of(dev, stream))
+    return y, mean, rstd
+
+
+def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                           weight: Optional[torch.Tensor] = None, *, out: Optional[torch.Tensor] = None,
+                           dweight: Optional[torch.Tensor] = None, dbias: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None, stream=None
+                           ) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Gradients of mxtrain_layer_norm_fwd for upstream dy; returns (dx, dweight, dbias).
+
+    dx has x's dtype; dweight and dbias are fp32 [N] sums over the rows."""
+    _gpu(x, "x", _FLOATS, 2)
+    M, N = x.shape
+    dev = x.device
+    _gpu(dy, "dy", (x.dtype,), 2, dev)
+    if dy.shape != x.shape:
+        raise ValueError("dy and x must have the same shape")
+    pw = _param(weight, "weight", N, dev)
+    pm, pr = _param(mean, "mean", M, dev, torch.float32), _param(rstd, "rstd", M, dev, torch.float32)
+    dx = _out(out, "out", (M, N), x.dtype, dev)
+    dw = _out(dweight, "dweight", (N,), torch.float32, dev)
+    db = _out(dbias, "dbias", (N,), torch.float32, dev)
+    nbytes = train_lib().mxtrain_layer_norm_bwd_workspace(M, N)
+    ws = _workspace(nbytes, workspace, dev, stream)
+    _call("mxtrain_layer_norm_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), pm, pr, pw,
+          _TYPES[weight.dtype] if weight is not None else 0, M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
+          _param(dw, "dweight", N, dev), _param(db, "dbias", N, dev), ws.data_ptr(),
+          ws.numel() * ws.element_size(), _stream_of(dev, stream))
+    return dx, dw, db

@@ -1,0 +1,236 @@
+// mxtrain.hip -- C ABI of libmxtrain.so: argument checks, the choice of kernel
+// and the launches.  Nothing is allocated, synchronized or read back, and no
+// exception can leave an entry point (nothing here throws).
+#include <hip/hip_runtime.h>
+#include <algorithm>
+#include <cmath>
+#include <limits.h>
+#include <stdint.h>
+
+#include "mxtrain.h"
+#include "tr_norm.hpp"
+
+namespace {
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+// Elements of a [rows, cols] matrix with row stride ld, counted from its
+// base, fit int64 with room for the element size and a batch on top.
+bool extent_ok(int64_t rows, int64_t cols, int64_t ld) {
+  int64_t r;
+  if (rows == 0 || cols == 0) return true;
+  return !__builtin_mul_overflow(rows - 1, ld, &r) && !__builtin_add_overflow(r, cols, &r) && r < (INT64_MAX >> 4);
+}
+
+template <class Args>
+mxtrain_status launch(const void *kernel, int64_t blocks, int threads, const Args &a, void *stream, unsigned lds = 0) {
+  // grid x times block x stays below 2^31
+  if (blocks <= 0 || blocks > (int64_t)INT32_MAX / threads) return MXTRAIN_ERR_OVERFLOW;
+  Args copy = a;
+  void *kargs[] = {&copy};
+  const hipError_t err =
+      hipLaunchKernel(kernel, dim3((unsigned)blocks), dim3((unsigned)threads), kargs, lds, (hipStream_t)stream);
+  return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;
+}
+
+// ------------------------------------------------------------- layer norm
+// How a row is spread over threads: `tpr` threads (0: a whole workgroup of
+// `threads`) holding `elems` elements each; elems == 0: the row does not fit
+// registers.
+struct RowPlan {
+  int tpr, threads, elems;
+};
+
+// Short rows share a workgroup of 256 threads (16 or 64 threads a row); a
+// longer one has a workgroup of just the wavefronts it needs.  With many rows
+// a thread holds as many elements as keep the workgroup at 256 threads (fewer
+// threads to join per row, the other workgroups of the CU hide the waits);
+// with few rows, where one row's latency is the time, as few as 1024 threads
+// allow.
+RowPlan row_plan(int64_t M, int64_t N, int vec, bool bwd) {
+  const bool many = M >= 1024;
+  if (many && N <= 128) return {16, 256, 8};
+  if (N <= 512) return {64, 256, 8};
+  if (many && N <= 1024) return {64, 256, 16};
+  const int most32 = bwd ? 512 : 1024;  // threads of a workgroup whose threads hold 32 elements
+  const int cap = many ? 256 : 1024;
+  const int64_t chunks = (N + vec - 1) / vec;
+  for (int pass = 0; pass < 2; pass++)
+    for (int e = 8; e <= 32; e *= 2) {
+      const int64_t per = e / vec, need = (chunks + per - 1) / per;
+      const int64_t t = (need + 63) / 64 * 64;
+      if (t <= std::min(pass == 0 ? cap : 1024, e == 32 ? most32 : 1024)) return {0, (int)t, e};
+    }
+  return {0, 1024, 0};
+}
+
+// Workgroups of the backward pass, each of which leaves one partial row of
+// 2 N sums: at most 512 (two per CU), and at least four rows each.
+constexpr int64_t kLnParts = 512;
+int64_t ln_parts(int64_t M) { return std::min<int64_t>(kLnParts, (M + 3) / 4); }
+
+template <class T, int VEC, int TPR, int E, bool BWD>
+const void *ln_pick() {
+  if constexpr (BWD) return (const void *)&mxt::k_ln_bwd<T, VEC, TPR, E / VEC>;
+  else return (const void *)&mxt::k_ln_fwd<T, VEC, TPR, E / VEC>;
+}
+
+template <class T, int VEC, bool BWD>
+const void *ln_kernel(const RowPlan &p) {
+  if (p.tpr == 16) return ln_pick<T, VEC, 16, 8, BWD>();
+  if (p.tpr == 64) return p.elems == 8 ? ln_pick<T, VEC, 64, 8, BWD>() : ln_pick<T, VEC, 64, 16, BWD>();
+  return p.elems == 8    ? ln_pick<T, VEC, 0, 8, BWD>()
+         : p.elems == 16 ? ln_pick<T, VEC, 0, 16, BWD>()
+                         : ln_pick<T, VEC, 0, 32, BWD>();
+}
+
+template <bool BWD>
+const void *ln_kernel(const RowPlan &p, int dtype, bool vec) {
+  if (p.elems == 0) {
+    if constexpr (BWD)
+      return dtype == MXTRAIN_F32 ? (const void *)&mxt::k_ln_bwd_long<float> : (const void *)&mxt::k_ln_bwd_long<uint16_t>;
+    else
+      return dtype == MXTRAIN_F32 ? (const void *)&mxt::k_ln_fwd_long<float> : (const void *)&mxt::k_ln_fwd_long<uint16_t>;
+  }
+  if (dtype == MXTRAIN_F32) return vec ? ln_kernel<float, 4, BWD>(p) : ln_kernel<float, 1, BWD>(p);
+  return vec ? ln_kernel<uint16_t, 8, BWD>(p) : ln_kernel<uint16_t, 1, BWD>(p);
+}
+
+bool type_ok(int t) { return t == MXTRAIN_BF16 || t == MXTRAIN_F32; }
+int size_of(int t) { return t == MXTRAIN_F32 ? 4 : 2; }
+
+// Checks shared by both passes (M > 0, N > 0 from here on).
+mxtrain_status ln_check(const void *const *mats, const int64_t *lds, int n, const void *weight, const void *bias,
+                        int64_t M, int64_t N, int dtype, int param_dtype) {
+  const uintptr_t e = (uintptr_t)size_of(dtype);
+  for (int i = 0; i < n; i++)
+    if (!mats[i]) return MXTRAIN_ERR_NULL;
+  for (int i = 0; i < n; i++)
+    if (lds[i] < N) return MXTRAIN_ERR_STRIDE;
+  for (int i = 0; i < n; i++)
+    if (!aligned(mats[i], e)) return MXTRAIN_ERR_ALIGN;
+  if (!aligned(weight, (uintptr_t)size_of(param_dtype)) || !aligned(bias, (uintptr_t)size_of(param_dtype)))
+    return MXTRAIN_ERR_ALIGN;
+  for (int i = 0; i < n; i++)
+    if (!extent_ok(M, N, lds[i])) return MXTRAIN_ERR_OVERFLOW;
+  return MXTRAIN_OK;
+}
+
+bool ln_vec(const void *const *mats, const int64_t *lds, int n, int64_t N, int dtype) {
+  const int v = 16 / size_of(dtype);
+  if (N % v != 0) return false;
+  for (int i = 0; i < n; i++)
+    if (!aligned(mats[i], 16) || lds[i] % v != 0) return false;
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *weight, const void *bias,
+                                      int param_dtype, int64_t M, int64_t N, int dtype, float eps, void *y,
+                                      int64_t ld_y, float *mean, float *rstd, void *stream) {
+  if (!type_ok(dtype) || !type_ok(param_dtype)) return MXTRAIN_ERR_TYPE;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return MXTRAIN_ERR_VALUE;
+  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX - 4096) return MXTRAIN_ERR_SHAPE;
+  if (M == 0) return MXTRAIN_OK;
+  if (N == 0) return MXTRAIN_ERR_SHAPE;
+  const void *mats[] = {x, y};
+  const int64_t lds[] = {ld_x, ld_y};
+  const mxtrain_status st = ln_check(mats, lds, 2, weight, bias, M, N, dtype, param_dtype);
+  if (st != MXTRAIN_OK) return st;
+  if (!aligned(mean, 4) || !aligned(rstd, 4)) return MXTRAIN_ERR_ALIGN;
+  const bool vec = ln_vec(mats, lds, 2, N, dtype);
+  const RowPlan p = row_plan(M, N, vec ? 16 / size_of(dtype) : 1, false);
+  mxt::LnArgs g{};
+  g.x = x;
+  g.w = weight;
+  g.b = bias;
+  g.y = y;
+  g.ld_x = ld_x;
+  g.ld_y = ld_y;
+  g.mean = mean;
+  g.rstd = rstd;
+  g.M = M;
+  g.N = (int32_t)N;
+  g.w_f32 = param_dtype == MXTRAIN_F32;
+  g.eps = eps;
+  const int64_t rows = p.tpr ? 256 / p.tpr : 1;
+  return launch(ln_kernel<false>(p, dtype, vec), (M + rows - 1) / rows, p.threads, g, stream);
+}
+
+int64_t mxtrain_layer_norm_bwd_workspace(int64_t M, int64_t N) {
+  if (M <= 0 || N <= 0 || M > INT32_MAX || N > INT32_MAX - 4096) return 0;
+  return ln_parts(M) * 2 * N * (int64_t)sizeof(float);
+}
+
+mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void *x, int64_t ld_x, const float *mean,
+                                      const float *rstd, const void *weight, int param_dtype, int64_t M, int64_t N,
+                                      int dtype, void *dx, int64_t ld_dx, float *dweight, float *dbias,
+                                      void *workspace, int64_t workspace_bytes, void *stream) {
+  if (!type_ok(dtype) || !type_ok(param_dtype)) return MXTRAIN_ERR_TYPE;
+  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX - 4096) return MXTRAIN_ERR_SHAPE;
+  if (N == 0) return M == 0 ? MXTRAIN_OK : MXTRAIN_ERR_SHAPE;
+  if (!aligned(dweight, 4) || !aligned(dbias, 4)) return MXTRAIN_ERR_ALIGN;
+  const bool sums = dweight || dbias;
+  int64_t parts = 0;
+  if (M > 0) {
+    const void *mats[] = {dy, x, dx};
+    const int64_t lds[] = {ld_dy, ld_x, ld_dx};
+    if (!mean || !rstd || (sums && !workspace)) return MXTRAIN_ERR_NULL;
+    const mxtrain_status st = ln_check(mats, lds, 3, weight, nullptr, M, N, dtype, param_dtype);
+    if (st != MXTRAIN_OK) return st;
+    if (!aligned(mean, 4) || !aligned(rstd, 4) || (sums && !aligned(workspace, 4))) return MXTRAIN_ERR_ALIGN;
+    if (sums && workspace_bytes < mxtrain_layer_norm_bwd_workspace(M, N)) return MXTRAIN_ERR_WORKSPACE;
+    const bool vec = ln_vec(mats, lds, 3, N, dtype);
+    const RowPlan p = row_plan(M, N, vec ? 16 / size_of(dtype) : 1, true);
+    mxt::LnArgs g{};
+    g.x = x;
+    g.dy = dy;
+    g.w = weight;
+    g.y = dx;
+    g.ld_x = ld_x;
+    g.ld_dy = ld_dy;
+    g.ld_y = ld_dx;
+    g.mean = const_cast<float *>(mean);
+    g.rstd = const_cast<float *>(rstd);
+    g.part = sums ? static_cast<float *>(workspace) : nullptr;
+    g.M = M;
+    g.N = (int32_t)N;
+    g.w_f32 = param_dtype == MXTRAIN_F32;
+    const int64_t slots = p.tpr ? 256 / p.tpr : 1;
+    parts = std::min<int64_t>(ln_parts(M), (M + slots - 1) / slots);
+    const unsigned joined = p.tpr ? (unsigned)(slots * 2 * N * (int64_t)sizeof(float)) : 0u;
+    const mxtrain_status run = launch(ln_kernel<true>(p, dtype, vec), parts, p.threads, g, stream, joined);
+    if (run != MXTRAIN_OK) return run;
+  }
+  if (!sums) return MXTRAIN_OK;
+  const float *part = static_cast<const float *>(workspace);
+  int n_parts = (int)parts;
+  int32_t n = (int32_t)N;
+  void *kargs[] = {&part, &n_parts, &n, &dweight, &dbias};
+  const int64_t blocks = (2 * N + 31) / 32;
+  if (blocks > INT32_MAX / 1024) return MXTRAIN_ERR_OVERFLOW;
+  const hipError_t err = hipLaunchKernel((const void *)&mxt::k_ln_join, dim3((unsigned)blocks), dim3(1024), kargs, 0,
+                                         (hipStream_t)stream);
+  return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;
+}
+
+const char *mxtrain_status_str(mxtrain_status status) {
+  switch (status) {
+    case MXTRAIN_OK: return "ok";
+    case MXTRAIN_ERR_NULL: return "a required pointer is NULL";
+    case MXTRAIN_ERR_SHAPE: return "a dimension is negative or out of its range";
+    case MXTRAIN_ERR_STRIDE: return "a leading dimension is smaller than the row, or not the multiple asked";
+    case MXTRAIN_ERR_ALIGN: return "a pointer lacks the alignment asked";
+    case MXTRAIN_ERR_TYPE: return "an element type is not one the call takes";
+    case MXTRAIN_ERR_OVERFLOW: return "sizes overflow the addressable range or the launch grid";
+    case MXTRAIN_ERR_LAUNCH: return "the HIP runtime refused the kernel launch";
+    case MXTRAIN_ERR_WORKSPACE: return "the workspace is smaller than the call needs";
+    case MXTRAIN_ERR_VALUE: return "a scalar argument is not one the call takes";
+  }
+  return "unknown status";
+}
+
+}  // extern "C"

@@ -1,0 +1,393 @@
+// tr_norm.hpp -- layer norm, forward and backward (gfx950).
+//
+// Forward, per row x of N elements:
+//   mean = sum x / N,  rstd = 1 / sqrt(sum (x - mean)^2 / N + eps),
+//   y = (x - mean) rstd w + b.
+// Backward, with xh = (x - mean) rstd and g = dy w:
+//   dx = rstd (g - sum g / N - xh sum (g xh) / N),
+//   dw = sum over rows of dy xh,  db = sum over rows of dy.
+//
+// Both are bound by HBM: the forward reads x and writes y, the backward reads
+// dy and x and writes dx, each once.  So a row stays in registers between its
+// reductions and its output (up to 32 elements a thread), and the backward's column sums are kept in registers over all the rows that
+// a workgroup walks, written once per workgroup as a partial row and joined
+// by a second kernel in a fixed order (no atomics: equal inputs give equal
+// bits).  All arithmetic is fp32; outputs are rounded once.
+//
+// Rows far off centre: the variance is taken from deviations d = x - m to the
+// mean m already known, and the second reduction sums d beside d^2.  With
+// e = sum d / N, m + e is the mean freed from the first sum's rounding, and
+// sum d^2 / N - e^2 the variance about it; y uses d - e, which keeps the
+// places that m itself has no room for.  The extra sum rides along in the
+// second reduction.  Where the row's mean is smaller than its spread, the
+// first sum is as exact as the second (more so for bf16 rows, whose few
+// places add up without rounding), and e, then only rounding, is dropped.
+#pragma once
+#include "tr_common.hpp"
+
+namespace mxt {
+
+struct LnArgs {
+  const void *x, *dy, *w, *b;
+  void *y;  // y, or dx in the backward pass
+  int64_t ld_x, ld_dy, ld_y;
+  float *mean, *rstd;  // written by the forward (may be NULL), read by the backward
+  float *part;         // backward: partial column sums [gridDim.x][2][N], or NULL
+  int64_t M;
+  int32_t N;
+  int32_t w_f32;  // weight and bias are fp32 (else bf16)
+  float eps;
+};
+
+// A thread holds CH chunks of VEC consecutive elements; chunk i starts at
+// column (i * TPR + t) * VEC.  VEC is 16 bytes' worth where every row starts
+// 16-byte aligned and N is a multiple of it, otherwise 1.
+template <class T, int VEC>
+__device__ __forceinline__ void load_chunk(const T *p, float *v) {
+  if constexpr (VEC == 1) {
+    v[0] = to_f32(*mx::gptr(p));
+  } else if constexpr (sizeof(T) == 2) {
+    const mx::u32x4_t q = *mx::gptr(reinterpret_cast<const mx::u32x4_t *>(p));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+      v[2 * i] = mx::lo_f(q[i]);
+      v[2 * i + 1] = mx::hi_f(q[i]);
+    }
+  } else {
+    const f32x4_t q = *mx::gptr(reinterpret_cast<const f32x4_t *>(p));
+#pragma unroll
+    for (int i = 0; i < 4; i++) v[i] = q[i];
+  }
+}
+
+template <class T, int VEC>
+__device__ __forceinline__ void store_chunk(T *p, const float *v) {
+  if constexpr (VEC == 1) {
+    *mx::gptr(p) = from_f32<T>(v[0]);
+  } else if constexpr (sizeof(T) == 2) {
+    mx::u32x4_t q;
+#pragma unroll
+    for (int i = 0; i < 4; i++) q[i] = mx::pack_bf16(v[2 * i], v[2 * i + 1]);
+    __builtin_nontemporal_store(q, mx::gptr(reinterpret_cast<mx::u32x4_t *>(p)));
+  } else {
+    f32x4_t q;
+#pragma unroll
+    for (int i = 0; i < 4; i++) q[i] = v[i];
+    __builtin_nontemporal_store(q, mx::gptr(reinterpret_cast<f32x4_t *>(p)));
+  }
+}
+
+// VEC elements of the weight or bias (bf16 or fp32; `missing` where NULL).
+// A vector is read as VEC scalars where the parameter is fp32 against bf16
+// rows or its base is not 16-byte aligned: it stays in cache either way.
+template <int VEC>
+__device__ __forceinline__ void load_param(const void *p, bool f32, int32_t col, float missing, float *v) {
+  if (!p) {
+#pragma unroll
+    for (int i = 0; i < VEC; i++) v[i] = missing;
+  } else if (f32) {
+    const float *q = static_cast<const float *>(p) + col;
+#pragma unroll
+    for (int i = 0; i < VEC; i++) v[i] = *mx::gptr(q + i);
+  } else {
+    const uint16_t *q = static_cast<const uint16_t *>(p) + col;
+#pragma unroll
+    for (int i = 0; i < VEC; i++) v[i] = to_f32(*mx::gptr(q + i));
+  }
+}
+
+// Sums of a and b over the TPR threads of a row, in every one of them.
+// TPR <= 64: lane swaps inside the wavefront.  TPR == 0: the row is the whole
+// workgroup (a multiple of 64 threads); `sm` holds two values per wavefront
+// and is not reused before another barrier.
+template <int TPR>
+__device__ __forceinline__ void row_sum2(float &a, float &b, float (*sm)[2]) {
+  constexpr int W = TPR == 0 ? 64 : TPR;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) {
+    a += __shfl_xor(a, o, 64);
+    b += __shfl_xor(b, o, 64);
+  }
+  if constexpr (TPR == 0) {
+    const int w = threadIdx.x >> 6, n = blockDim.x >> 6;
+    if ((threadIdx.x & 63) == 0) {
+      sm[w][0] = a;
+      sm[w][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.0f;
+    for (int i = 0; i < n; i++) {
+      a += sm[i][0];
+      b += sm[i][1];
+    }
+  }
+}
+
+// TPR threads per row (0: the whole workgroup) in the kernels below.
+// The correction e and 1 / sqrt(var + eps) from the second reduction's sums.
+__device__ __forceinline__ float ln_rstd(float m, float q, float &e, const LnArgs &g) {
+  q /= (float)g.N;
+  e = m * m > q ? e / (float)g.N : 0.0f;
+  const float var = fmaf(-e, e, q);
+  return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + g.eps);  // a NaN stays one
+}
+
+template <class T, int VEC, int TPR, int CH>
+__global__ __launch_bounds__(TPR == 0 ? 1024 : 256) void k_ln_fwd(const LnArgs g) {
+  __shared__ float sm[2][16][2];
+  const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
+  const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % (TPR == 0 ? 1 : TPR);
+  const int64_t row = TPR == 0 ? (int64_t)blockIdx.x
+                               : (int64_t)blockIdx.x * (256 / (TPR == 0 ? 256 : TPR)) + threadIdx.x / (TPR == 0 ? 1 : TPR);
+  if (TPR != 0 && row >= g.M) return;  // whole rows of lanes; no barrier follows
+  const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
+  T *y = static_cast<T *>(g.y) + row * g.ld_y;
+  float v[CH][VEC];
+  float s = 0.0f, unused = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const int32_t col = (i * tpr + t) * VEC;
+    if (col < g.N) {
+      load_chunk<T, VEC>(x + col, v[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[i][j] = 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < CH; i++)
+#pragma unroll
+    for (int j = 0; j < VEC; j++) s += v[i][j];
+  row_sum2<TPR>(s, unused, sm[0]);
+  const float m = s / (float)g.N;
+  float q = 0.0f, e = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; i++)
+    if ((i * tpr + t) * VEC < g.N) {
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float d = v[i][j] - m;
+        v[i][j] = d;
+        e += d;
+        q = fmaf(d, d, q);
+      }
+    }
+  row_sum2<TPR>(q, e, sm[1]);
+  const float rstd = ln_rstd(m, q, e, g);
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const int32_t col = (i * tpr + t) * VEC;
+    if (col < g.N) {
+      float w[VEC], b[VEC];
+      load_param<VEC>(g.w, g.w_f32, col, 1.0f, w);
+      load_param<VEC>(g.b, g.w_f32, col, 0.0f, b);
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[i][j] = fmaf((v[i][j] - e) * rstd, w[j], b[j]);
+      store_chunk<T, VEC>(y + col, v[i]);
+    }
+  }
+  if (t == 0 && g.mean) *mx::gptr(g.mean + row) = m + e;
+  if (t == 0 && g.rstd) *mx::gptr(g.rstd + row) = rstd;
+}
+
+// Rows longer than the registers of a workgroup hold: the row is read three
+// times (sum, squared deviations, output), one element at a time.
+template <class T>
+__global__ __launch_bounds__(1024) void k_ln_fwd_long(const LnArgs g) {
+  __shared__ float sm[2][16][2];
+  const int64_t row = blockIdx.x;
+  const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
+  T *y = static_cast<T *>(g.y) + row * g.ld_y;
+  float s = 0.0f, q = 0.0f, e = 0.0f, unused = 0.0f;
+  for (int64_t c = threadIdx.x; c < g.N; c += 1024) s += to_f32(*mx::gptr(x + c));
+  row_sum2<0>(s, unused, sm[0]);
+  const float m = s / (float)g.N;
+  for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+    const float d = to_f32(*mx::gptr(x + c)) - m;
+    e += d;
+    q = fmaf(d, d, q);
+  }
+  row_sum2<0>(q, e, sm[1]);
+  const float rstd = ln_rstd(m, q, e, g);
+  for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+    float w, b;
+    load_param<1>(g.w, g.w_f32, (int32_t)c, 1.0f, &w);
+    load_param<1>(g.b, g.w_f32, (int32_t)c, 0.0f, &b);
+    *mx::gptr(y + c) = from_f32<T>(fmaf((to_f32(*mx::gptr(x + c)) - m - e) * rstd, w, b));
+  }
+  if (threadIdx.x == 0 && g.mean) *mx::gptr(g.mean + row) = m + e;
+  if (threadIdx.x == 0 && g.rstd) *mx::gptr(g.rstd + row) = rstd;
+}
+
+// Backward.  Workgroup b walks rows b, b + gridDim.x, ... (TPR == 0) or the
+// same for groups of 256 / TPR rows; every thread keeps its columns' sums of
+// dy xh and dy over all of them.  With TPR > 0 the row slots of a workgroup
+// are joined in LDS (dynamic: slots * 2 * N floats) before the partial row is
+// written.
+template <class T, int VEC, int TPR, int CH>
+__global__ __launch_bounds__(TPR != 0 ? 256 : CH * VEC > 16 ? 512 : 1024) void k_ln_bwd(const LnArgs g) {
+  __shared__ float sm[2][16][2];
+  extern __shared__ float joined[];
+  constexpr int kTpr = TPR == 0 ? 1 : TPR;
+  constexpr int kSlots = TPR == 0 ? 1 : 256 / kTpr;
+  const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
+  const int t = TPR == 0 ? (int)threadIdx.x : (int)threadIdx.x % kTpr;
+  const int slot = TPR == 0 ? 0 : (int)threadIdx.x / kTpr;
+  const float inv_n = 1.0f / (float)g.N;
+  float w[CH][VEC], aw[CH][VEC], ab[CH][VEC];
+#pragma unroll
+  for (int i = 0; i < CH; i++) {
+    const int32_t col = (i * tpr + t) * VEC;
+    if (col < g.N) load_param<VEC>(g.w, g.w_f32, col, 1.0f, w[i]);
+#pragma unroll
+    for (int j = 0; j < VEC; j++) {
+      if (col >= g.N) w[i][j] = 0.0f;
+      aw[i][j] = ab[i][j] = 0.0f;
+    }
+  }
+  int phase = 0;
+  for (int64_t row = (int64_t)blockIdx.x * kSlots + slot; row < g.M; row += (int64_t)gridDim.x * kSlots) {
+    const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
+    const T *dy = static_cast<const T *>(g.dy) + row * g.ld_dy;
+    T *dx = static_cast<T *>(g.y) + row * g.ld_y;
+    const float mean = *mx::gptr(g.mean + row), rstd = *mx::gptr(g.rstd + row);
+    float xh[CH][VEC], d[CH][VEC];
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      const int32_t col = (i * tpr + t) * VEC;
+      if (col < g.N) {
+        load_chunk<T, VEC>(x + col, xh[i]);
+        load_chunk<T, VEC>(dy + col, d[i]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) xh[i][j] = mean, d[i][j] = 0.0f;
+      }
+    }
+    float s1 = 0.0f, s2 = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; i++)
+#pragma unroll
+      for (int j = 0; j < VEC; j++) {
+        const float h = (xh[i][j] - mean) * rstd;
+        xh[i][j] = h;
+        aw[i][j] = fmaf(d[i][j], h, aw[i][j]);
+        ab[i][j] += d[i][j];
+        const float gd = d[i][j] * w[i][j];
+        d[i][j] = gd;
+        s1 += gd;
+        s2 = fmaf(gd, h, s2);
+      }
+    row_sum2<TPR>(s1, s2, sm[phase]);  // the other buffer next row: one barrier a row is enough
+    phase ^= 1;
+    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      const int32_t col = (i * tpr + t) * VEC;
+      if (col < g.N) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) d[i][j] = (d[i][j] - fmaf(xh[i][j], c2, c1)) * rstd;
+        store_chunk<T, VEC>(dx + col, d[i]);
+      }
+    }
+  }
+  if (!g.part) return;
+  float *part = g.part + (int64_t)blockIdx.x * 2 * g.N;
+  if constexpr (TPR == 0) {
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      const int32_t col = (i * tpr + t) * VEC;
+      if (col < g.N) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+          *mx::gptr(part + col + j) = aw[i][j];
+          *mx::gptr(part + g.N + col + j) = ab[i][j];
+        }
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < CH; i++) {
+      const int32_t col = (i * tpr + t) * VEC;
+      if (col < g.N) {
+#pragma unroll
+        for (int j = 0; j < VEC; j++) {
+          joined[(slot * 2) * g.N + col + j] = aw[i][j];
+          joined[(slot * 2 + 1) * g.N + col + j] = ab[i][j];
+        }
+      }
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < 2 * g.N; c += 256) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < kSlots; k++) s += joined[k * 2 * g.N + c];
+      *mx::gptr(part + c) = s;
+    }
+  }
+}
+
+// Rows longer than the registers hold: two passes over the row, and the
+// workgroup's partial sums kept in its own row of `part` (each thread adds to
+// its own columns only).
+template <class T>
+__global__ __launch_bounds__(1024) void k_ln_bwd_long(const LnArgs g) {
+  __shared__ float sm[2][16][2];
+  float *part = g.part ? g.part + (int64_t)blockIdx.x * 2 * g.N : nullptr;
+  const float inv_n = 1.0f / (float)g.N;
+  int phase = 0;
+  for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x) {
+    const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
+    const T *dy = static_cast<const T *>(g.dy) + row * g.ld_dy;
+    T *dx = static_cast<T *>(g.y) + row * g.ld_y;
+    const float mean = *mx::gptr(g.mean + row), rstd = *mx::gptr(g.rstd + row);
+    float s1 = 0.0f, s2 = 0.0f;
+    for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+      float w;
+      load_param<1>(g.w, g.w_f32, (int32_t)c, 1.0f, &w);
+      const float d = to_f32(*mx::gptr(dy + c)), h = (to_f32(*mx::gptr(x + c)) - mean) * rstd;
+      s1 += d * w;
+      s2 = fmaf(d * w, h, s2);
+      if (part) {
+        const bool first = row == (int64_t)blockIdx.x;
+        *mx::gptr(part + c) = fmaf(d, h, first ? 0.0f : *mx::gptr(part + c));
+        *mx::gptr(part + g.N + c) = d + (first ? 0.0f : *mx::gptr(part + g.N + c));
+      }
+    }
+    row_sum2<0>(s1, s2, sm[phase]);
+    phase ^= 1;
+    const float c1 = s1 * inv_n, c2 = s2 * inv_n;
+    for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+      float w;
+      load_param<1>(g.w, g.w_f32, (int32_t)c, 1.0f, &w);
+      const float d = to_f32(*mx::gptr(dy + c)), h = (to_f32(*mx::gptr(x + c)) - mean) * rstd;
+      *mx::gptr(dx + c) = from_f32<T>((d * w - fmaf(h, c2, c1)) * rstd);
+    }
+  }
+}
+
+// dw and db: the sums of `parts` partial rows, in row order within each of 32
+// slices and then over the slices.  A workgroup takes 32 columns of the 2 N
+// (dw's, then db's); no rows give zeros.
+__global__ __launch_bounds__(1024) void k_ln_join(const float *part, int parts, int32_t N, float *dw, float *db) {
+  __shared__ float sm[32][33];
+  const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
+  const int64_t col = (int64_t)blockIdx.x * 32 + c;
+  float a = 0.0f;
+  if (col < 2 * (int64_t)N)
+#pragma unroll 4
+    for (int p = s; p < parts; p += 32) a += *mx::gptr(part + (int64_t)p * 2 * N + col);
+  sm[s][c] = a;
+  __syncthreads();
+  if (s == 0 && col < 2 * (int64_t)N) {
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; k++) t += sm[k][c];
+    if (col < N) {
+      if (dw) *mx::gptr(dw + col) = t;
+    } else {
+      if (db) *mx::gptr(db + col - N) = t;
+    }
+  }
+}
+
+}  // namespace mxt

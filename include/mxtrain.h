@@ -83,6 +83,42 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
                                       float *dweight, float *dbias,
                                       void *workspace, int64_t workspace_bytes, void *stream);
 
+/*
+ * The experts' products in bf16: the high-precision form of mxfp8.h's grouped
+ * products, over the same ragged token groups.  group_ends is a DEVICE int32
+ * array of G cumulative end rows, read on the GPU only: group g is rows
+ * [end_{g-1}, end_g), with end_g = min(max(group_ends[g], end_{g-1}, 0), M),
+ * so that any values give ranges inside the matrices.  Groups may have any
+ * number of rows, none among them.
+ *
+ *   mxtrain_grouped_gemm:    C_g = A_g B_g^T (forward, transpose_b = 1) or
+ *                            C_g = A_g B_g (input gradient, transpose_b = 0)
+ *   a : bf16 [M, K], row stride lda
+ *   b : bf16, expert g at b + g * stride_b: [N, K] (transpose_b = 1) or [K, N]
+ *       (transpose_b = 0), row stride ldb
+ *   c : c_dtype (MXTRAIN_BF16 or MXTRAIN_F32) [M, N], row stride ldc; rows
+ *       past the last group's end are not written.
+ *
+ *   mxtrain_grouped_gemm_k:  C_g = A_g^T B_g (weight gradient)
+ *   a : bf16 [T, M], b : bf16 [T, N] (tokens along the rows; M above is T
+ *       here), row strides lda, ldb
+ *   c : c_dtype, C_g [M, N] at c + g * stride_c; an empty group gives zeros.
+ *
+ * Sums are fp32, rounded once into C.  Any dimensions; a and b 16-byte
+ * aligned, lda, ldb and stride_b multiples of 8 (16 bytes) and below 2^22
+ * (lda, ldb); c aligned to its element.  Elements between a row's end and the
+ * next multiple of 8 may be read (never used), nothing else outside the
+ * matrices.  0 <= G <= 65535; G == 0, or an empty C, returns MXTRAIN_OK and
+ * enqueues nothing.
+ */
+mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t stride_b,
+                                    int transpose_b, const int32_t *group_ends, int64_t G,
+                                    int64_t M, int64_t N, int64_t K,
+                                    void *c, int64_t ldc, int c_dtype, void *stream);
+mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b, int64_t ldb,
+                                      const int32_t *group_ends, int64_t G, int64_t M, int64_t N, int64_t T,
+                                      void *c, int64_t ldc, int64_t stride_c, int c_dtype, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *mxtrain_status_str(mxtrain_status status);
 

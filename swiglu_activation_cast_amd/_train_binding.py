@@ -33,6 +33,8 @@ _SIGNATURES = {
     "mxtrain_layer_norm_bwd_workspace": (_i64, [_i64, _i64]),
     "mxtrain_layer_norm_bwd": (_int, [_p, _i64, _p, _i64, _p, _p, _p, _int, _i64, _i64, _int, _p, _i64, _p, _p, _p,
                                       _i64, _p]),
+    "mxtrain_grouped_gemm": (_int, [_p, _i64, _p, _i64, _i64, _int, _p, _i64, _i64, _i64, _i64, _p, _i64, _int, _p]),
+    "mxtrain_grouped_gemm_k": (_int, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _i64, _i64, _int, _p]),
     "mxtrain_status_str": (ctypes.c_char_p, [_int]),
 }
 
@@ -199,3 +201,63 @@ def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
           _param(dw, "dweight", N, dev), _param(db, "dbias", N, dev), ws.data_ptr(),
           ws.numel() * ws.element_size(), _stream_of(dev, stream))
     return dx, dw, db
+
+
+def _ends(t: torch.Tensor, device) -> Tuple[int, int]:
+    _gpu(t, "group_ends", (torch.int32,), 1, device)
+    if t.shape[0] > 1 and t.stride(0) != 1:
+        raise ValueError("group_ends must be contiguous")
+    return t.data_ptr(), t.shape[0]
+
+
+def _out_dtype(out: Optional[torch.Tensor], out_dtype: torch.dtype) -> torch.dtype:
+    dtype = out.dtype if out is not None else out_dtype
+    if dtype not in _TYPES:
+        raise TypeError(f"results are bfloat16 or float32, not {dtype}")
+    return dtype
+
+
+def mxtrain_grouped_gemm(a: torch.Tensor, b: torch.Tensor, group_ends: torch.Tensor, *, transpose_b: bool = True,
+                         out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                         stream=None) -> torch.Tensor:
+    """The experts' products in bf16: row i of a [M, K], in group g, times b[g].
+
+    transpose_b True: b [G, N, K], a_g b_g^T (forward); False: b [G, K, N],
+    a_g b_g (input gradient).  group_ends: device int32 [G], cumulative row
+    ends of any group sizes, read on the GPU only.  Returns [M, N] in `out`'s
+    dtype or `out_dtype` (bf16 or fp32); rows past the last end are left as
+    they are in `out` (uninitialized when `out` is None)."""
+    _gpu(a, "a", (torch.bfloat16,), 2)
+    dev = a.device
+    _gpu(b, "b", (torch.bfloat16,), 3, dev)
+    pe, G = _ends(group_ends, dev)
+    M, K = a.shape
+    N, kb = (b.shape[1], b.shape[2]) if transpose_b else (b.shape[2], b.shape[1])
+    if b.shape[0] != G or kb != K:
+        raise ValueError(f"b must be [{G}, N, {K}] (transpose_b) or [{G}, {K}, N], got {tuple(b.shape)}")
+    c = _out(out, "out", (M, N), _out_dtype(out, out_dtype), dev)
+    ldb = _ld(b, "b")
+    _call("mxtrain_grouped_gemm", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), ldb,
+          b.stride(0) if G > 1 else 0, int(transpose_b), pe, G, M, N, K, c.data_ptr(), _ld(c, "out"),
+          _TYPES[c.dtype], _stream_of(dev, stream))
+    return c
+
+
+def mxtrain_grouped_gemm_k(a: torch.Tensor, b: torch.Tensor, group_ends: torch.Tensor, *,
+                           out_dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """The experts' weight gradients: a_g^T b_g [G, M, N] over each group's
+    tokens, a [T, M] and b [T, N] in bf16; an empty group gives zeros."""
+    _gpu(a, "a", (torch.bfloat16,), 2)
+    dev = a.device
+    _gpu(b, "b", (torch.bfloat16,), 2, dev)
+    pe, G = _ends(group_ends, dev)
+    T, M = a.shape
+    N = b.shape[1]
+    if b.shape[0] != T:
+        raise ValueError("a [T, M] and b [T, N] must have the same tokens")
+    c = _out(out, "out", (G, M, N), _out_dtype(out, out_dtype), dev)
+    ldc = _ld(c, "out")
+    _call("mxtrain_grouped_gemm_k", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), _ld(b, "b"), pe, G, M, N, T,
+          c.data_ptr(), ldc, c.stride(0) if G > 1 else max(ldc * M, 1), _TYPES[c.dtype], _stream_of(dev, stream))
+    return c

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "mxtrain.h"
+#include "tr_gemm.hpp"
 #include "tr_norm.hpp"
 
 namespace {
@@ -124,6 +125,50 @@ bool ln_vec(const void *const *mats, const int64_t *lds, int n, int64_t N, int d
   return true;
 }
 
+// -------------------------------------------------- the experts' products
+constexpr int64_t kMaxGroups = 65535;
+
+// Compute units of the current device (it decides tile sizes, no result
+// depends on it).
+int cu_count() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1)
+    return 256;
+  return cus;
+}
+
+struct GroupKernel {
+  const void *k;
+  int bm, bn;
+};
+
+template <int MODE, int AL, int BL, int WI, int WJ, int RING>
+GroupKernel group_kernel(bool f32) {
+  return {f32 ? (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, RING, true>
+              : (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, RING, false>,
+          64 * WI, 64 * WJ};
+}
+
+// 256 x 256 tiles, or 128 x 128 where those would not give every CU one.
+template <int MODE, int AL, int BL>
+GroupKernel group_pick(int64_t rows, int64_t N, int64_t copies, bool f32) {
+  const int64_t big = (rows + 255) / 256 * ((N + 255) / 256) * copies;
+  if (big >= cu_count()) return group_kernel<MODE, AL, BL, 4, 4, 2>(f32);
+  return group_kernel<MODE, AL, BL, 2, 2, 2>(f32);
+}
+
+mxtrain_status operand_check(const void *p, int64_t ld, int64_t rows, int64_t cols) {
+  if (ld < cols || ld % 8 != 0) return MXTRAIN_ERR_STRIDE;
+  if (!aligned(p, 16)) return MXTRAIN_ERR_ALIGN;
+  if (ld >= mxt::kMaxLd || !extent_ok(rows, cols, ld)) return MXTRAIN_ERR_OVERFLOW;
+  return MXTRAIN_OK;
+}
+
+bool vec_c_ok(const void *c, int64_t ldc, int64_t stride_c, int type) {
+  return aligned(c, (uintptr_t)(4 * size_of(type))) && ldc % 4 == 0 && stride_c % 4 == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -215,6 +260,93 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
   const hipError_t err = hipLaunchKernel((const void *)&mxt::k_ln_join, dim3((unsigned)blocks), dim3(1024), kargs, 0,
                                          (hipStream_t)stream);
   return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;
+}
+
+mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, int64_t ldb, int64_t stride_b,
+                                    int transpose_b, const int32_t *group_ends, int64_t G, int64_t M, int64_t N,
+                                    int64_t K, void *c, int64_t ldc, int c_dtype, void *stream) {
+  if (!type_ok(c_dtype)) return MXTRAIN_ERR_TYPE;
+  if (transpose_b != 0 && transpose_b != 1) return MXTRAIN_ERR_VALUE;
+  if (G < 0 || G > kMaxGroups || M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+    return MXTRAIN_ERR_SHAPE;
+  if (G == 0 || M == 0 || N == 0) return MXTRAIN_OK;
+  if (!group_ends || !c || (K > 0 && (!a || !b))) return MXTRAIN_ERR_NULL;
+  const int64_t b_rows = transpose_b ? N : K, b_cols = transpose_b ? K : N;
+  mxtrain_status st = operand_check(a, lda, M, K);
+  if (st == MXTRAIN_OK) st = operand_check(b, ldb, b_rows, b_cols);
+  if (st != MXTRAIN_OK) return st;
+  int64_t all;
+  if (stride_b < 0 || stride_b % 8 != 0 || ldc < N) return MXTRAIN_ERR_STRIDE;
+  if (G > 1 && b_rows > 0 && stride_b < (b_rows - 1) * ldb + b_cols) return MXTRAIN_ERR_STRIDE;
+  if (!aligned(group_ends, 4) || !aligned(c, (uintptr_t)size_of(c_dtype))) return MXTRAIN_ERR_ALIGN;
+  if (!extent_ok(M, N, ldc) || __builtin_mul_overflow(stride_b, G, &all) || all > (INT64_MAX >> 4))
+    return MXTRAIN_ERR_OVERFLOW;
+  const bool f32 = c_dtype == MXTRAIN_F32;
+  const GroupKernel k = transpose_b ? group_pick<mxt::kGroupM, mxt::kKC, mxt::kKC>(M, N, 1, f32)
+                                    : group_pick<mxt::kGroupM, mxt::kKC, mxt::kMC>(M, N, 1, f32);
+  // an upper bound of tile rows, each group adding at most one partial one:
+  // the host never reads the ends
+  const int64_t tiles_m = (M + k.bm - 1) / k.bm + G, tiles_n = (N + k.bn - 1) / k.bn;
+  int64_t blocks;
+  if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks)) return MXTRAIN_ERR_OVERFLOW;
+  mxt::GemmArgs g{};
+  g.a = static_cast<const uint16_t *>(a);
+  g.b = static_cast<const uint16_t *>(b);
+  g.lda = lda;
+  g.ldb = ldb;
+  g.stride_b = stride_b;
+  g.M = M;
+  g.N = N;
+  g.K = K;
+  g.c = c;
+  g.ldc = ldc;
+  g.ends = group_ends;
+  g.G = (int32_t)G;
+  g.tiles_m = (int32_t)tiles_m;
+  g.tiles_n = (int32_t)tiles_n;
+  g.vec_c = vec_c_ok(c, ldc, 0, c_dtype);
+  return launch(k.k, blocks, mxt::kThreads, g, stream);
+}
+
+mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b, int64_t ldb,
+                                      const int32_t *group_ends, int64_t G, int64_t M, int64_t N, int64_t T, void *c,
+                                      int64_t ldc, int64_t stride_c, int c_dtype, void *stream) {
+  if (!type_ok(c_dtype)) return MXTRAIN_ERR_TYPE;
+  if (G < 0 || G > kMaxGroups || M < 0 || N < 0 || T < 0 || M > INT32_MAX || N > INT32_MAX || T > INT32_MAX)
+    return MXTRAIN_ERR_SHAPE;
+  if (G == 0 || M == 0 || N == 0) return MXTRAIN_OK;
+  if (!group_ends || !c || (T > 0 && (!a || !b))) return MXTRAIN_ERR_NULL;
+  mxtrain_status st = operand_check(a, lda, T, M);
+  if (st == MXTRAIN_OK) st = operand_check(b, ldb, T, N);
+  if (st != MXTRAIN_OK) return st;
+  int64_t all;
+  if (ldc < N || stride_c < 0) return MXTRAIN_ERR_STRIDE;
+  if (!aligned(group_ends, 4) || !aligned(c, (uintptr_t)size_of(c_dtype))) return MXTRAIN_ERR_ALIGN;
+  if (!extent_ok(M, N, ldc) || __builtin_mul_overflow(stride_c, G, &all) || all > (INT64_MAX >> 4))
+    return MXTRAIN_ERR_OVERFLOW;
+  if (G > 1 && stride_c < (M - 1) * ldc + N) return MXTRAIN_ERR_STRIDE;
+  const GroupKernel k = group_pick<mxt::kGroupK, mxt::kMC, mxt::kMC>(M, N, G, c_dtype == MXTRAIN_F32);
+  const int64_t tiles_m = (M + k.bm - 1) / k.bm, tiles_n = (N + k.bn - 1) / k.bn;
+  int64_t blocks;
+  if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks) || __builtin_mul_overflow(blocks, G, &blocks))
+    return MXTRAIN_ERR_OVERFLOW;
+  mxt::GemmArgs g{};
+  g.a = static_cast<const uint16_t *>(a);
+  g.b = static_cast<const uint16_t *>(b);
+  g.lda = lda;
+  g.ldb = ldb;
+  g.M = M;
+  g.N = N;
+  g.K = T;
+  g.c = c;
+  g.ldc = ldc;
+  g.stride_c = stride_c;
+  g.ends = group_ends;
+  g.G = (int32_t)G;
+  g.tiles_m = (int32_t)tiles_m;
+  g.tiles_n = (int32_t)tiles_n;
+  g.vec_c = vec_c_ok(c, ldc, stride_c, c_dtype);
+  return launch(k.k, blocks, mxt::kThreads, g, stream);
 }
 
 const char *mxtrain_status_str(mxtrain_status status) {

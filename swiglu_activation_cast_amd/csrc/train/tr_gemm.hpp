@@ -1,0 +1,534 @@
+// tr_gemm.hpp -- products of 16-bit matrices with fp32 sums on gfx950's matrix
+// cores (v_mfma_f32_32x32x16_bf16 / _f16): the experts' products over ragged
+// groups and the products of the Newton-Schulz steps.
+//
+//   C[m][n] = sum over k of A(m, k) B(n, k)
+//
+// Each operand is stored either with K adjacent (kKC: row m or n holds its
+// K elements) or with its own index adjacent (kMC: row k holds the operand's
+// M or N elements), so that the forward product (both kKC), the input
+// gradient (B kMC) and the weight gradient (both kMC) read the tensors as they
+// are, without a transposed copy.
+//
+// Structure: a 64 WI x 64 WJ tile of C per workgroup of four wavefronts
+// (2 x 2, each 32 WI x 32 WJ, its sums in accumulation registers).  K is staged
+// kBK elements at a time in a ring of LDS slots that direct global -> LDS
+// loads fill ahead of use.  A stage is consumed in steps of 16 (one MFMA
+// deep): while a step's MFMAs run from registers, the next step's operands are
+// read from LDS into the other register set, and the loads of a later stage
+// are issued, one of each between two MFMAs.  The barrier of a stage sits
+// before its last step's MFMAs, whose operands are then already in registers:
+// from there the stage's slot is free to be filled again, and the MFMAs that
+// follow cover the wait.
+//
+// LDS layouts.  kKC: rows of kBK elements (128 bytes), 16-byte chunks at
+// position chunk ^ (row / 2) % 8, so that the 16 rows that a quarter of a
+// wavefront reads at one chunk hit all banks once.  kMC: rows of the tile's
+// 64 W columns, one per k; they are read with ds_read_b64_tr_b16, which
+// hands lane i of 16 the i-th of 16 columns of four k rows (lane group of
+// four = row; checked on gfx950); the chunk position is XORed with a function
+// of k that spreads the four rows over the banks.
+//
+// MFMA operand and result layout (32x32x16): lane l holds k 8 (l / 32) .. + 7
+// of row l % 32; result register v of lane l is row 8 (v / 4) + 4 (l / 32) +
+// v % 4 of the first operand, column l % 32 the second's row.  B is passed
+// first, so that a lane holds four adjacent columns of one row of C.
+#pragma once
+#include <type_traits>
+
+#include "tr_common.hpp"
+
+namespace mxt {
+
+using mx::u32x4_t;
+
+enum Layout { kKC = 0, kMC = 1 };
+enum Mode { kBatch = 0, kGroupM = 1, kGroupK = 2 };
+enum Elem { kBf16 = 0, kF16 = 1 };
+
+constexpr int kThreads = 256;
+constexpr int kBK = 64;                   // elements of K per stage
+constexpr int kKS = kBK / 16;             // MFMA steps per stage
+constexpr int kTileRows = 4;              // tile rows per band of the tile order
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows of this many elements stay below 2^31 bytes
+
+struct GemmArgs {
+  const uint16_t *a, *b;
+  int64_t lda, ldb;
+  int64_t stride_a, stride_b;  // per batch entry; stride_b per expert in kGroupM
+  int64_t M, N, K;             // M: all rows in kGroupM; K: all of it in kGroupK
+  void *c;
+  int64_t ldc, stride_c;       // stride_c per batch entry or group
+  const int32_t *ends;         // cumulative group ends (device), G of them
+  int32_t G;                   // groups, or batch entries
+  int32_t tiles_m, tiles_n;    // tiles_m: an upper bound in kGroupM
+  int32_t vec_c;               // four adjacent results of C may be stored at once
+};
+
+typedef float v16f_t __attribute__((ext_vector_type(16)));
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+#define MXT_LDS __attribute__((address_space(3)))
+
+// 16 bytes a lane, global -> LDS: lane l's land at LDS byte `lds` + 16 l.
+// Asm, so that the compiler does not wait for it before LDS reads of other
+// slots; wait_vm awaits it.  M0 holds the LDS base (one wait state between its
+// write and the load) and is put back.
+__device__ __forceinline__ void dma16(const void *base, u32 off, u32 lds) {
+  u32 saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "global_load_lds_dwordx4 %2, %3\n\t"
+      "s_nop 0\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(lds), "v"(off), "s"(base));
+}
+// A value that every lane holds alike, in a scalar register.
+template <class P>
+__device__ __forceinline__ P *uniform(P *p) {
+  const uint64_t v = (uint64_t)(uintptr_t)p;
+  return (P *)(uintptr_t)(((uint64_t)(u32)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+                          (u32)__builtin_amdgcn_readfirstlane((int)(u32)v));
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ u32 lds_addr(const void *p) { return (u32)(uintptr_t)(const MXT_LDS void *)p; }
+
+template <int EL>
+__device__ __forceinline__ v16f_t mfma(u32x4_t first, u32x4_t second, v16f_t c) {
+  typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+  typedef _Float16 h8 __attribute__((ext_vector_type(8)));
+  if constexpr (EL == kBf16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, first), __builtin_bit_cast(b8, second), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, first), __builtin_bit_cast(h8, second), c, 0, 0, 0);
+}
+
+// One operand of a tile: W 64-row halves (64 W rows of the operand, or
+// columns where it is stored kMC).  `rows` of them exist (>= 1); the others
+// are read as the last one and never stored.  A wavefront fills kLoads
+// kilobytes of each stage.
+template <int L, int W>
+struct Operand {
+  static constexpr int kRows = 64 * W;
+  static constexpr int kBytes = kRows * kBK * 2;  // of a stage
+  static constexpr int kLoads = kBytes / 1024 / 4;
+  static constexpr int kRowB = L == kKC ? kBK * 2 : kRows * 2;  // bytes of an LDS row
+  static constexpr int kPer = 1024 / kRowB;                     // LDS rows per load
+  static constexpr int kLanes = 64 / kPer;                      // lanes (chunks) per LDS row
+
+  const uint8_t *base;  // of the tile's first k (uniform)
+  int64_t step;         // bytes from a stage to the next (uniform)
+  u32 off[kLoads];      // this lane's byte offset in each load
+  u32 tail[kLoads];     // kMC: the same at the stage's first k row
+  int k_of[kLoads];     // first k (within the stage) of what the lane loads
+  u32 lds_w;            // LDS byte (within a stage's operand) of this wavefront's first load
+  u32 rd[L == kKC ? kKS : W];  // this lane's LDS read offsets
+
+  // XOR of the chunk position in LDS row r.
+  static __device__ __forceinline__ u32 key(u32 r) {
+    if constexpr (L == kKC) return (r >> 1) & 7u;
+    else if constexpr (W == 1) return ((r >> 1) & 1u) << 2;  // 128-byte rows: two rows per turn of the banks
+    else return (r & 3u) << 2;
+  }
+
+  // `blk0` + x * `blk_step` is the x-th 32-row block of this wavefront.
+  __device__ __forceinline__ void init(const uint16_t *p, int64_t ld, u32 rows, int wave, int lane, int blk0,
+                                       int blk_step) {
+    base = uniform(reinterpret_cast<const uint8_t *>(p));
+    step = L == kKC ? (int64_t)kBK * 2 : (int64_t)kBK * ld * 2;
+    lds_w = (u32)(wave * kLoads) * 1024u;
+#pragma unroll
+    for (int q = 0; q < kLoads; q++) {
+      const u32 r = (u32)((wave * kLoads + q) * kPer) + (u32)lane / kLanes;  // LDS row
+      const u32 c = ((u32)lane % kLanes) ^ key(r);                          // chunk of that row
+      if constexpr (L == kKC) {
+        off[q] = min(r, rows - 1) * (u32)(ld * 2) + c * 16u;
+        tail[q] = min(r, rows - 1) * (u32)(ld * 2);
+        k_of[q] = (int)c * 8;
+      } else {
+        const u32 cc = min(c, (rows - 1) / 8u) * 16u;
+        off[q] = r * (u32)(ld * 2) + cc;
+        tail[q] = cc;
+        k_of[q] = (int)r;
+      }
+    }
+    const u32 h = (u32)lane >> 5;
+    if constexpr (L == kKC) {
+      const u32 r = (u32)lane & 31u;
+#pragma unroll
+      for (int s = 0; s < kKS; s++) rd[s] = ((u32)blk0 * 32u + r) * kRowB + ((((u32)(2 * s) + h) ^ key(r)) << 4);
+    } else {
+      const u32 i = (u32)lane & 15u, c16 = ((u32)lane >> 4) & 1u;
+      const u32 k = 8u * h + (i >> 2);  // of a step; key(k) is the same for every step and half
+#pragma unroll
+      for (int x = 0; x < W; x++) {
+        const u32 chunk = (u32)(blk0 + x * blk_step) * 4u + 2u * c16 + ((i & 3u) >> 1);
+        rd[x] = k * kRowB + ((chunk ^ key(k)) << 4) + (i & 1u) * 8u;
+      }
+    }
+  }
+  // Loads q of the stage at `src`, kmax of whose k exist: chunks (rows) at or
+  // past it are read at the stage's first k instead and cleared afterwards.
+  __device__ __forceinline__ void load(int q, const uint8_t *src, int kmax, u32 slot) const {
+    dma16(src, k_of[q] < kmax ? off[q] : tail[q], slot + lds_w + (u32)q * 1024u);
+  }
+  // This lane's part of a landed stage, k >= kmax -> 0.
+  __device__ __forceinline__ void clear(MXT_LDS uint8_t *slot, int lane, int kmax) const {
+#pragma unroll
+    for (int q = 0; q < kLoads; q++) {
+      MXT_LDS u32x4_t *p = (MXT_LDS u32x4_t *)(slot + lds_w + (u32)q * 1024u + 16u * (u32)lane);
+      if constexpr (L == kMC) {
+        if (k_of[q] >= kmax) *p = u32x4_t{0, 0, 0, 0};
+      } else if (k_of[q] + 8 > kmax) {
+        const int keep = kmax - k_of[q];  // elements of the chunk that exist
+        u32x4_t v = *p;
+#pragma unroll
+        for (int d = 0; d < 4; d++) v[d] &= keep >= 2 * d + 2 ? 0xffffffffu : keep == 2 * d + 1 ? 0xffffu : 0u;
+        *p = v;
+      }
+    }
+  }
+  static constexpr int kReads = L == kKC ? W : 2 * W;  // LDS reads of a step
+  // Read number t of step s into the fragments.
+  __device__ __forceinline__ void read(const MXT_LDS uint8_t *slot, int s, int t, int blk_step, u32x4_t *f) const {
+    if constexpr (L == kKC) {
+      f[t] = *(const MXT_LDS u32x4_t *)(slot + rd[s] + (u32)(t * blk_step) * 32u * kRowB);
+    } else {
+      const int x = t / 2, j = t % 2;
+      typedef u32 u32x2_t __attribute__((ext_vector_type(2)));
+      const u32x2_t v = __builtin_bit_cast(
+          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXT_LDS s16x4_t *)(slot + rd[x] + (u32)(16 * s + 4 * j) * kRowB)));
+      f[x][2 * j] = v[0];
+      f[x][2 * j + 1] = v[1];
+    }
+  }
+};
+
+// What a tile's workgroup computes: rows [m0, m0 + rows) x columns [n0, n0 +
+// cols) of matrix `entry`, over `k_len` of K from the operands' bases.  With
+// SPLIT, A and B each come as a high and a low plane and the sum runs over
+// high x low, low x high and high x high.
+struct Tile {
+  const uint16_t *a, *b;        // at the tile's first row (column) and k
+  const uint16_t *a_lo, *b_lo;  // SPLIT
+  int64_t k_len;
+  u32 rows, cols;
+};
+
+template <int EL, int AL, int BL, int WI, int WJ, int RING, bool SPLIT, class Emit>
+__device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint8_t *smem, const Emit &emit) {
+  using A = Operand<AL, WI>;
+  using B = Operand<BL, WJ>;
+  constexpr int kSlot = A::kBytes + B::kBytes;
+  constexpr int kLoads = A::kLoads + B::kLoads;
+  constexpr int kMfmas = WI * WJ;
+  constexpr int kReads = A::kReads + B::kReads;
+  const int lane = threadIdx.x & 63;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = w >> 1, wn = w & 1;
+  // 32-row blocks of C: A's alternate between the two wavefront rows (a short
+  // tile has rows in both), B's are adjacent
+  A oa;
+  B ob;
+  oa.init(t.a, g.lda, t.rows, w, lane, wm, 2);
+  ob.init(t.b, g.ldb, t.cols, w, lane, WJ * wn, 1);
+
+  v16f_t acc[WI][WJ];
+#pragma unroll
+  for (int i = 0; i < WI; i++)
+#pragma unroll
+    for (int j = 0; j < WJ; j++) acc[i][j] = v16f_t{};
+
+  const int per = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));  // stages of one pass over K
+  const int n_stage = SPLIT ? 3 * per : per;
+  const int k_tail = (int)(t.k_len - (int64_t)(per - 1) * kBK);  // k in the last stage of a pass, 1 .. kBK
+  MXT_LDS uint8_t *lds = (MXT_LDS uint8_t *)smem;
+  const u32 lds0 = lds_addr(smem);
+
+  const uint8_t *a_lo = nullptr, *b_lo = nullptr;
+  if constexpr (SPLIT) {
+    a_lo = uniform(reinterpret_cast<const uint8_t *>(t.a_lo));
+    b_lo = uniform(reinterpret_cast<const uint8_t *>(t.b_lo));
+  }
+  struct Src {
+    const uint8_t *a, *b;
+    int kmax;
+    u32 slot;
+  };
+  // Stages past the last re-read it into a slot that is not read again.
+  auto source = [&](int st) {
+    int s = min(st, n_stage - 1), pass = 0;
+    if constexpr (SPLIT) {
+      pass = s / per;
+      s -= pass * per;
+    }
+    Src r;
+    r.a = (SPLIT && pass == 1 ? a_lo : oa.base) + s * oa.step;
+    r.b = (SPLIT && pass == 0 ? b_lo : ob.base) + s * ob.step;
+    r.kmax = s == per - 1 ? k_tail : kBK;
+    r.slot = lds0 + (u32)(st % RING) * kSlot;
+    return r;
+  };
+  auto load = [&](int q, const Src &r) {
+    if (q < A::kLoads) oa.load(q < A::kLoads ? q : 0, r.a, r.kmax, r.slot);
+    else ob.load(q < A::kLoads ? 0 : q - A::kLoads, r.b, r.kmax, r.slot + A::kBytes);
+  };
+  // Stage st has landed: clear what lies past K (each lane what it loaded).
+  auto clear = [&](int st) {
+    if (k_tail == kBK || st >= n_stage || (SPLIT ? (st + 1) % per : st + 1 - per) != 0) return;
+    MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
+    oa.clear(slot, lane, k_tail);
+    ob.clear(slot + A::kBytes, lane, k_tail);
+  };
+
+  struct Frags {
+    u32x4_t a[WI], b[WJ];
+  };
+  // LDS read number n of step s of the stage in `slot`: A's first block, B's
+  // blocks, A's others, in the order in which the MFMAs need them.
+  auto read = [&](const MXT_LDS uint8_t *slot, int s, int n, Frags &f) {
+    constexpr int a1 = A::kReads / WI;  // reads of one A block
+    if (n < a1) oa.read(slot, s, n, 2, f.a);
+    else if (n < a1 + B::kReads) ob.read(slot + A::kBytes, s, n - a1, 1, f.b);
+    else oa.read(slot, s, n - B::kReads, 2, f.a);
+  };
+  // MFMAs of one step from `cur`, and between them the reads of step s of
+  // `slot` into `nxt` and loads [q0, q1) of `src`.
+  auto phase = [&](auto do_mfma, const MXT_LDS uint8_t *slot, int s, Frags &cur, Frags &nxt, int q0, int q1,
+                   const Src &src) {
+#pragma unroll
+    for (int k = 0; k < kMfmas; k++) {
+      const int i = k / WJ, j = k % WJ;
+      if constexpr (decltype(do_mfma)::value) acc[i][j] = mfma<EL>(cur.b[j], cur.a[i], acc[i][j]);
+      // reads as early as one per MFMA allows, loads spread evenly
+      constexpr int per_k = (kReads + kMfmas - 1) / kMfmas;
+#pragma unroll
+      for (int n = k * per_k; n < (k + 1) * per_k; n++)
+        if (n < kReads) read(slot, s, n, nxt);
+#pragma unroll
+      for (int q = 0; q < kLoads; q++)
+        if (q >= q0 + k * (q1 - q0) / kMfmas && q < q0 + (k + 1) * (q1 - q0) / kMfmas) load(q, src);
+      __builtin_amdgcn_sched_barrier(0);  // keep this order
+    }
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  // The stage's loads go out in its first two phases.
+  constexpr int kHalf = (kLoads + 1) / 2;
+
+  Frags f0, f1;  // the steps alternate between the two
+  static_assert(kKS % 2 == 0, "the last step of a stage leaves its operands in f1");
+  // Stage st: the last step of stage st - 1 (from f1), then its own steps but
+  // the last, which it leaves in f1.  At its end stage st + 1 has landed and
+  // stage st's slot is free.
+  auto stage = [&](auto has_last, int st) {
+    const MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
+    const bool first = !decltype(has_last)::value;
+    // the loads of the stage that takes over stage st - 1's slot
+    const Src src = first ? Src{} : source(st - 1 + RING);
+    phase(has_last, slot, 0, f1, f0, 0, first ? 0 : kHalf, src);
+    phase(Yes{}, slot, 1, f0, f1, first ? 0 : kHalf, first ? 0 : kLoads, src);
+#pragma unroll
+    for (int s = 2; s < kKS; s += 2) {
+      phase(Yes{}, slot, s, f1, f0, 0, 0, src);
+      phase(Yes{}, slot, s + 1, f0, f1, 0, 0, src);
+    }
+#if __HIP_DEVICE_COMPILE__
+    // keep this stage's results in its block
+#pragma unroll
+    for (int i = 0; i < WI; i++) {
+#pragma unroll
+      for (int j = 0; j < WJ; j++) asm volatile("" ::"a"(acc[i][j]));
+      asm volatile("" ::"v"(f1.a[i]));
+    }
+#pragma unroll
+    for (int j = 0; j < WJ; j++) asm volatile("" ::"v"(f1.b[j]));
+#endif
+    // issued so far: stages up to st - 1 + RING
+    wait_vm<(RING - 2) * kLoads>();
+    clear(st + 1);
+    __syncthreads();
+  };
+
+  if (n_stage > 0) {
+#pragma unroll
+    for (int st = 0; st < RING; st++) {
+      const Src src = source(st);
+#pragma unroll
+      for (int q = 0; q < kLoads; q++) load(q, src);
+    }
+    wait_vm<(RING - 1) * kLoads>();
+    clear(0);
+    __syncthreads();
+    stage(No{}, 0);
+    for (int st = 1; st < n_stage; st++) stage(Yes{}, st);
+#pragma unroll
+    for (int k = 0; k < kMfmas; k++) acc[k / WJ][k % WJ] = mfma<EL>(f1.b[k % WJ], f1.a[k / WJ], acc[k / WJ][k % WJ]);
+    wait_vm<0>();  // nothing may still be landing in LDS when the workgroup ends or goes on
+  }
+
+  // four adjacent columns of a row at a time
+  const u32 h = (u32)lane >> 5, r = (u32)lane & 31u;
+#pragma unroll
+  for (int i = 0; i < WI; i++)
+#pragma unroll
+    for (int j = 0; j < WJ; j++)
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const u32 m = 32u * (u32)(2 * i + wm) + r, n = 32u * (u32)(WJ * wn + j) + 2u * (u32)v + 4u * h;
+        if (m < t.rows && n < t.cols) emit(m, n, f32x4_t{acc[i][j][v], acc[i][j][v + 1], acc[i][j][v + 2], acc[i][j][v + 3]});
+      }
+}
+
+// ------------------------------------------------------- the experts' products
+// Results of a tile at c (row stride ldc), fp32 or rounded to bf16.
+template <bool F32>
+struct EmitC {
+  void *c;
+  int64_t ldc;
+  u32 cols;
+  bool vec;
+  __device__ __forceinline__ void operator()(u32 m, u32 n, f32x4_t v) const {
+    typedef u32 u32x2_t __attribute__((ext_vector_type(2)));
+    if constexpr (F32) {
+      float *p = static_cast<float *>(c) + (int64_t)m * ldc + n;
+      if (vec && n + 4 <= cols) {
+        __builtin_nontemporal_store(v, mx::gptr(reinterpret_cast<f32x4_t *>(p)));
+      } else {
+#pragma unroll
+        for (u32 e = 0; e < 4; e++)
+          if (n + e < cols) *mx::gptr(p + e) = v[e];
+      }
+    } else {
+      uint16_t *p = static_cast<uint16_t *>(c) + (int64_t)m * ldc + n;
+      const u32x2_t q = {mx::pack_bf16(v[0], v[1]), mx::pack_bf16(v[2], v[3])};
+      if (vec && n + 4 <= cols) {
+        __builtin_nontemporal_store(q, mx::gptr(reinterpret_cast<u32x2_t *>(p)));
+      } else {
+#pragma unroll
+        for (u32 e = 0; e < 4; e++)
+          if (n + e < cols) *mx::gptr(p + e) = (uint16_t)(q[e / 2] >> (16 * (e % 2)));
+      }
+    }
+  }
+};
+
+// Group bounds: cumulative ends, made non-decreasing and clamped into [0, M]:
+// any values give ranges inside the matrices.
+//
+// kGroupM: the group and first row of tile row `want` (tile rows of BM rows,
+// counted group by group from each group's first row), and the number of tile
+// rows.  64 groups a time, one per lane: a running maximum (the clamp) and a
+// running sum of tile counts over the lanes.
+struct GroupTile {
+  int32_t group;  // -1: past the last
+  int64_t m0, m_end, total;
+};
+template <int BM>
+__device__ __forceinline__ GroupTile find_tile(const int32_t *ends, int32_t G, int64_t M, int64_t want) {
+  const int lane = threadIdx.x & 63;
+  GroupTile r{-1, 0, 0, 0};
+  int32_t floor_end = 0;
+  int64_t before = 0;
+  for (int32_t g0 = 0; g0 < G; g0 += 64) {
+    const int32_t m32 = (int32_t)M;
+    int32_t end = g0 + lane < G ? min(max(*mx::gptr(ends + g0 + lane), 0), m32) : 0;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int32_t up = __shfl_up(end, o, 64);
+      if (lane >= o) end = max(end, up);
+    }
+    end = max(end, floor_end);
+    int32_t start = __shfl_up(end, 1, 64);
+    if (lane == 0) start = floor_end;
+    int32_t tiles = (end - start + BM - 1) / BM, sum = tiles;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int32_t up = __shfl_up(sum, o, 64);
+      if (lane >= o) sum += up;
+    }
+    const uint64_t hit = __ballot(want < before + sum);
+    if (hit && r.group < 0) {
+      const int e = __builtin_amdgcn_readfirstlane((int)__ffsll((unsigned long long)hit) - 1);
+      r.group = g0 + e;
+      const int32_t s = __builtin_amdgcn_readlane(start, e), inc = __builtin_amdgcn_readlane(sum, e);
+      const int32_t own = __builtin_amdgcn_readlane(tiles, e);
+      r.m0 = s + (int64_t)((int32_t)(want - before) - (inc - own)) * BM;
+      r.m_end = __builtin_amdgcn_readlane(end, e);
+    }
+    floor_end = __builtin_amdgcn_readlane(end, 63);
+    before += __builtin_amdgcn_readlane(sum, 63);
+  }
+  r.total = before;
+  return r;
+}
+
+// kGroupK: the start and end of group `want`.
+__device__ __forceinline__ void find_group(const int32_t *ends, int32_t want, int64_t T, int64_t &start, int64_t &end) {
+  const int lane = threadIdx.x & 63;
+  int32_t below = 0;  // largest end before `want`
+  for (int32_t e = lane; e < want; e += 64) below = max(below, *mx::gptr(ends + e));
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) below = max(below, __shfl_xor(below, o, 64));
+  below = __builtin_amdgcn_readfirstlane(below);
+  start = min<int64_t>(below, T);
+  end = min<int64_t>(max(below, __builtin_amdgcn_readfirstlane(*mx::gptr(ends + want))), T);
+}
+
+// Position in the tile order -> tile row and column: bands of kTileRows tile
+// rows, walked column by column, so that tiles in flight share operand rows.
+__device__ __forceinline__ void tile_of(u32 L, u32 tiles_m, u32 tiles_n, u32 &tm, u32 &tn) {
+  const u32 per = (u32)kTileRows * tiles_n, band = L / per, in = L % per;
+  const u32 rows = min((u32)kTileRows, tiles_m - band * (u32)kTileRows);
+  tm = band * (u32)kTileRows + in % rows;
+  tn = in / rows;
+}
+
+template <int MODE, int AL, int BL, int WI, int WJ, int RING, bool F32>
+__global__ __launch_bounds__(kThreads, 1) void k_group_gemm(const GemmArgs g) {
+  constexpr int BM = 64 * WI, BN = 64 * WJ;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * kBK * 2];
+  Tile t{};
+  u32 tm, tn;
+  EmitC<F32> emit{g.c, g.ldc, 0, g.vec_c != 0};
+  if constexpr (MODE == kGroupM) {
+    // the real number of tile rows first, then this workgroup's tile
+    const int64_t total = find_tile<BM>(g.ends, g.G, g.M, INT64_MAX).total;
+    const u32 R = (u32)total * (u32)g.tiles_n;
+    if (blockIdx.x >= R) return;
+    tile_of(mx::xcd_remap(blockIdx.x, R), (u32)total, (u32)g.tiles_n, tm, tn);
+    const GroupTile gt = find_tile<BM>(g.ends, g.G, g.M, tm);
+    t.a = g.a + gt.m0 * g.lda;
+    t.b = g.b + (int64_t)gt.group * g.stride_b;
+    t.rows = (u32)min<int64_t>(BM, gt.m_end - gt.m0);
+    t.k_len = g.K;
+    emit.c = F32 ? (void *)(static_cast<float *>(g.c) + gt.m0 * g.ldc) : (void *)(static_cast<uint16_t *>(g.c) + gt.m0 * g.ldc);
+  } else {
+    const u32 R = (u32)g.tiles_m * (u32)g.tiles_n;
+    const u32 L = mx::xcd_remap(blockIdx.x, R * (u32)g.G);
+    const int32_t grp = (int32_t)(L / R);
+    tile_of(L % R, (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
+    int64_t start, end;
+    find_group(g.ends, grp, g.K, start, end);
+    const int64_t m0 = (int64_t)tm * BM;
+    t.a = g.a + start * g.lda + m0;
+    t.b = g.b + start * g.ldb;
+    t.rows = (u32)min<int64_t>(BM, g.M - m0);
+    t.k_len = end - start;
+    const int64_t at = (int64_t)grp * g.stride_c + m0 * g.ldc;
+    emit.c = F32 ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
+  }
+  const int64_t n0 = (int64_t)tn * BN;
+  t.b += BL == kKC ? n0 * g.ldb : n0;
+  t.cols = emit.cols = (u32)min<int64_t>(BN, g.N - n0);
+  emit.c = F32 ? (void *)(static_cast<float *>(emit.c) + n0) : (void *)(static_cast<uint16_t *>(emit.c) + n0);
+  gemm_tile<kBf16, AL, BL, WI, WJ, RING, false>(g, t, smem, emit);
+}
+
+}  // namespace mxt

@@ -119,6 +119,36 @@ mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b,
                                       const int32_t *group_ends, int64_t G, int64_t M, int64_t N, int64_t T,
                                       void *c, int64_t ldc, int64_t stride_c, int c_dtype, void *stream);
 
+/*
+ * Orthogonalised updates (Newton-Schulz): for each of `batch` matrices
+ * G [m, n],
+ *   X = G / (|G| + eps),  |G| = sqrt(sum of squares),
+ *   `steps` times  X <- a X + b (X X^T) X + c (X X^T)^2 X,
+ * with coeffs = {a, b, c} (HOST memory, read during the call).  Every singular
+ * value s of X goes to a s + b s^3 + c s^5 at each step; coefficients like
+ * (3.4445, -4.7750, 2.0315) bring five steps' values near 1.
+ *   g   : dtype, matrix i at g + i * stride_g, row stride ld_g
+ *   out : out_dtype, likewise with stride_out, ld_out
+ *   workspace : at least mxtrain_newton_schulz_workspace(...) bytes, 256-byte
+ *         aligned.
+ * Requires that the steps keep the singular values at most 2 (they start at
+ * most 1); a step that leads past that overflows to infinities or NaN.  An
+ * fp32 result is computed to about fp32's accuracy, a bf16 result with 11
+ * significant bits between the products.  A matrix with NaN or infinite
+ * entries gives NaN everywhere (steps >= 1); the others of the batch are not
+ * touched by it.  A zero matrix gives zeros where eps > 0.
+ * Any dimensions (the odd ones and single rows among them) and strides;
+ * pointers aligned to their element.  0 <= steps <= 100, eps >= 0, finite
+ * coefficients (MXTRAIN_ERR_VALUE); batch <= 65535, m, n < 2^22
+ * (MXTRAIN_ERR_SHAPE).  An empty batch or matrix returns MXTRAIN_OK and
+ * enqueues nothing.
+ */
+int64_t mxtrain_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int out_dtype);
+mxtrain_status mxtrain_newton_schulz(const void *g, int64_t ld_g, int64_t stride_g, int dtype,
+                                     int64_t batch, int64_t m, int64_t n, int steps, const float *coeffs, float eps,
+                                     void *out, int64_t ld_out, int64_t stride_out, int out_dtype,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+
 /* Static, NUL-terminated description of a status code (never NULL). */
 const char *mxtrain_status_str(mxtrain_status status);
 

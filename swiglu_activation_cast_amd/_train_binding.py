@@ -16,7 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import Optional, Sequence, Tuple
 
 import torch
 
@@ -35,6 +35,9 @@ _SIGNATURES = {
                                       _i64, _p]),
     "mxtrain_grouped_gemm": (_int, [_p, _i64, _p, _i64, _i64, _int, _p, _i64, _i64, _i64, _i64, _p, _i64, _int, _p]),
     "mxtrain_grouped_gemm_k": (_int, [_p, _i64, _p, _i64, _p, _i64, _i64, _i64, _i64, _p, _i64, _i64, _int, _p]),
+    "mxtrain_newton_schulz_workspace": (_i64, [_i64, _i64, _i64, _int]),
+    "mxtrain_newton_schulz": (_int, [_p, _i64, _i64, _int, _i64, _i64, _i64, _int, _p, _f32, _p, _i64, _i64, _int, _p,
+                                     _i64, _p]),
     "mxtrain_status_str": (ctypes.c_char_p, [_int]),
 }
 
@@ -260,4 +263,35 @@ def mxtrain_grouped_gemm_k(a: torch.Tensor, b: torch.Tensor, group_ends: torch.T
     ldc = _ld(c, "out")
     _call("mxtrain_grouped_gemm_k", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), _ld(b, "b"), pe, G, M, N, T,
           c.data_ptr(), ldc, c.stride(0) if G > 1 else max(ldc * M, 1), _TYPES[c.dtype], _stream_of(dev, stream))
+    return c
+
+
+def mxtrain_newton_schulz(g: torch.Tensor, *, steps: int = 5,
+                          coeffs: Sequence[float] = (3.4445, -4.7750, 2.0315), eps: float = 1e-7,
+                          out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Orthogonalised update of each matrix of g [m, n] or [B, m, n] (bf16 or fp32).
+
+    X = g / (|g| + eps), then `steps` times X <- a X + b (X X^T) X +
+    c (X X^T)^2 X with (a, b, c) = coeffs.  Returns g's shape in `out`'s
+    dtype, `out_dtype`, or g's; the workspace is
+    mxtrain_newton_schulz_workspace(B, m, n, type) bytes, 256-byte aligned."""
+    if not isinstance(g, torch.Tensor) or g.dim() not in (2, 3):
+        raise ValueError("g must be a matrix [m, n] or a batch [B, m, n]")
+    _gpu(g, "g", _FLOATS, g.dim())
+    dev = g.device
+    if len(coeffs) != 3:
+        raise ValueError("coeffs must be three numbers")
+    c = _out(out, "out", tuple(g.shape), _out_dtype(out, out_dtype or g.dtype), dev)
+    m, n = g.shape[-2:]
+    batch = g.shape[0] if g.dim() == 3 else 1
+    ld_g, ld_c = _ld(g, "g"), _ld(c, "out")
+    several = g.dim() == 3 and batch > 1
+    stride_g = g.stride(0) if several else 0
+    stride_c = c.stride(0) if several else 0
+    nbytes = train_lib().mxtrain_newton_schulz_workspace(batch, m, n, _TYPES[c.dtype])
+    ws = _workspace(nbytes, workspace, dev, stream)
+    _call("mxtrain_newton_schulz", dev, g.data_ptr(), ld_g, stride_g, _TYPES[g.dtype], batch, m, n, int(steps),
+          (ctypes.c_float * 3)(*coeffs), eps, c.data_ptr(), ld_c, stride_c, _TYPES[c.dtype], ws.data_ptr(),
+          ws.numel() * ws.element_size(), _stream_of(dev, stream))
     return c

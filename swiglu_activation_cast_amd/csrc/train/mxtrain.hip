@@ -10,6 +10,7 @@
 #include "mxtrain.h"
 #include "tr_gemm.hpp"
 #include "tr_norm.hpp"
+#include "tr_ortho.hpp"
 
 namespace {
 
@@ -167,6 +168,140 @@ mxtrain_status operand_check(const void *p, int64_t ld, int64_t rows, int64_t co
 
 bool vec_c_ok(const void *c, int64_t ldc, int64_t stride_c, int type) {
   return aligned(c, (uintptr_t)(4 * size_of(type))) && ldc % 4 == 0 && stride_c % 4 == 0;
+}
+
+// ------------------------------------------------------- orthogonalisation
+// Workspace: the fp16 planes of X (two, in turn), S and p(S), then the sums
+// of squares and phi.  Every part starts at a multiple of 256 bytes.
+struct NsPlan {
+  bool split, tall;
+  int64_t s;             // the shorter side
+  int64_t ld_x, stride_x, ld_s, stride_s;
+  int64_t x[2][2], sq[2][2];  // byte offsets: [which][plane]; sq: S, p(S)
+  int64_t sums, phi, bytes;   // bytes < 0: too large
+};
+
+NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int out_dtype) {
+  NsPlan p{};
+  p.split = out_dtype == MXTRAIN_F32;
+  p.tall = m > n;
+  p.s = std::min(m, n);
+  p.ld_x = (n + 7) / 8 * 8;
+  p.stride_x = m * p.ld_x;
+  p.ld_s = (p.s + 7) / 8 * 8;
+  p.stride_s = p.s * p.ld_s;
+  int64_t at = 0;
+  bool ok = true;
+  auto take = [&](int64_t elems, int64_t size) {
+    const int64_t here = at;
+    int64_t b;
+    ok = ok && !__builtin_mul_overflow(elems, size * batch, &b) && b < (INT64_MAX >> 8);
+    if (ok) at += (b + 255) / 256 * 256;
+    return here;
+  };
+  for (int which = 0; which < 2; which++)
+    for (int plane = 0; plane < (p.split ? 2 : 1); plane++) {
+      p.x[which][plane] = take(p.stride_x, 2);
+      p.sq[which][plane] = take(p.stride_s, 2);
+    }
+  p.sums = take(mxt::kNormBlocks, 8);
+  p.phi = take(1, 4);
+  p.bytes = ok ? at : -1;
+  return p;
+}
+
+template <int STEP, int AL, int BL, bool SPLIT>
+mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
+  constexpr bool sym = STEP == mxt::kGram || STEP == mxt::kPoly;
+  auto tiles = [&](int64_t b) {
+    const int64_t tm = (p.g.M + b - 1) / b, tn = (p.g.N + b - 1) / b;
+    return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
+  };
+  const int cus = cu_count();
+  const int64_t b = tiles(256) >= cus ? 256 : tiles(128) >= cus / 2 ? 128 : 64;
+  p.g.tiles_m = (int32_t)((p.g.M + b - 1) / b);
+  p.g.tiles_n = (int32_t)((p.g.N + b - 1) / b);
+  const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, 2, SPLIT>
+                  : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, 2, SPLIT>
+                             : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 4, SPLIT>;
+  return launch(k, tiles(b), mxt::kThreads, p, stream);
+}
+
+template <bool SPLIT>
+mxtrain_status ns_run(const NsPlan &pl, mxt::NsArgs n, int64_t batch, int64_t m, int64_t cols, int steps,
+                      const float *co, void *out, int64_t ld_out, int64_t stride_out, uint8_t *ws, void *stream) {
+  auto plane = [&](const int64_t *off, int i) { return reinterpret_cast<_Float16 *>(ws + off[i]); };
+  auto bits = [](const _Float16 *p) { return reinterpret_cast<const uint16_t *>(p); };
+  // p(S) is held times the largest power of two that keeps |a| + 4 |b| + 16 |c|
+  // (its bound for singular values up to 2) below fp16's largest number
+  const float most = std::max(std::fabs(co[0]) + 4 * std::fabs(co[1]) + 16 * std::fabs(co[2]), 1e-30f);
+  const float ps = std::ldexp(1.0f, std::min(14, std::max(-100, std::ilogb(60000.0f / most))));
+  mxtrain_status st = MXTRAIN_OK;
+  for (int step = 0; step < steps; step++) {
+    const int cur = step & 1;
+    const bool last = step == steps - 1;
+    const _Float16 *x = plane(pl.x[cur], 0), *x_lo = SPLIT ? plane(pl.x[cur], 1) : nullptr;
+    _Float16 *s = plane(pl.sq[0], 0), *s_lo = SPLIT ? plane(pl.sq[0], 1) : nullptr;
+    _Float16 *q = plane(pl.sq[1], 0), *q_lo = SPLIT ? plane(pl.sq[1], 1) : nullptr;
+    mxt::NsGemm gram{}, poly{}, next{};
+    gram.g.a = gram.g.b = bits(x);
+    gram.a_lo = gram.b_lo = bits(x_lo);
+    gram.g.lda = gram.g.ldb = pl.ld_x;
+    gram.g.stride_a = gram.g.stride_b = pl.stride_x;
+    gram.g.M = gram.g.N = pl.s;
+    gram.g.K = pl.tall ? m : cols;
+    gram.g.c = s;
+    gram.c_lo = s_lo;
+    gram.g.ldc = pl.ld_s;
+    gram.g.stride_c = pl.stride_s;
+    gram.scale = mxt::kSScale / (mxt::kXScale * mxt::kXScale);
+    poly.g.a = poly.g.b = bits(s);
+    poly.a_lo = poly.b_lo = bits(s_lo);
+    poly.s = s;
+    poly.s_lo = s_lo;
+    poly.g.lda = poly.g.ldb = poly.g.ldc = pl.ld_s;
+    poly.g.stride_a = poly.g.stride_b = poly.g.stride_c = pl.stride_s;
+    poly.g.M = poly.g.N = poly.g.K = pl.s;
+    poly.g.c = q;
+    poly.c_lo = q_lo;
+    poly.phi = step == 0 ? n.phi : nullptr;
+    poly.ca = co[0] * ps;
+    poly.cb = co[1] * ps / mxt::kSScale;
+    poly.cc = co[2] * ps / (mxt::kSScale * mxt::kSScale);
+    const uint16_t *hx = bits(x), *hq = bits(q), *lx = bits(x_lo), *lq = bits(q_lo);
+    next.g.a = pl.tall ? hx : hq;
+    next.a_lo = pl.tall ? lx : lq;
+    next.g.b = pl.tall ? hq : hx;
+    next.b_lo = pl.tall ? lq : lx;
+    next.g.lda = pl.tall ? pl.ld_x : pl.ld_s;
+    next.g.stride_a = pl.tall ? pl.stride_x : pl.stride_s;
+    next.g.ldb = pl.tall ? pl.ld_s : pl.ld_x;
+    next.g.stride_b = pl.tall ? pl.stride_s : pl.stride_x;
+    next.g.M = m;
+    next.g.N = cols;
+    next.g.K = pl.s;
+    next.g.c = last ? out : plane(pl.x[cur ^ 1], 0);
+    next.c_lo = last || !SPLIT ? nullptr : plane(pl.x[cur ^ 1], 1);
+    next.g.ldc = last ? ld_out : pl.ld_x;
+    next.g.stride_c = last ? stride_out : pl.stride_x;
+    next.g.vec_c = last && vec_c_ok(out, ld_out, stride_out, SPLIT ? MXTRAIN_F32 : MXTRAIN_BF16);
+    next.phi = step == 0 ? n.phi : nullptr;
+    next.scale = (last ? 1.0f / mxt::kXScale : 1.0f) / ps;
+    using namespace mxt;
+    st = pl.tall ? ns_gemm<kGram, kMC, kMC, SPLIT>(gram, batch, stream)
+                 : ns_gemm<kGram, kKC, kKC, SPLIT>(gram, batch, stream);
+    if (st == MXTRAIN_OK) st = ns_gemm<kPoly, kKC, kKC, SPLIT>(poly, batch, stream);
+    if (st == MXTRAIN_OK) {
+      if (last)
+        st = pl.tall ? ns_gemm<kLast, kKC, kKC, SPLIT>(next, batch, stream)
+                     : ns_gemm<kLast, kKC, kMC, SPLIT>(next, batch, stream);
+      else
+        st = pl.tall ? ns_gemm<kNext, kKC, kKC, SPLIT>(next, batch, stream)
+                     : ns_gemm<kNext, kKC, kMC, SPLIT>(next, batch, stream);
+    }
+    if (st != MXTRAIN_OK) return st;
+  }
+  return MXTRAIN_OK;
 }
 
 }  // namespace
@@ -347,6 +482,76 @@ mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b,
   g.tiles_n = (int32_t)tiles_n;
   g.vec_c = vec_c_ok(c, ldc, stride_c, c_dtype);
   return launch(k.k, blocks, mxt::kThreads, g, stream);
+}
+
+int64_t mxtrain_newton_schulz_workspace(int64_t batch, int64_t m, int64_t n, int out_dtype) {
+  if (!type_ok(out_dtype) || batch <= 0 || m <= 0 || n <= 0 || batch > kMaxGroups || m >= mxt::kMaxLd ||
+      n >= mxt::kMaxLd)
+    return 0;
+  return std::max<int64_t>(ns_plan(batch, m, n, out_dtype).bytes, 0);
+}
+
+mxtrain_status mxtrain_newton_schulz(const void *g, int64_t ld_g, int64_t stride_g, int dtype, int64_t batch,
+                                     int64_t m, int64_t n, int steps, const float *coeffs, float eps, void *out,
+                                     int64_t ld_out, int64_t stride_out, int out_dtype, void *workspace,
+                                     int64_t workspace_bytes, void *stream) {
+  if (!type_ok(dtype) || !type_ok(out_dtype)) return MXTRAIN_ERR_TYPE;
+  if (!coeffs) return MXTRAIN_ERR_NULL;
+  if (steps < 0 || steps > 100 || !(eps >= 0.0f) || std::isinf(eps)) return MXTRAIN_ERR_VALUE;
+  for (int i = 0; i < 3; i++)
+    if (!std::isfinite(coeffs[i])) return MXTRAIN_ERR_VALUE;
+  if (batch < 0 || m < 0 || n < 0 || batch > kMaxGroups || m >= mxt::kMaxLd - 8 || n >= mxt::kMaxLd - 8)
+    return MXTRAIN_ERR_SHAPE;
+  if (batch == 0 || m == 0 || n == 0) return MXTRAIN_OK;
+  if (!g || !out || !workspace) return MXTRAIN_ERR_NULL;
+  if (ld_g < n || ld_out < n || stride_g < 0 || stride_out < 0) return MXTRAIN_ERR_STRIDE;
+  if (!aligned(g, (uintptr_t)size_of(dtype)) || !aligned(out, (uintptr_t)size_of(out_dtype)) || !aligned(workspace, 256))
+    return MXTRAIN_ERR_ALIGN;
+  int64_t all;
+  if (!extent_ok(m, n, ld_g) || !extent_ok(m, n, ld_out) || __builtin_mul_overflow(stride_g, batch, &all) ||
+      all > (INT64_MAX >> 4) || __builtin_mul_overflow(stride_out, batch, &all) || all > (INT64_MAX >> 4))
+    return MXTRAIN_ERR_OVERFLOW;
+  if (batch > 1 && stride_out < (m - 1) * ld_out + n) return MXTRAIN_ERR_STRIDE;
+  const NsPlan pl = ns_plan(batch, m, n, out_dtype);
+  if (pl.bytes < 0) return MXTRAIN_ERR_OVERFLOW;
+  if (workspace_bytes < pl.bytes) return MXTRAIN_ERR_WORKSPACE;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  mxt::NsArgs a{};
+  a.g = g;
+  a.ld_g = ld_g;
+  a.stride_g = stride_g;
+  a.rows = m;
+  a.cols = n;
+  a.batch = batch;
+  a.g_f32 = dtype == MXTRAIN_F32;
+  const int64_t v = 16 / size_of(dtype);
+  a.vec = aligned(g, 16) && ld_g % v == 0 && stride_g % v == 0;
+  a.eps = (double)eps;
+  a.sums = reinterpret_cast<double *>(ws + pl.sums);
+  a.phi = reinterpret_cast<float *>(ws + pl.phi);
+  a.x = reinterpret_cast<_Float16 *>(ws + pl.x[0][0]);
+  a.x_lo = pl.split ? reinterpret_cast<_Float16 *>(ws + pl.x[0][1]) : nullptr;
+  a.ld_x = pl.ld_x;
+  a.stride_x = pl.stride_x;
+  void *kargs[] = {&a};
+  if (hipLaunchKernel((const void *)&mxt::k_ns_norm, dim3(mxt::kNormBlocks, (unsigned)batch), dim3(256), kargs, 0,
+                      (hipStream_t)stream) != hipSuccess)
+    return MXTRAIN_ERR_LAUNCH;
+  const int64_t pieces = (m * (pl.ld_x / 8) + 255) / 256;
+  const unsigned grid = (unsigned)std::min<int64_t>(pieces, std::max<int64_t>(1, 2048 / batch));
+  if (hipLaunchKernel((const void *)&mxt::k_ns_cast, dim3(grid, (unsigned)batch), dim3(256), kargs, 0,
+                      (hipStream_t)stream) != hipSuccess)
+    return MXTRAIN_ERR_LAUNCH;
+  if (steps == 0) {
+    int f32 = out_dtype == MXTRAIN_F32;
+    void *pargs[] = {&a, &out, &ld_out, &stride_out, &f32};
+    return hipLaunchKernel((const void *)&mxt::k_ns_plain, dim3(grid, (unsigned)batch), dim3(256), pargs, 0,
+                           (hipStream_t)stream) == hipSuccess
+               ? MXTRAIN_OK
+               : MXTRAIN_ERR_LAUNCH;
+  }
+  return pl.split ? ns_run<true>(pl, a, batch, m, n, steps, coeffs, out, ld_out, stride_out, ws, stream)
+                  : ns_run<false>(pl, a, batch, m, n, steps, coeffs, out, ld_out, stride_out, ws, stream);
 }
 
 const char *mxtrain_status_str(mxtrain_status status) {

@@ -1,0 +1,286 @@
+// tr_ortho.hpp -- orthogonalising weight updates by Newton-Schulz steps.
+//
+//   X_0 = G / (|G| + eps),  |G| the root of the sum of squares,
+//   X <- p(X X^T) X,  p(S) = a I + b S + c S^2       (wide: rows <= columns)
+//   X <- X p(X^T X)                                  (tall)
+// so that every singular value s goes to a s + b s^3 + c s^5.  S has the
+// shorter side; it and p(S) are symmetric, so only the tiles on and below
+// their diagonal are computed and the others written as their transposes.
+//
+// A step is three products: S; S^2 with p's sum in its epilogue (a goes on the
+// diagonal, so that the third product needs no extra read of X); and p(S) X.
+//
+// Number format.  X, S and p(S) are held between the products as fp16 times a
+// power of two (their entries are bounded, since the singular values are: X by
+// 2^14, S by 2^13, p(S) by a power that keeps its largest possible entry in
+// range).  fp16's 11 places cost a bf16 result nothing that shows beside its
+// own 8.  For an fp32 result each is held as two fp16 numbers, high and low
+// part, 22 places, and a product is the sum of high x low, low x high and
+// high x high (low x low lies below 2^-22): three matrix-core passes, where
+// an fp32 product on this card runs at less than a tenth of the 16-bit rate.
+//
+// The first X is G times a power of two 2^e with (|G| + eps) 2^e in [1/2, 1),
+// which is exact for bf16 input; the factor that is left, phi = 1 / ((|G| +
+// eps) 2^e) in (1, 2], enters the first step's polynomial and result in fp32.
+// |G| is summed in 64 bits, which no fp32 input overflows.
+#pragma once
+#include "tr_gemm.hpp"
+
+namespace mxt {
+
+typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kXScale = 16384.0f;  // 2^14: singular values up to 2 stay below fp16's 65504
+constexpr float kSScale = 8192.0f;   // 2^13
+constexpr int kNormBlocks = 128;     // workgroups that share one matrix's sum of squares
+
+struct NsArgs {
+  const void *g;
+  int64_t ld_g, stride_g;
+  int64_t rows, cols, batch;
+  int32_t g_f32, vec;
+  double eps;
+  double *sums;  // [batch][kNormBlocks]
+  float *phi;    // [batch]
+  _Float16 *x, *x_lo;
+  int64_t ld_x, stride_x;
+};
+
+// Eight columns from `col` of a row of G; zeros past its end.
+__device__ __forceinline__ void ns_load8(const NsArgs &n, int64_t row, int64_t col, int64_t batch, float *v) {
+  const int64_t at = batch * n.stride_g + row * n.ld_g + col;
+  if (n.vec && col + 8 <= n.cols) {
+    if (n.g_f32) {
+      const f32x4_t *p = reinterpret_cast<const f32x4_t *>(static_cast<const float *>(n.g) + at);
+      const f32x4_t a = *mx::gptr(p), b = *mx::gptr(p + 1);
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+      const u32x4_t q = *mx::gptr(reinterpret_cast<const u32x4_t *>(static_cast<const uint16_t *>(n.g) + at));
+#pragma unroll
+      for (int i = 0; i < 4; i++) v[2 * i] = mx::lo_f(q[i]), v[2 * i + 1] = mx::hi_f(q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; i++)
+      v[i] = col + i >= n.cols ? 0.0f
+             : n.g_f32         ? *mx::gptr(static_cast<const float *>(n.g) + at + i)
+                               : to_f32(*mx::gptr(static_cast<const uint16_t *>(n.g) + at + i));
+  }
+}
+
+// Sum over the workgroup's 256 threads, in every thread.
+__device__ __forceinline__ double block_sum(double v, double *sm) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (sm[0] + sm[1]) + (sm[2] + sm[3]);
+}
+
+// Workgroup (p, batch): the squares of every kNormBlocks-th piece of 256
+// eight-column chunks.
+__global__ __launch_bounds__(256) void k_ns_norm(const NsArgs n) {
+  __shared__ double sm[4];
+  const int64_t cpr = (n.cols + 7) / 8, total = n.rows * cpr, batch = blockIdx.y;
+  double s = 0.0;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)kNormBlocks * 256) {
+    const int64_t row = i / cpr;
+    float v[8];
+    ns_load8(n, row, (i - row * cpr) * 8, batch, v);
+#pragma unroll
+    for (int j = 0; j < 8; j++) s = fma((double)v[j], (double)v[j], s);
+  }
+  s = block_sum(s, sm);
+  if (threadIdx.x == 0) *mx::gptr(n.sums + batch * kNormBlocks + blockIdx.x) = s;
+}
+
+// v as two fp16 numbers.  v is made opaque first: fused with the product it
+// comes from, the compiler may round that straight to fp16 for one use of the
+// high part and by way of fp32 for the other, which near a tie gives two
+// different high parts and a low part that fits neither.
+__device__ __forceinline__ void split_f16(float v, _Float16 &hi, _Float16 &lo) {
+#if __HIP_DEVICE_COMPILE__
+  asm volatile("" : "+v"(v));
+#endif
+  hi = (_Float16)v;
+  lo = (_Float16)(v - (float)hi);
+}
+
+// X_0's fp16 form (both planes where x_lo is given) and phi.
+__global__ __launch_bounds__(256) void k_ns_cast(const NsArgs n) {
+  __shared__ double sm[4];
+  const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
+  double norm = threadIdx.x < kNormBlocks ? *mx::gptr(n.sums + batch * kNormBlocks + threadIdx.x) : 0.0;
+  norm = sqrt(block_sum(norm, sm)) + n.eps;
+  // 2^e with norm 2^e in [1/2, 1); 0 or not finite: no scaling (phi carries it)
+  int ex = 0;
+  if (norm > 0.0 && norm < 1e300) frexp(norm, &ex);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *mx::gptr(n.phi + batch) = (float)(1.0 / ldexp(norm, -ex));
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / cpr, col = (i - row * cpr) * 8;
+    float v[8];
+    ns_load8(n, row, col, batch, v);
+    typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+    h8_t hi, lo;
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+      _Float16 a, b;
+      split_f16(ldexpf(v[j], 14 - ex), a, b);
+      hi[j] = a;
+      lo[j] = b;
+    }
+    const int64_t at = batch * n.stride_x + row * n.ld_x + col;
+    *mx::gptr(reinterpret_cast<h8_t *>(n.x + at)) = hi;
+    if (n.x_lo) *mx::gptr(reinterpret_cast<h8_t *>(n.x_lo + at)) = lo;
+  }
+}
+
+// No steps: X_0 itself.
+__global__ __launch_bounds__(256) void k_ns_plain(const NsArgs n, void *out, int64_t ld, int64_t stride, int f32) {
+  const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
+  const float f = *mx::gptr(n.phi + batch) / kXScale;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
+    const int64_t row = i / cpr, col = (i - row * cpr) * 8, at = batch * n.stride_x + row * n.ld_x + col;
+    for (int j = 0; j < 8 && col + j < n.cols; j++) {
+      const float v = ((float)*mx::gptr(n.x + at + j) + (n.x_lo ? (float)*mx::gptr(n.x_lo + at + j) : 0.0f)) * f;
+      const int64_t o = batch * stride + row * ld + col + j;
+      if (f32) *mx::gptr(static_cast<float *>(out) + o) = v;
+      else *mx::gptr(static_cast<uint16_t *>(out) + o) = from_f32<uint16_t>(v);
+    }
+  }
+}
+
+enum NsStep { kGram = 0, kPoly = 1, kNext = 2, kLast = 3 };
+
+struct NsGemm {
+  GemmArgs g;  // a, b: high planes; c: the result's high plane, or the output
+  const uint16_t *a_lo, *b_lo;
+  _Float16 *c_lo;
+  const _Float16 *s, *s_lo;  // kPoly: S itself
+  const float *phi;          // per matrix, or NULL (1)
+  float ca, cb, cc;          // kPoly: coefficients times p's scale, b and c over S's scales
+  float scale;               // the other steps: of the sums
+};
+
+// One step's results at tile (m0, n0) of matrix `batch`.
+template <int STEP, bool SPLIT>
+struct EmitNs {
+  _Float16 *hi, *lo;              // at the tile
+  _Float16 *mir_hi, *mir_lo;      // at the transposed tile, or NULL
+  const _Float16 *s_hi, *s_lo;    // kPoly: S at the tile
+  int64_t ld;
+  u32 cols;
+  bool diag;                      // kPoly: the tile is on the diagonal
+  float f0, f1, f2;
+  EmitC<SPLIT> out;               // kLast
+
+  __device__ __forceinline__ void operator()(u32 m, u32 n, f32x4_t v) const {
+    f32x4_t r;
+    if constexpr (STEP == kPoly) {
+      const int64_t at = (int64_t)m * ld + n;
+      const h4_t s = *mx::gptr(reinterpret_cast<const h4_t *>(s_hi + at));
+      h4_t sl = {};
+      if constexpr (SPLIT) sl = *mx::gptr(reinterpret_cast<const h4_t *>(s_lo + at));
+#pragma unroll
+      for (u32 e = 0; e < 4; e++) {
+        const float sv = (float)s[e] + (float)sl[e];
+        r[e] = fmaf(f2, v[e], f1 * sv) + (diag && m == n + e ? f0 : 0.0f);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; e++) r[e] = v[e] * f0;
+    }
+    if constexpr (STEP == kLast) {
+      out(m, n, r);
+    } else {
+      h4_t a, b;
+#pragma unroll
+      for (int e = 0; e < 4; e++) {
+        _Float16 x, y;
+        split_f16(r[e], x, y);
+        a[e] = x;
+        b[e] = y;
+      }
+      // rows are padded to whole chunks of 8: the four always fit
+      const int64_t at = (int64_t)m * ld + n;
+      *mx::gptr(reinterpret_cast<h4_t *>(hi + at)) = a;
+      if constexpr (SPLIT) *mx::gptr(reinterpret_cast<h4_t *>(lo + at)) = b;
+      if constexpr (STEP == kGram || STEP == kPoly) {
+        if (mir_hi) {
+#pragma unroll
+          for (u32 e = 0; e < 4; e++)
+            if (n + e < cols) {
+              const int64_t am = (int64_t)(n + e) * ld + m;
+              *mx::gptr(mir_hi + am) = a[e];
+              if constexpr (SPLIT) *mx::gptr(mir_lo + am) = b[e];
+            }
+        }
+      }
+    }
+  }
+};
+
+// Position L in row order of the tiles on and below the diagonal.
+__device__ __forceinline__ void lower_tile(u32 L, u32 &tm, u32 &tn) {
+  tm = (u32)((sqrtf(8.0f * (float)L + 1.0f) - 1.0f) * 0.5f);
+  while (tm * (tm + 1) / 2 > L) tm--;  // the root is within one of the row
+  while ((tm + 1) * (tm + 2) / 2 <= L) tm++;
+  tn = L - tm * (tm + 1) / 2;
+}
+
+template <int STEP, int AL, int BL, int WI, int WJ, int RING, bool SPLIT>
+__global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
+  constexpr int BM = 64 * WI, BN = 64 * WJ;
+  constexpr bool SYM = STEP == kGram || STEP == kPoly;
+  static_assert(!SYM || WI == WJ, "symmetric results take square tiles");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * kBK * 2];
+  const GemmArgs &g = p.g;
+  const u32 tiles = SYM ? (u32)g.tiles_m * (u32)(g.tiles_m + 1) / 2 : (u32)g.tiles_m * (u32)g.tiles_n;
+  const u32 L = mx::xcd_remap(blockIdx.x, gridDim.x);
+  const int64_t batch = L / tiles;
+  u32 tm, tn;
+  if constexpr (SYM) lower_tile(L % tiles, tm, tn);
+  else tile_of(L % tiles, (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
+  tm = (u32)__builtin_amdgcn_readfirstlane((int)tm);
+  tn = (u32)__builtin_amdgcn_readfirstlane((int)tn);
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int64_t a_at = batch * g.stride_a + (AL == kKC ? m0 * g.lda : m0);
+  const int64_t b_at = batch * g.stride_b + (BL == kKC ? n0 * g.ldb : n0);
+  Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, g.K, (u32)min<int64_t>(BM, g.M - m0), (u32)min<int64_t>(BN, g.N - n0)};
+  if constexpr (SPLIT) {
+    t.a_lo = p.a_lo + a_at;
+    t.b_lo = p.b_lo + b_at;
+  }
+  const float phi = p.phi ? *mx::gptr(p.phi + batch) : 1.0f;
+  EmitNs<STEP, SPLIT> e{};
+  const int64_t at = batch * g.stride_c + m0 * g.ldc + n0, mir = batch * g.stride_c + n0 * g.ldc + m0;
+  e.ld = g.ldc;
+  e.cols = t.cols;
+  if constexpr (STEP == kLast) {
+    e.out.c = SPLIT ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
+    e.out.ldc = g.ldc;
+    e.out.cols = t.cols;
+    e.out.vec = g.vec_c != 0;
+  } else {
+    e.hi = static_cast<_Float16 *>(g.c) + at;
+    e.lo = SPLIT ? p.c_lo + at : nullptr;
+    if (SYM && tm != tn) {
+      e.mir_hi = static_cast<_Float16 *>(g.c) + mir;
+      e.mir_lo = SPLIT ? p.c_lo + mir : nullptr;
+    }
+  }
+  if constexpr (STEP == kPoly) {
+    e.s_hi = p.s + at;
+    e.s_lo = SPLIT ? p.s_lo + at : nullptr;
+    e.diag = tm == tn;
+    e.f0 = p.ca;
+    e.f1 = p.cb * phi * phi;
+    e.f2 = p.cc * phi * phi * phi * phi;
+  } else {
+    e.f0 = STEP == kGram ? p.scale : p.scale * phi;
+  }
+  gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
+}
+
+}  // namespace mxt

@@ -167,7 +167,8 @@ mxtrain_status operand_check(const void *p, int64_t ld, int64_t rows, int64_t co
 }
 
 bool vec_c_ok(const void *c, int64_t ldc, int64_t stride_c, int type) {
-  return aligned(c, (uintptr_t)(4 * size_of(type))) && ldc % 4 == 0 && stride_c % 4 == 0;
+  const int64_t v = 16 / size_of(type);
+  return aligned(c, 16) && ldc % v == 0 && stride_c % v == 0;
 }
 
 // ------------------------------------------------------- orthogonalisation

@@ -163,22 +163,25 @@ struct NsGemm {
   float scale;               // the other steps: of the sums
 };
 
-// One step's results at tile (m0, n0) of matrix `batch`.
+// One step's results at a tile: fp16 planes (high, and low where SPLIT).
 template <int STEP, bool SPLIT>
 struct EmitNs {
-  _Float16 *hi, *lo;              // at the tile
-  _Float16 *mir_hi, *mir_lo;      // at the transposed tile, or NULL
-  const _Float16 *s_hi, *s_lo;    // kPoly: S at the tile
+  static constexpr bool kF32 = false, kMirror = STEP != kNext;
+  static constexpr int kPlanes = SPLIT ? 2 : 1;
+  _Float16 *out[2];             // at the tile
+  _Float16 *mir[2];             // at the transposed tile, or NULL
+  const _Float16 *s_hi, *s_lo;  // kPoly: S at the tile
   int64_t ld;
-  u32 cols;
-  bool diag;                      // kPoly: the tile is on the diagonal
+  bool diag;                    // kPoly: the tile is on the diagonal
   float f0, f1, f2;
-  EmitC<SPLIT> out;               // kLast
 
-  __device__ __forceinline__ void operator()(u32 m, u32 n, f32x4_t v) const {
+  __device__ __forceinline__ bool mirrored() const { return mir[0] != nullptr; }
+  __device__ __forceinline__ void pack(u32 m, u32 n, f32x4_t v, u32x2_t *p) const {
     f32x4_t r;
     if constexpr (STEP == kPoly) {
-      const int64_t at = (int64_t)m * ld + n;
+      // past the matrix (rows and columns that are not stored) S is read at
+      // the tile's first element
+      const int64_t at = m < rows && n < cols ? (int64_t)m * ld + n : 0;
       const h4_t s = *mx::gptr(reinterpret_cast<const h4_t *>(s_hi + at));
       h4_t sl = {};
       if constexpr (SPLIT) sl = *mx::gptr(reinterpret_cast<const h4_t *>(s_lo + at));
@@ -191,33 +194,34 @@ struct EmitNs {
 #pragma unroll
       for (int e = 0; e < 4; e++) r[e] = v[e] * f0;
     }
-    if constexpr (STEP == kLast) {
-      out(m, n, r);
-    } else {
-      h4_t a, b;
+    h4_t a, b;
 #pragma unroll
-      for (int e = 0; e < 4; e++) {
-        _Float16 x, y;
-        split_f16(r[e], x, y);
-        a[e] = x;
-        b[e] = y;
-      }
-      // rows are padded to whole chunks of 8: the four always fit
-      const int64_t at = (int64_t)m * ld + n;
-      *mx::gptr(reinterpret_cast<h4_t *>(hi + at)) = a;
-      if constexpr (SPLIT) *mx::gptr(reinterpret_cast<h4_t *>(lo + at)) = b;
-      if constexpr (STEP == kGram || STEP == kPoly) {
-        if (mir_hi) {
-#pragma unroll
-          for (u32 e = 0; e < 4; e++)
-            if (n + e < cols) {
-              const int64_t am = (int64_t)(n + e) * ld + m;
-              *mx::gptr(mir_hi + am) = a[e];
-              if constexpr (SPLIT) *mx::gptr(mir_lo + am) = b[e];
-            }
-        }
-      }
+    for (int e = 0; e < 4; e++) {
+      _Float16 x, y;
+      split_f16(r[e], x, y);
+      a[e] = x;
+      b[e] = y;
     }
+    p[0] = __builtin_bit_cast(u32x2_t, a);
+    if constexpr (SPLIT) p[1] = __builtin_bit_cast(u32x2_t, b);
+  }
+  // Rows are padded to whole chunks of 8, which all fit.
+  __device__ __forceinline__ void store(int k, u32 m, u32 n, u32x4_t v) const {
+    *mx::gptr(reinterpret_cast<u32x4_t *>(out[k] + (int64_t)m * ld + n)) = v;
+  }
+  __device__ __forceinline__ void store_mirror(int k, u32 n, u32 m, u32x4_t v) const {
+    *mx::gptr(reinterpret_cast<u32x4_t *>(mir[k] + (int64_t)n * ld + m)) = v;
+  }
+  u32 rows, cols;
+};
+
+// The last step's: C in its own type.
+template <bool F32>
+struct EmitLast : EmitC<F32> {
+  float f0;
+  __device__ __forceinline__ f32x4_t map(u32, u32, f32x4_t v) const { return f32x4_t{v[0] * f0, v[1] * f0, v[2] * f0, v[3] * f0}; }
+  __device__ __forceinline__ void pack(u32 m, u32 n, f32x4_t v, u32x2_t *p) const {
+    EmitC<F32>::pack(m, n, map(m, n, v), p);
   }
 };
 
@@ -253,34 +257,39 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     t.b_lo = p.b_lo + b_at;
   }
   const float phi = p.phi ? *mx::gptr(p.phi + batch) : 1.0f;
-  EmitNs<STEP, SPLIT> e{};
-  const int64_t at = batch * g.stride_c + m0 * g.ldc + n0, mir = batch * g.stride_c + n0 * g.ldc + m0;
-  e.ld = g.ldc;
-  e.cols = t.cols;
+  const int64_t at = batch * g.stride_c + m0 * g.ldc + n0;
   if constexpr (STEP == kLast) {
-    e.out.c = SPLIT ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
-    e.out.ldc = g.ldc;
-    e.out.cols = t.cols;
-    e.out.vec = g.vec_c != 0;
+    EmitLast<SPLIT> e{};
+    e.c = SPLIT ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
+    e.ldc = g.ldc;
+    e.cols = t.cols;
+    e.vec = g.vec_c != 0;
+    e.f0 = p.scale * phi;
+    gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
   } else {
-    e.hi = static_cast<_Float16 *>(g.c) + at;
-    e.lo = SPLIT ? p.c_lo + at : nullptr;
+    EmitNs<STEP, SPLIT> e{};
+    e.ld = g.ldc;
+    e.rows = t.rows;
+    e.cols = t.cols;
+    e.out[0] = static_cast<_Float16 *>(g.c) + at;
+    if (SPLIT) e.out[1] = p.c_lo + at;
     if (SYM && tm != tn) {
-      e.mir_hi = static_cast<_Float16 *>(g.c) + mir;
-      e.mir_lo = SPLIT ? p.c_lo + mir : nullptr;
+      const int64_t mir = batch * g.stride_c + n0 * g.ldc + m0;
+      e.mir[0] = static_cast<_Float16 *>(g.c) + mir;
+      if (SPLIT) e.mir[1] = p.c_lo + mir;
     }
+    if constexpr (STEP == kPoly) {
+      e.s_hi = p.s + at;
+      if (SPLIT) e.s_lo = p.s_lo + at;
+      e.diag = tm == tn;
+      e.f0 = p.ca;
+      e.f1 = p.cb * phi * phi;
+      e.f2 = p.cc * phi * phi * phi * phi;
+    } else {
+      e.f0 = STEP == kGram ? p.scale : p.scale * phi;
+    }
+    gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
   }
-  if constexpr (STEP == kPoly) {
-    e.s_hi = p.s + at;
-    e.s_lo = SPLIT ? p.s_lo + at : nullptr;
-    e.diag = tm == tn;
-    e.f0 = p.ca;
-    e.f1 = p.cb * phi * phi;
-    e.f2 = p.cc * phi * phi * phi * phi;
-  } else {
-    e.f0 = STEP == kGram ? p.scale : p.scale * phi;
-  }
-  gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
 }
 
 }  // namespace mxt

@@ -144,10 +144,18 @@ struct GroupKernel {
   int bm, bn;
 };
 
-template <int MODE, int AL, int BL, int WI, int WJ, int RING>
+#ifndef MXT_BK
+#define MXT_BK 64
+#define MXT_RING 2
+#endif
+#ifndef MXT_WI
+#define MXT_WI 4
+#define MXT_WJ 4
+#endif
+template <int MODE, int AL, int BL, int WI, int WJ, int BK, int RING>
 GroupKernel group_kernel(bool f32) {
-  return {f32 ? (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, RING, true>
-              : (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, RING, false>,
+  return {f32 ? (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, BK, RING, true>
+              : (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, BK, RING, false>,
           64 * WI, 64 * WJ};
 }
 
@@ -155,8 +163,8 @@ GroupKernel group_kernel(bool f32) {
 template <int MODE, int AL, int BL>
 GroupKernel group_pick(int64_t rows, int64_t N, int64_t copies, bool f32) {
   const int64_t big = (rows + 255) / 256 * ((N + 255) / 256) * copies;
-  if (big >= cu_count()) return group_kernel<MODE, AL, BL, 4, 4, 2>(f32);
-  return group_kernel<MODE, AL, BL, 2, 2, 2>(f32);
+  if (big >= cu_count()) return group_kernel<MODE, AL, BL, MXT_WI, MXT_WJ, MXT_BK, MXT_RING>(f32);
+  return group_kernel<MODE, AL, BL, 2, 2, 64, 2>(f32);
 }
 
 mxtrain_status operand_check(const void *p, int64_t ld, int64_t rows, int64_t cols) {
@@ -222,9 +230,9 @@ mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
   const int64_t b = tiles(256) >= cus ? 256 : tiles(128) >= cus / 2 ? 128 : 64;
   p.g.tiles_m = (int32_t)((p.g.M + b - 1) / b);
   p.g.tiles_n = (int32_t)((p.g.N + b - 1) / b);
-  const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, 2, SPLIT>
-                  : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, 2, SPLIT>
-                             : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 4, SPLIT>;
+  const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, 64, 2, SPLIT>
+                  : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, 64, 2, SPLIT>
+                             : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 64, 4, SPLIT>;
   return launch(k, tiles(b), mxt::kThreads, p, stream);
 }
 

@@ -48,8 +48,6 @@ enum Mode { kBatch = 0, kGroupM = 1, kGroupK = 2 };
 enum Elem { kBf16 = 0, kF16 = 1 };
 
 constexpr int kThreads = 256;
-constexpr int kBK = 64;                   // elements of K per stage
-constexpr int kKS = kBK / 16;             // MFMA steps per stage
 constexpr int kTileRows = 4;              // tile rows per band of the tile order
 constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows of this many elements stay below 2^31 bytes
 
@@ -72,21 +70,31 @@ typedef u32 u32x2_t __attribute__((ext_vector_type(2)));
 
 #define MXT_LDS __attribute__((address_space(3)))
 
-// 16 bytes a lane, global -> LDS: lane l's land at LDS byte `lds` + 16 l.
+// f(0), f(1), ... f(N - 1), each with its index as a compile-time constant.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void static_for(F &&f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    static_for<N, I + 1>(f);
+  }
+}
+
+// 16 bytes a lane, global -> LDS: lane l's land at LDS byte lds + AT + 16 l.
 // Asm, so that the compiler does not wait for it before LDS reads of other
-// slots; wait_vm awaits it.  M0 holds the LDS base (one wait state between its
-// write and the load) and is put back.
+// slots; wait_vm awaits it.  M0 takes the LDS base, which needs one wait state
+// between its write and the load; nothing else in these kernels uses M0, so it
+// is not put back.  Three instructions, since a wavefront alone on its SIMD
+// has room for about seven between two MFMAs (with the base's sum, M0 put back
+// and the bounds select per load, ten, a stage took 2650 cycles for its 2048
+// of MFMA).
+template <int AT>
 __device__ __forceinline__ void dma16(const void *base, u32 off, u32 lds) {
-  u32 saved;
   asm volatile(
-      "s_mov_b32 %0, m0\n\t"
-      "s_mov_b32 m0, %1\n\t"
+      "s_add_u32 m0, %0, %3\n\t"
       "s_nop 0\n\t"
-      "global_load_lds_dwordx4 %2, %3\n\t"
-      "s_nop 0\n\t"
-      "s_mov_b32 m0, %0"
-      : "=&s"(saved)
-      : "s"(lds), "v"(off), "s"(base));
+      "global_load_lds_dwordx4 %1, %2" ::"s"(lds),
+      "v"(off), "s"(base), "n"(AT)
+      : "scc");
 }
 // A value that every lane holds alike, in a scalar register.
 template <class P>
@@ -115,8 +123,9 @@ __device__ __forceinline__ v16f_t mfma(u32x4_t first, u32x4_t second, v16f_t c) 
 // columns where it is stored kMC).  `rows` of them exist (>= 1); the others
 // are read as the last one and never stored.  A wavefront fills kLoads
 // kilobytes of each stage.
-template <int L, int W>
+template <int L, int W, int BK>
 struct Operand {
+  static constexpr int kBK = BK, kKS = BK / 16;  // elements and MFMA steps of a stage
   static constexpr int kRows = 64 * W;
   static constexpr int kBytes = kRows * kBK * 2;  // of a stage
   static constexpr int kLoads = kBytes / 1024 / 4;
@@ -127,14 +136,16 @@ struct Operand {
   const uint8_t *base;  // of the tile's first k (uniform)
   int64_t step;         // bytes from a stage to the next (uniform)
   u32 off[kLoads];      // this lane's byte offset in each load
-  u32 tail[kLoads];     // kMC: the same at the stage's first k row
+  u32 tail[kLoads];     // the same at the stage's first k
+  u32 cur[kLoads];      // which of the two the loads use
   int k_of[kLoads];     // first k (within the stage) of what the lane loads
   u32 lds_w;            // LDS byte (within a stage's operand) of this wavefront's first load
   u32 rd[L == kKC ? kKS : W];  // this lane's LDS read offsets
 
   // XOR of the chunk position in LDS row r.
   static __device__ __forceinline__ u32 key(u32 r) {
-    if constexpr (L == kKC) return (r >> 1) & 7u;
+    if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
+    else if constexpr (L == kKC) return (r >> 2) & 3u;
     else if constexpr (W == 1) return ((r >> 1) & 1u) << 2;  // 128-byte rows: two rows per turn of the banks
     else return (r & 3u) << 2;
   }
@@ -175,10 +186,17 @@ struct Operand {
       }
     }
   }
-  // Loads q of the stage at `src`, kmax of whose k exist: chunks (rows) at or
-  // past it are read at the stage's first k instead and cleared afterwards.
-  __device__ __forceinline__ void load(int q, const uint8_t *src, int kmax, u32 slot) const {
-    dma16(src, k_of[q] < kmax ? off[q] : tail[q], slot + lds_w + (u32)q * 1024u);
+  // From here on the stages to be loaded have kmax elements of K: chunks (rows)
+  // at or past it are read at the stage's first k instead, and cleared once
+  // they have landed.
+  __device__ __forceinline__ void set_kmax(int kmax) {
+#pragma unroll
+    for (int q = 0; q < kLoads; q++) cur[q] = k_of[q] < kmax ? off[q] : tail[q];
+  }
+  // Load number Q of the stage at `src`; `slot`: this wavefront's first byte.
+  template <int Q>
+  __device__ __forceinline__ void load(const uint8_t *src, u32 slot) const {
+    dma16<Q * 1024>(src, cur[Q], slot);
   }
   // This lane's part of a landed stage, k >= kmax -> 0.
   __device__ __forceinline__ void clear(MXT_LDS uint8_t *slot, int lane, int kmax) const {
@@ -222,10 +240,11 @@ struct Tile {
   u32 rows, cols;
 };
 
-template <int EL, int AL, int BL, int WI, int WJ, int RING, bool SPLIT, class Emit>
+template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, class Emit>
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint8_t *smem, const Emit &emit) {
-  using A = Operand<AL, WI>;
-  using B = Operand<BL, WJ>;
+  using A = Operand<AL, WI, BK>;
+  using B = Operand<BL, WJ, BK>;
+  constexpr int kBK = BK, kKS = BK / 16;
   constexpr int kSlot = A::kBytes + B::kBytes;
   constexpr int kLoads = A::kLoads + B::kLoads;
   constexpr int kMfmas = WI * WJ;
@@ -259,9 +278,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   }
   struct Src {
     const uint8_t *a, *b;
-    int kmax;
-    u32 slot;
+    u32 slot_a, slot_b;
   };
+  int kmax = kBK;  // of the stages being loaded
+  oa.set_kmax(kmax);
+  ob.set_kmax(kmax);
   // Stages past the last re-read it into a slot that is not read again.
   auto source = [&](int st) {
     int s = min(st, n_stage - 1), pass = 0;
@@ -272,13 +293,20 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     Src r;
     r.a = (SPLIT && pass == 1 ? a_lo : oa.base) + s * oa.step;
     r.b = (SPLIT && pass == 0 ? b_lo : ob.base) + s * ob.step;
-    r.kmax = s == per - 1 ? k_tail : kBK;
-    r.slot = lds0 + (u32)(st % RING) * kSlot;
+    r.slot_a = lds0 + (u32)(st % RING) * kSlot + oa.lds_w;
+    r.slot_b = lds0 + (u32)(st % RING) * kSlot + A::kBytes + ob.lds_w;
+    const int k = s == per - 1 ? k_tail : kBK;
+    if (k != kmax) {  // uniform; once per pass over K, if K has a partial stage
+      kmax = k;
+      oa.set_kmax(k);
+      ob.set_kmax(k);
+    }
     return r;
   };
-  auto load = [&](int q, const Src &r) {
-    if (q < A::kLoads) oa.load(q < A::kLoads ? q : 0, r.a, r.kmax, r.slot);
-    else ob.load(q < A::kLoads ? 0 : q - A::kLoads, r.b, r.kmax, r.slot + A::kBytes);
+  auto load = [&](auto q, const Src &r) {
+    constexpr int Q = decltype(q)::value;
+    if constexpr (Q < A::kLoads) oa.template load<Q>(r.a, r.slot_a);
+    else ob.template load<Q - A::kLoads>(r.b, r.slot_b);
   };
   // Stage st has landed: clear what lies past K (each lane what it loaded).
   auto clear = [&](int st) {
@@ -299,29 +327,29 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     else if (n < a1 + B::kReads) ob.read(slot + A::kBytes, s, n - a1, 1, f.b);
     else oa.read(slot, s, n - B::kReads, 2, f.a);
   };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  // The stage's loads go out in its first two phases, half each.
+  constexpr int kHalf = (kLoads + 1) / 2;
   // MFMAs of one step from `cur`, and between them the reads of step s of
-  // `slot` into `nxt` and loads [q0, q1) of `src`.
-  auto phase = [&](auto do_mfma, const MXT_LDS uint8_t *slot, int s, Frags &cur, Frags &nxt, int q0, int q1,
+  // `slot` into `nxt` and, in phase 0 and 1 of a stage, half of its loads.
+  auto phase = [&](auto do_mfma, auto loads, const MXT_LDS uint8_t *slot, int s, Frags &cur, Frags &nxt,
                    const Src &src) {
-#pragma unroll
-    for (int k = 0; k < kMfmas; k++) {
-      const int i = k / WJ, j = k % WJ;
+    constexpr int half = decltype(loads)::value;  // 0, 1, or 2: none
+    constexpr int q0 = half == 0 ? 0 : half == 1 ? kHalf : kLoads, q1 = half == 0 ? kHalf : kLoads;
+    static_for<kMfmas>([&](auto kk) {
+      constexpr int k = decltype(kk)::value, i = k / WJ, j = k % WJ;
       if constexpr (decltype(do_mfma)::value) acc[i][j] = mfma<EL>(cur.b[j], cur.a[i], acc[i][j]);
       // reads as early as one per MFMA allows, loads spread evenly
       constexpr int per_k = (kReads + kMfmas - 1) / kMfmas;
 #pragma unroll
       for (int n = k * per_k; n < (k + 1) * per_k; n++)
         if (n < kReads) read(slot, s, n, nxt);
-#pragma unroll
-      for (int q = 0; q < kLoads; q++)
-        if (q >= q0 + k * (q1 - q0) / kMfmas && q < q0 + (k + 1) * (q1 - q0) / kMfmas) load(q, src);
+      static_for<(k + 1) * (q1 - q0) / kMfmas - k * (q1 - q0) / kMfmas>(
+          [&](auto q) { load(std::integral_constant<int, q0 + k * (q1 - q0) / kMfmas + decltype(q)::value>{}, src); });
       __builtin_amdgcn_sched_barrier(0);  // keep this order
-    }
+    });
   };
-  using Yes = std::true_type;
-  using No = std::false_type;
-  // The stage's loads go out in its first two phases.
-  constexpr int kHalf = (kLoads + 1) / 2;
 
   Frags f0, f1;  // the steps alternate between the two
   static_assert(kKS % 2 == 0, "the last step of a stage leaves its operands in f1");
@@ -330,15 +358,18 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   // stage st's slot is free.
   auto stage = [&](auto has_last, int st) {
     const MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
-    const bool first = !decltype(has_last)::value;
+    constexpr bool first = !decltype(has_last)::value;
     // the loads of the stage that takes over stage st - 1's slot
     const Src src = first ? Src{} : source(st - 1 + RING);
-    phase(has_last, slot, 0, f1, f0, 0, first ? 0 : kHalf, src);
-    phase(Yes{}, slot, 1, f0, f1, first ? 0 : kHalf, first ? 0 : kLoads, src);
+    using L0 = std::integral_constant<int, first ? 2 : 0>;
+    using L1 = std::integral_constant<int, first ? 2 : 1>;
+    using None = std::integral_constant<int, 2>;
+    phase(has_last, L0{}, slot, 0, f1, f0, src);
+    phase(Yes{}, L1{}, slot, 1, f0, f1, src);
 #pragma unroll
     for (int s = 2; s < kKS; s += 2) {
-      phase(Yes{}, slot, s, f1, f0, 0, 0, src);
-      phase(Yes{}, slot, s + 1, f0, f1, 0, 0, src);
+      phase(Yes{}, None{}, slot, s, f1, f0, src);
+      phase(Yes{}, None{}, slot, s + 1, f0, f1, src);
     }
 #if __HIP_DEVICE_COMPILE__
     // keep this stage's results in its block
@@ -361,8 +392,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
 #pragma unroll
     for (int st = 0; st < RING; st++) {
       const Src src = source(st);
-#pragma unroll
-      for (int q = 0; q < kLoads; q++) load(q, src);
+      static_for<kLoads>([&](auto q) { load(q, src); });
     }
     wait_vm<(RING - 1) * kLoads>();
     clear(0);
@@ -546,10 +576,10 @@ __device__ __forceinline__ void tile_of(u32 L, u32 tiles_m, u32 tiles_n, u32 &tm
   tn = in / rows;
 }
 
-template <int MODE, int AL, int BL, int WI, int WJ, int RING, bool F32>
-__global__ __launch_bounds__(kThreads, 1) void k_group_gemm(const GemmArgs g) {
+template <int MODE, int AL, int BL, int WI, int WJ, int BK, int RING, bool F32>
+__global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(const GemmArgs g) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * kBK * 2];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * 2];
   Tile t{};
   u32 tm, tn;
   EmitC<F32> emit{g.c, g.ldc, 0, g.vec_c != 0};
@@ -584,7 +614,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_group_gemm(const GemmArgs g) {
   t.b += BL == kKC ? n0 * g.ldb : n0;
   t.cols = emit.cols = (u32)min<int64_t>(BN, g.N - n0);
   emit.c = F32 ? (void *)(static_cast<float *>(emit.c) + n0) : (void *)(static_cast<uint16_t *>(emit.c) + n0);
-  gemm_tile<kBf16, AL, BL, WI, WJ, RING, false>(g, t, smem, emit);
+  gemm_tile<kBf16, AL, BL, WI, WJ, BK, RING, false>(g, t, smem, emit);
 }
 
 }  // namespace mxt

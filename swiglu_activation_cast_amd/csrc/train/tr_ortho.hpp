@@ -233,12 +233,12 @@ __device__ __forceinline__ void lower_tile(u32 L, u32 &tm, u32 &tn) {
   tn = L - tm * (tm + 1) / 2;
 }
 
-template <int STEP, int AL, int BL, int WI, int WJ, int RING, bool SPLIT>
+template <int STEP, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
   constexpr bool SYM = STEP == kGram || STEP == kPoly;
   static_assert(!SYM || WI == WJ, "symmetric results take square tiles");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * kBK * 2];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * 2];
   const GemmArgs &g = p.g;
   const u32 tiles = SYM ? (u32)g.tiles_m * (u32)(g.tiles_m + 1) / 2 : (u32)g.tiles_m * (u32)g.tiles_n;
   const u32 L = mx::xcd_remap(blockIdx.x, gridDim.x);
@@ -265,7 +265,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     e.cols = t.cols;
     e.vec = g.vec_c != 0;
     e.f0 = p.scale * phi;
-    gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
+    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
   } else {
     EmitNs<STEP, SPLIT> e{};
     e.ld = g.ldc;
@@ -288,7 +288,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     } else {
       e.f0 = STEP == kGram ? p.scale : p.scale * phi;
     }
-    gemm_tile<kF16, AL, BL, WI, WJ, RING, SPLIT>(g, t, smem, e);
+    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
   }
 }
 

@@ -144,14 +144,6 @@ struct GroupKernel {
   int bm, bn;
 };
 
-#ifndef MXT_BK
-#define MXT_BK 64
-#define MXT_RING 2
-#endif
-#ifndef MXT_WI
-#define MXT_WI 4
-#define MXT_WJ 4
-#endif
 template <int MODE, int AL, int BL, int WI, int WJ, int BK, int RING>
 GroupKernel group_kernel(bool f32) {
   return {f32 ? (const void *)&mxt::k_group_gemm<MODE, AL, BL, WI, WJ, BK, RING, true>
@@ -163,7 +155,7 @@ GroupKernel group_kernel(bool f32) {
 template <int MODE, int AL, int BL>
 GroupKernel group_pick(int64_t rows, int64_t N, int64_t copies, bool f32) {
   const int64_t big = (rows + 255) / 256 * ((N + 255) / 256) * copies;
-  if (big >= cu_count()) return group_kernel<MODE, AL, BL, MXT_WI, MXT_WJ, MXT_BK, MXT_RING>(f32);
+  if (big >= cu_count()) return group_kernel<MODE, AL, BL, 4, 4, 64, 2>(f32);
   return group_kernel<MODE, AL, BL, 2, 2, 64, 2>(f32);
 }
 
@@ -434,6 +426,8 @@ mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, i
   int64_t blocks;
   if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks)) return MXTRAIN_ERR_OVERFLOW;
   mxt::GemmArgs g{};
+  g.cus = cu_count();
+  if (k.bm == 256) blocks = mxt::work_items_bound(blocks, g.cus);
   g.a = static_cast<const uint16_t *>(a);
   g.b = static_cast<const uint16_t *>(b);
   g.lda = lda;
@@ -475,6 +469,8 @@ mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b,
   if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks) || __builtin_mul_overflow(blocks, G, &blocks))
     return MXTRAIN_ERR_OVERFLOW;
   mxt::GemmArgs g{};
+  g.cus = cu_count();
+  if (k.bm == 256) blocks = mxt::work_items(blocks, g.cus);
   g.a = static_cast<const uint16_t *>(a);
   g.b = static_cast<const uint16_t *>(b);
   g.lda = lda;

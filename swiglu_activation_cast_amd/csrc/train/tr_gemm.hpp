@@ -12,28 +12,37 @@
 //
 // Structure: a 64 WI x 64 WJ tile of C per workgroup of four wavefronts
 // (2 x 2, each 32 WI x 32 WJ, its sums in accumulation registers).  K is staged
-// kBK elements at a time in a ring of LDS slots that direct global -> LDS
-// loads fill ahead of use.  A stage is consumed in steps of 16 (one MFMA
-// deep): while a step's MFMAs run from registers, the next step's operands are
-// read from LDS into the other register set, and the loads of a later stage
-// are issued, one of each between two MFMAs.  The barrier of a stage sits
-// before its last step's MFMAs, whose operands are then already in registers:
-// from there the stage's slot is free to be filled again, and the MFMAs that
-// follow cover the wait.
+// BK elements at a time in a ring of LDS slots that direct global -> LDS loads
+// fill ahead of use.  A stage is consumed in steps of 32 (one MFMA deep):
+// while a step's MFMAs run from registers, the next step's operands are read
+// from LDS into the other register set, and the loads of a later stage are
+// issued, between two MFMAs each.  The barrier of a stage sits before its last
+// step's MFMAs, whose operands are then already in registers: from there the
+// stage's slot is free to be filled again, and the MFMAs that follow cover the
+// wait.  256 x 256 tiles with stages of 64 in a ring of two run fastest (8192 x
+// 8192 x 8192, both kKC: 0.75 ms, 1.47 PFLOP/s; stages of 32 in a ring of four
+// meet twice as many barriers, 8% slower; two workgroups to a CU with 128 x 256
+// or 128 x 128 tiles read more of each operand, 20-35% slower).
 //
-// LDS layouts.  kKC: rows of kBK elements (128 bytes), 16-byte chunks at
-// position chunk ^ (row / 2) % 8, so that the 16 rows that a quarter of a
+// The card runs such a product at its power limit, near 1.73 GHz, so what an
+// instruction moves counts beside what it takes: the 16x16x32 MFMA passes
+// half as many accumulator bits through the registers per product as the
+// 32x32x16 one, and is 4-6% faster here.
+//
+// LDS layouts.  kKC: rows of BK elements, 16-byte chunks at a position XORed
+// with a function of the row, so that the 16 rows that a quarter of a
 // wavefront reads at one chunk hit all banks once.  kMC: rows of the tile's
 // 64 W columns, one per k; they are read with ds_read_b64_tr_b16, which
 // hands lane i of 16 the i-th of 16 columns of four k rows (lane group of
 // four = row; checked on gfx950); the chunk position is XORed with a function
-// of k that spreads the four rows over the banks.
+// of k that spreads the eight k rows that half a wavefront reads over the
+// banks.
 //
-// MFMA operand and result layout (32x32x16): lane l holds k 8 (l / 32) .. + 7
-// of row l % 32; result register v of lane l is row 8 (v / 4) + 4 (l / 32) +
-// v % 4 of the first operand, column l % 32 the second's row.  B is passed
-// first, so that a lane holds four adjacent columns of one row of C (packed
-// for the staged store at the end).
+// MFMA operand and result layout (16x16x32): lane l holds k 8 (l / 16) .. + 7
+// of row l % 16; result register v of lane l is row 4 (l / 16) + v of the
+// first operand, column l % 16 the second's row.  B is passed first, so that a
+// lane holds four adjacent columns of one row of C (packed for the staged
+// store at the end).
 #pragma once
 #include <type_traits>
 
@@ -62,9 +71,9 @@ struct GemmArgs {
   int32_t G;                   // groups, or batch entries
   int32_t tiles_m, tiles_n;    // tiles_m: an upper bound in kGroupM
   int32_t vec_c;               // whole 16-byte chunks of C may be stored
+  int32_t cus;                 // compute units (see work_item)
 };
 
-typedef float v16f_t __attribute__((ext_vector_type(16)));
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef u32 u32x2_t __attribute__((ext_vector_type(2)));
 
@@ -110,13 +119,13 @@ __device__ __forceinline__ void wait_vm() {
 __device__ __forceinline__ u32 lds_addr(const void *p) { return (u32)(uintptr_t)(const MXT_LDS void *)p; }
 
 template <int EL>
-__device__ __forceinline__ v16f_t mfma(u32x4_t first, u32x4_t second, v16f_t c) {
+__device__ __forceinline__ f32x4_t mfma(u32x4_t first, u32x4_t second, f32x4_t c) {
   typedef __bf16 b8 __attribute__((ext_vector_type(8)));
   typedef _Float16 h8 __attribute__((ext_vector_type(8)));
   if constexpr (EL == kBf16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8, first), __builtin_bit_cast(b8, second), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8, first), __builtin_bit_cast(b8, second), c, 0, 0, 0);
   else
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8, first), __builtin_bit_cast(h8, second), c, 0, 0, 0);
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8, first), __builtin_bit_cast(h8, second), c, 0, 0, 0);
 }
 
 // One operand of a tile: W 64-row halves (64 W rows of the operand, or
@@ -125,7 +134,7 @@ __device__ __forceinline__ v16f_t mfma(u32x4_t first, u32x4_t second, v16f_t c) 
 // kilobytes of each stage.
 template <int L, int W, int BK>
 struct Operand {
-  static constexpr int kBK = BK, kKS = BK / 16;  // elements and MFMA steps of a stage
+  static constexpr int kBK = BK, kKS = BK / 32;  // elements and MFMA steps of a stage
   static constexpr int kRows = 64 * W;
   static constexpr int kBytes = kRows * kBK * 2;  // of a stage
   static constexpr int kLoads = kBytes / 1024 / 4;
@@ -140,14 +149,14 @@ struct Operand {
   u32 cur[kLoads];      // which of the two the loads use
   int k_of[kLoads];     // first k (within the stage) of what the lane loads
   u32 lds_w;            // LDS byte (within a stage's operand) of this wavefront's first load
-  u32 rd[L == kKC ? kKS : W];  // this lane's LDS read offsets
+  u32 rd[L == kKC ? kKS : 2 * W];  // this lane's LDS read offsets
 
   // XOR of the chunk position in LDS row r.
   static __device__ __forceinline__ u32 key(u32 r) {
     if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
     else if constexpr (L == kKC) return (r >> 2) & 3u;
-    else if constexpr (W == 1) return ((r >> 1) & 1u) << 2;  // 128-byte rows: two rows per turn of the banks
-    else return (r & 3u) << 2;
+    else if constexpr (W == 1) return (((r >> 1) & 1u) | ((r >> 3) & 1u) << 1) << 1;  // 128-byte rows: two per turn of the banks
+    else return ((r & 3u) | ((r >> 3) & 1u) << 2) << 1;
   }
 
   // `blk0` + x * `blk_step` is the x-th 32-row block of this wavefront.
@@ -171,17 +180,15 @@ struct Operand {
         k_of[q] = (int)r;
       }
     }
-    const u32 h = (u32)lane >> 5;
+    const u32 gq = (u32)lane >> 4, i = (u32)lane & 15u;
     if constexpr (L == kKC) {
-      const u32 r = (u32)lane & 31u;
 #pragma unroll
-      for (int s = 0; s < kKS; s++) rd[s] = ((u32)blk0 * 32u + r) * kRowB + ((((u32)(2 * s) + h) ^ key(r)) << 4);
+      for (int s = 0; s < kKS; s++) rd[s] = ((u32)blk0 * 32u + i) * kRowB + ((((u32)(4 * s) + gq) ^ key(i)) << 4);
     } else {
-      const u32 i = (u32)lane & 15u, c16 = ((u32)lane >> 4) & 1u;
-      const u32 k = 8u * h + (i >> 2);  // of a step; key(k) is the same for every step and half
+      const u32 k = 8u * gq + (i >> 2);  // of a step; key(k) is the same for every step and half
 #pragma unroll
-      for (int x = 0; x < W; x++) {
-        const u32 chunk = (u32)(blk0 + x * blk_step) * 4u + 2u * c16 + ((i & 3u) >> 1);
+      for (int x = 0; x < 2 * W; x++) {
+        const u32 chunk = (u32)(blk0 + x / 2 * blk_step) * 4u + 2u * (u32)(x & 1) + ((i & 3u) >> 1);
         rd[x] = k * kRowB + ((chunk ^ key(k)) << 4) + (i & 1u) * 8u;
       }
     }
@@ -214,15 +221,15 @@ struct Operand {
       }
     }
   }
-  static constexpr int kReads = L == kKC ? W : 2 * W;  // LDS reads of a step
+  static constexpr int kReads = L == kKC ? 2 * W : 4 * W;  // LDS reads of a step
   // Read number t of step s into the fragments.
   __device__ __forceinline__ void read(const MXT_LDS uint8_t *slot, int s, int t, int blk_step, u32x4_t *f) const {
     if constexpr (L == kKC) {
-      f[t] = *(const MXT_LDS u32x4_t *)(slot + rd[s] + (u32)(t * blk_step) * 32u * kRowB);
+      f[t] = *(const MXT_LDS u32x4_t *)(slot + rd[s] + (u32)((t / 2) * blk_step * 32 + (t & 1) * 16) * kRowB);
     } else {
       const int x = t / 2, j = t % 2;
       const u32x2_t v = __builtin_bit_cast(
-          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXT_LDS s16x4_t *)(slot + rd[x] + (u32)(16 * s + 4 * j) * kRowB)));
+          u32x2_t, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MXT_LDS s16x4_t *)(slot + rd[x] + (u32)(32 * s + 4 * j) * kRowB)));
       f[x][2 * j] = v[0];
       f[x][2 * j + 1] = v[1];
     }
@@ -244,10 +251,11 @@ template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, 
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint8_t *smem, const Emit &emit) {
   using A = Operand<AL, WI, BK>;
   using B = Operand<BL, WJ, BK>;
-  constexpr int kBK = BK, kKS = BK / 16;
+  constexpr int kBK = BK, kKS = BK / 32;
   constexpr int kSlot = A::kBytes + B::kBytes;
   constexpr int kLoads = A::kLoads + B::kLoads;
-  constexpr int kMfmas = WI * WJ;
+  constexpr int WA = 2 * WI, WB = 2 * WJ;  // 16-row blocks
+  constexpr int kMfmas = WA * WB;
   constexpr int kReads = A::kReads + B::kReads;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -259,11 +267,11 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   oa.init(t.a, g.lda, t.rows, w, lane, wm, 2);
   ob.init(t.b, g.ldb, t.cols, w, lane, WJ * wn, 1);
 
-  v16f_t acc[WI][WJ];
+  f32x4_t acc[WA][WB];
 #pragma unroll
-  for (int i = 0; i < WI; i++)
+  for (int i = 0; i < WA; i++)
 #pragma unroll
-    for (int j = 0; j < WJ; j++) acc[i][j] = v16f_t{};
+    for (int j = 0; j < WB; j++) acc[i][j] = f32x4_t{};
 
   const int per = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));  // stages of one pass over K
   const int n_stage = SPLIT ? 3 * per : per;
@@ -317,36 +325,36 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   };
 
   struct Frags {
-    u32x4_t a[WI], b[WJ];
+    u32x4_t a[WA], b[WB];
   };
   // LDS read number n of step s of the stage in `slot`: A's first block, B's
   // blocks, A's others, in the order in which the MFMAs need them.
   auto read = [&](const MXT_LDS uint8_t *slot, int s, int n, Frags &f) {
-    constexpr int a1 = A::kReads / WI;  // reads of one A block
+    constexpr int a1 = A::kReads / WA;  // reads of one A block
     if (n < a1) oa.read(slot, s, n, 2, f.a);
     else if (n < a1 + B::kReads) ob.read(slot + A::kBytes, s, n - a1, 1, f.b);
     else oa.read(slot, s, n - B::kReads, 2, f.a);
   };
   using Yes = std::true_type;
   using No = std::false_type;
-  // The stage's loads go out in its first two phases, half each.
-  constexpr int kHalf = (kLoads + 1) / 2;
-  // MFMAs of one step from `cur`, and between them the reads of step s of
-  // `slot` into `nxt` and, in phase 0 and 1 of a stage, half of its loads.
+  // MFMAs of one step from `cur`; between them the reads of step s of `slot`
+  // into `nxt`, after every other MFMA, and, where asked, all loads of a
+  // stage, spread evenly.  (Loads over the whole stage leave the last of them
+  // too little time to land, 10% slower; packed more densely they queue, 5%.)
   auto phase = [&](auto do_mfma, auto loads, const MXT_LDS uint8_t *slot, int s, Frags &cur, Frags &nxt,
                    const Src &src) {
-    constexpr int half = decltype(loads)::value;  // 0, 1, or 2: none
-    constexpr int q0 = half == 0 ? 0 : half == 1 ? kHalf : kLoads, q1 = half == 0 ? kHalf : kLoads;
+    constexpr int Q = decltype(loads)::value ? kLoads : 0;
+    constexpr int kEvery = kReads * 2 <= kMfmas ? 2 : 1, kPer = (kReads + kMfmas - 1) / kMfmas;
     static_for<kMfmas>([&](auto kk) {
-      constexpr int k = decltype(kk)::value, i = k / WJ, j = k % WJ;
+      constexpr int k = decltype(kk)::value, i = k / WB, j = k % WB;
       if constexpr (decltype(do_mfma)::value) acc[i][j] = mfma<EL>(cur.b[j], cur.a[i], acc[i][j]);
-      // reads as early as one per MFMA allows, loads spread evenly
-      constexpr int per_k = (kReads + kMfmas - 1) / kMfmas;
+      if constexpr (k % kEvery == 0) {
 #pragma unroll
-      for (int n = k * per_k; n < (k + 1) * per_k; n++)
-        if (n < kReads) read(slot, s, n, nxt);
-      static_for<(k + 1) * (q1 - q0) / kMfmas - k * (q1 - q0) / kMfmas>(
-          [&](auto q) { load(std::integral_constant<int, q0 + k * (q1 - q0) / kMfmas + decltype(q)::value>{}, src); });
+        for (int n = k / kEvery * kPer; n < (k / kEvery + 1) * kPer; n++)
+          if (n < kReads) read(slot, s, n, nxt);
+      }
+      static_for<(k + 1) * Q / kMfmas - k * Q / kMfmas>(
+          [&](auto q) { load(std::integral_constant<int, k * Q / kMfmas + decltype(q)::value>{}, src); });
       __builtin_amdgcn_sched_barrier(0);  // keep this order
     });
   };
@@ -361,26 +369,23 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     constexpr bool first = !decltype(has_last)::value;
     // the loads of the stage that takes over stage st - 1's slot
     const Src src = first ? Src{} : source(st - 1 + RING);
-    using L0 = std::integral_constant<int, first ? 2 : 0>;
-    using L1 = std::integral_constant<int, first ? 2 : 1>;
-    using None = std::integral_constant<int, 2>;
-    phase(has_last, L0{}, slot, 0, f1, f0, src);
-    phase(Yes{}, L1{}, slot, 1, f0, f1, src);
+    phase(has_last, std::integral_constant<bool, !first>{}, slot, 0, f1, f0, src);
+    phase(Yes{}, No{}, slot, 1, f0, f1, src);
 #pragma unroll
     for (int s = 2; s < kKS; s += 2) {
-      phase(Yes{}, None{}, slot, s, f1, f0, src);
-      phase(Yes{}, None{}, slot, s + 1, f0, f1, src);
+      phase(Yes{}, No{}, slot, s, f1, f0, src);
+      phase(Yes{}, No{}, slot, s + 1, f0, f1, src);
     }
 #if __HIP_DEVICE_COMPILE__
     // keep this stage's results in its block
 #pragma unroll
-    for (int i = 0; i < WI; i++) {
+    for (int i = 0; i < WA; i++) {
 #pragma unroll
-      for (int j = 0; j < WJ; j++) asm volatile("" ::"a"(acc[i][j]));
+      for (int j = 0; j < WB; j++) asm volatile("" ::"a"(acc[i][j]));
       asm volatile("" ::"v"(f1.a[i]));
     }
 #pragma unroll
-    for (int j = 0; j < WJ; j++) asm volatile("" ::"v"(f1.b[j]));
+    for (int j = 0; j < WB; j++) asm volatile("" ::"v"(f1.b[j]));
 #endif
     // issued so far: stages up to st - 1 + RING
     wait_vm<(RING - 2) * kLoads>();
@@ -400,7 +405,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     stage(No{}, 0);
     for (int st = 1; st < n_stage; st++) stage(Yes{}, st);
 #pragma unroll
-    for (int k = 0; k < kMfmas; k++) acc[k / WJ][k % WJ] = mfma<EL>(f1.b[k % WJ], f1.a[k / WJ], acc[k / WJ][k % WJ]);
+    for (int k = 0; k < kMfmas; k++) acc[k / WB][k % WB] = mfma<EL>(f1.b[k % WB], f1.a[k / WB], acc[k / WB][k % WB]);
     wait_vm<0>();  // nothing may still be landing in LDS when the workgroup ends or goes on
   }
 
@@ -416,7 +421,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   static_assert(4 * Emit::kPlanes * kPlane <= RING * kSlot, "the staged blocks fit the slots");
   MXT_LDS uint8_t *mine = lds + w * (Emit::kPlanes * kPlane);
   auto chunk_at = [&](u32 row, u32 c) { return row * kRow + ((c ^ ((row / kTurn) & (kChunks - 1))) << 4); };
-  const u32 h = (u32)lane >> 5, r = (u32)lane & 31u;
+  const u32 h = (u32)lane >> 4, r16 = (u32)lane & 15u;
   const u32 nw = 32u * (u32)(WJ * wn);  // the wavefront's first column
 #pragma unroll
   for (int i = 0; i < WI; i++) {
@@ -424,11 +429,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     if (mb >= t.rows) break;  // uniform
     asm volatile("" ::: "memory");
 #pragma unroll
-    for (int j = 0; j < WJ; j++)
+    for (int j = 0; j < WB; j++)
 #pragma unroll
-      for (int q = 0; q < 4; q++) {
-        const f32x4_t v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
-        const u32 n = 32u * (u32)j + 8u * (u32)q + 4u * h;
+      for (int q = 0; q < 2; q++) {
+        const f32x4_t v = acc[2 * i + q][j];
+        const u32 r = r16 + 16u * (u32)q;
+        const u32 n = 16u * (u32)j + 4u * h;
         if constexpr (Emit::kF32) {
           *(MXT_LDS f32x4_t *)(mine + chunk_at(r, n / 4)) = emit.map(mb + r, nw + n, v);
         } else {
@@ -576,19 +582,56 @@ __device__ __forceinline__ void tile_of(u32 L, u32 tiles_m, u32 tiles_n, u32 &tm
   tn = in / rows;
 }
 
+// A launch of R tiles of 256 x 256, one to a CU at a time, runs in rounds of
+// `cus`.  If the tiles of a last partial round would leave at least half of
+// the CUs idle, they run as 256 x 128 halves, if at least three quarters, as
+// 256 x 64 quarters, so that the round ends in a little over half (a quarter)
+// of the time.  item -> tile index, and which of its `parts`; false: no work.
+struct Item {
+  u32 L, part, parts;
+};
+__device__ __forceinline__ bool work_item(u32 b, u32 R, u32 cus, Item &it) {
+  const u32 tail = R % cus, R0 = R - tail;
+  it.parts = 1;
+  it.part = 0;
+  if (b < R0) {
+    it.L = b;
+    return true;
+  }
+  it.parts = tail <= cus / 4 ? 4u : tail <= cus / 2 ? 2u : 1u;
+  it.L = R0 + (b - R0) / it.parts;
+  it.part = (b - R0) % it.parts;
+  return it.L < R;
+}
+// Work items of R tiles, and an upper bound over all R' <= R.
+inline int64_t work_items(int64_t R, int64_t cus) {
+  const int64_t tail = R % cus;
+  return R + (tail <= cus / 4 ? 3 * tail : tail <= cus / 2 ? tail : 0);
+}
+inline int64_t work_items_bound(int64_t R, int64_t cus) {
+  const int64_t extra = 3 * (cus / 4) > cus / 2 ? 3 * (cus / 4) : cus / 2;
+  return R + extra;
+}
+
+// WI = WJ = 4: 256 x 256 tiles, short ones (a group's last rows) and those of a
+// last partial round cut down; WI = WJ = 2: 128 x 128 tiles, two workgroups to
+// a CU.
 template <int MODE, int AL, int BL, int WI, int WJ, int BK, int RING, bool F32>
 __global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(const GemmArgs g) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
+  constexpr bool kBig = WI == 4 && WJ == 4;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * 2];
   Tile t{};
   u32 tm, tn;
+  Item it{blockIdx.x, 0, 1};
   EmitC<F32> emit{g.c, g.ldc, 0, g.vec_c != 0};
   if constexpr (MODE == kGroupM) {
     // the real number of tile rows first, then this workgroup's tile
-    const int64_t total = find_tile<BM>(g.ends, g.G, g.M, INT64_MAX).total;
-    const u32 R = (u32)total * (u32)g.tiles_n;
-    if (blockIdx.x >= R) return;
-    tile_of(mx::xcd_remap(blockIdx.x, R), (u32)total, (u32)g.tiles_n, tm, tn);
+    const u32 total = (u32)find_tile<BM>(g.ends, g.G, g.M, INT64_MAX).total;
+    const u32 R = total * (u32)g.tiles_n;
+    if (kBig ? !work_item(blockIdx.x, R, (u32)g.cus, it) : blockIdx.x >= R) return;
+    const u32 whole = kBig ? R - R % (u32)g.cus : R;
+    tile_of(it.L < whole ? mx::xcd_remap(it.L, whole) : it.L, total, (u32)g.tiles_n, tm, tn);
     const GroupTile gt = find_tile<BM>(g.ends, g.G, g.M, tm);
     t.a = g.a + gt.m0 * g.lda;
     t.b = g.b + (int64_t)gt.group * g.stride_b;
@@ -596,10 +639,12 @@ __global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(co
     t.k_len = g.K;
     emit.c = F32 ? (void *)(static_cast<float *>(g.c) + gt.m0 * g.ldc) : (void *)(static_cast<uint16_t *>(g.c) + gt.m0 * g.ldc);
   } else {
-    const u32 R = (u32)g.tiles_m * (u32)g.tiles_n;
-    const u32 L = mx::xcd_remap(blockIdx.x, R * (u32)g.G);
-    const int32_t grp = (int32_t)(L / R);
-    tile_of(L % R, (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
+    // the groups one after another, each dealt to the XCDs in eighths: their
+    // depths differ, and a group to an XCD would leave the others waiting
+    const u32 per = (u32)g.tiles_m * (u32)g.tiles_n;
+    if (kBig && !work_item(blockIdx.x, per * (u32)g.G, (u32)g.cus, it)) return;
+    const int32_t grp = (int32_t)(it.L / per);
+    tile_of(mx::xcd_remap(it.L % per, per), (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
     int64_t start, end;
     find_group(g.ends, grp, g.K, start, end);
     const int64_t m0 = (int64_t)tm * BM;
@@ -610,11 +655,20 @@ __global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(co
     const int64_t at = (int64_t)grp * g.stride_c + m0 * g.ldc;
     emit.c = F32 ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
   }
-  const int64_t n0 = (int64_t)tn * BN;
+  const int64_t n0 = (int64_t)tn * BN + it.part * (BN / it.parts);
+  if (n0 >= g.N) return;  // a part past the last column
   t.b += BL == kKC ? n0 * g.ldb : n0;
-  t.cols = emit.cols = (u32)min<int64_t>(BN, g.N - n0);
+  t.cols = emit.cols = (u32)min<int64_t>(BN / it.parts, g.N - n0);
   emit.c = F32 ? (void *)(static_cast<float *>(emit.c) + n0) : (void *)(static_cast<uint16_t *>(emit.c) + n0);
-  gemm_tile<kBf16, AL, BL, WI, WJ, BK, RING, false>(g, t, smem, emit);
+  if constexpr (kBig) {
+    if (it.parts == 4) gemm_tile<kBf16, AL, BL, WI, 1, BK, RING, false>(g, t, smem, emit);
+    else if (it.parts == 2) gemm_tile<kBf16, AL, BL, WI, 2, BK, RING, false>(g, t, smem, emit);
+    else if (t.rows <= 64) gemm_tile<kBf16, AL, BL, 1, WJ, BK, RING, false>(g, t, smem, emit);
+    else if (t.rows <= 128) gemm_tile<kBf16, AL, BL, 2, WJ, BK, RING, false>(g, t, smem, emit);
+    else gemm_tile<kBf16, AL, BL, WI, WJ, BK, RING, false>(g, t, smem, emit);
+  } else {
+    gemm_tile<kBf16, AL, BL, WI, WJ, BK, RING, false>(g, t, smem, emit);
+  }
 }
 
 }  // namespace mxt

@@ -15,6 +15,7 @@ the current one it is recorded there, so that it is not reused too early.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -76,10 +77,15 @@ def train_status_str(status: int) -> str:
     return train_lib().mxtrain_status_str(int(status)).decode()
 
 
+@functools.lru_cache(maxsize=None)
+def _entry(name: str):
+    return getattr(train_lib(), name)
+
+
 def _call(name: str, device: torch.device, *args) -> None:
     """The C call with `device` current; raises on a status."""
-    fn = getattr(train_lib(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
+    fn = _entry(name)
+    if device.index == torch.cuda.current_device():
         status = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -88,10 +94,20 @@ def _call(name: str, device: torch.device, *args) -> None:
         raise MxtrainError(name, status, train_status_str(status))
 
 
+# The current stream's handle without building a torch Stream object around
+# it: 0.1 us of a small call's 10, against 1.9.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_of(device: torch.device, stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
+        return _raw_stream(device.index) if _raw_stream else torch.cuda.current_stream(device).cuda_stream
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name: str, *sizes) -> int:
+    return _entry(name)(*sizes)
 
 
 def _workspace(nbytes: int, given: Optional[torch.Tensor], device: torch.device, stream) -> torch.Tensor:
@@ -111,6 +127,9 @@ def _workspace(nbytes: int, given: Optional[torch.Tensor], device: torch.device,
 
 
 def _gpu(t, name: str, dtypes, dim: int, device=None) -> torch.Tensor:
+    if (isinstance(t, torch.Tensor) and t.dtype in dtypes and t.is_cuda and t.dim() == dim
+            and (device is None or t.device == device)):
+        return t
     if not isinstance(t, torch.Tensor) or t.dtype not in dtypes:
         want = " or ".join(str(d).replace("torch.", "") for d in dtypes)
         raise TypeError(f"{name} must be a {want} tensor, got {getattr(t, 'dtype', type(t).__name__)}")
@@ -118,37 +137,47 @@ def _gpu(t, name: str, dtypes, dim: int, device=None) -> torch.Tensor:
         raise ValueError(f"{name} must be a GPU tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must be {dim}-D, got shape {tuple(t.shape)}")
-    return t
+    raise ValueError(f"{name} must be {dim}-D, got shape {tuple(t.shape)}")
 
 
 def _ld(t: torch.Tensor, name: str) -> int:
     """Row stride of the last two dimensions, whose columns must be adjacent."""
     rows, cols = t.shape[-2:]
+    if t.is_contiguous():
+        return cols
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     return t.stride(-2) if rows > 1 else max(t.stride(-2), cols)
 
 
-def _param(t: Optional[torch.Tensor], name: str, n: int, device, dtype=None):
+def _vector(t: Optional[torch.Tensor], name: str, n: int, device, dtypes) -> Optional[int]:
+    """Address of n adjacent elements, or None."""
     if t is None:
         return None
-    _gpu(t, name, (torch.bfloat16, torch.float32) if dtype is None else (dtype,), 1, device)
-    if t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name} must hold {n} adjacent elements")
-    return t.data_ptr()
+    if t.dtype in dtypes and t.device == device and t.shape == (n,) and t.is_contiguous():
+        return t.data_ptr()
+    _gpu(t, name, dtypes, 1, device)
+    raise ValueError(f"{name} must hold {n} adjacent elements")
 
 
 def _out(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
     _gpu(t, name, (dtype,), len(shape), device)
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
+def _f32_out(t: Optional[torch.Tensor], name: str, n: int, device) -> Tuple[torch.Tensor, int]:
+    """An fp32 vector of n elements, given or new, and its address."""
+    if t is None:
+        t = torch.empty(n, dtype=torch.float32, device=device)
+        return t, t.data_ptr()
+    return t, _vector(t, name, n, device, _F32)
+
+
+_F32 = (torch.float32,)
 _FLOATS = (torch.bfloat16, torch.float32)
 
 
@@ -167,14 +196,14 @@ def mxtrain_layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     dev = x.device
     if weight is not None and bias is not None and weight.dtype != bias.dtype:
         raise TypeError("weight and bias must have the same dtype")
-    pw, pb = _param(weight, "weight", N, dev), _param(bias, "bias", N, dev)
+    pw, pb = _vector(weight, "weight", N, dev, _FLOATS), _vector(bias, "bias", N, dev, _FLOATS)
     param = weight if weight is not None else bias
-    y = _out(out, "out", (M, N), x.dtype, dev)
-    mean = _out(mean, "mean", (M,), torch.float32, dev)
-    rstd = _out(rstd, "rstd", (M,), torch.float32, dev)
+    y = _out(out, "out", x.shape, x.dtype, dev)
+    mean, pm = _f32_out(mean, "mean", M, dev)
+    rstd, pr = _f32_out(rstd, "rstd", M, dev)
     _call("mxtrain_layer_norm_fwd", dev, x.data_ptr(), _ld(x, "x"), pw, pb,
-          _TYPES[param.dtype] if param is not None else 0, M, N, _TYPES[x.dtype], eps, y.data_ptr(), _ld(y, "out"),
-          _param(mean, "mean", M, dev), _param(rstd, "rstd", M, dev), _stream_of(dev, stream))
+          0 if param is None else _TYPES[param.dtype], M, N, _TYPES[x.dtype], eps, y.data_ptr(), _ld(y, "out"),
+          pm, pr, _stream_of(dev, stream))
     return y, mean, rstd
 
 
@@ -192,17 +221,15 @@ def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     _gpu(dy, "dy", (x.dtype,), 2, dev)
     if dy.shape != x.shape:
         raise ValueError("dy and x must have the same shape")
-    pw = _param(weight, "weight", N, dev)
-    pm, pr = _param(mean, "mean", M, dev, torch.float32), _param(rstd, "rstd", M, dev, torch.float32)
-    dx = _out(out, "out", (M, N), x.dtype, dev)
-    dw = _out(dweight, "dweight", (N,), torch.float32, dev)
-    db = _out(dbias, "dbias", (N,), torch.float32, dev)
-    nbytes = train_lib().mxtrain_layer_norm_bwd_workspace(M, N)
-    ws = _workspace(nbytes, workspace, dev, stream)
+    pw = _vector(weight, "weight", N, dev, _FLOATS)
+    pm, pr = _vector(mean, "mean", M, dev, _F32), _vector(rstd, "rstd", M, dev, _F32)
+    dx = _out(out, "out", x.shape, x.dtype, dev)
+    dw, pdw = _f32_out(dweight, "dweight", N, dev)
+    db, pdb = _f32_out(dbias, "dbias", N, dev)
+    ws = _workspace(_workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N), workspace, dev, stream)
     _call("mxtrain_layer_norm_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), pm, pr, pw,
-          _TYPES[weight.dtype] if weight is not None else 0, M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
-          _param(dw, "dweight", N, dev), _param(db, "dbias", N, dev), ws.data_ptr(),
-          ws.numel() * ws.element_size(), _stream_of(dev, stream))
+          0 if weight is None else _TYPES[weight.dtype], M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
+          pdw, pdb, ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev, stream))
     return dx, dw, db
 
 
@@ -289,7 +316,7 @@ def mxtrain_newton_schulz(g: torch.Tensor, *, steps: int = 5,
     several = g.dim() == 3 and batch > 1
     stride_g = g.stride(0) if several else 0
     stride_c = c.stride(0) if several else 0
-    nbytes = train_lib().mxtrain_newton_schulz_workspace(batch, m, n, _TYPES[c.dtype])
+    nbytes = _workspace_bytes("mxtrain_newton_schulz_workspace", batch, m, n, _TYPES[c.dtype])
     ws = _workspace(nbytes, workspace, dev, stream)
     _call("mxtrain_newton_schulz", dev, g.data_ptr(), ld_g, stride_g, _TYPES[g.dtype], batch, m, n, int(steps),
           (ctypes.c_float * 3)(*coeffs), eps, c.data_ptr(), ld_c, stride_c, _TYPES[c.dtype], ws.data_ptr(),

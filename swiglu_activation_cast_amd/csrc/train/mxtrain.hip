@@ -44,30 +44,34 @@ struct RowPlan {
 };
 
 // Short rows share a workgroup of 256 threads (16 or 64 threads a row); a
-// longer one has a workgroup of just the wavefronts it needs.  With many rows
-// a thread holds as many elements as keep the workgroup at 256 threads (fewer
-// threads to join per row, the other workgroups of the CU hide the waits);
-// with few rows, where one row's latency is the time, as few as 1024 threads
-// allow.
+// longer one has a workgroup of just the wavefronts it needs.  In the forward
+// pass over many rows a thread holds as many elements as keep the workgroup at
+// 256 threads (fewer threads to join per row, the other workgroups of the CU
+// hide the waits); with few rows, where one row's latency is the time, and in
+// the backward pass, whose threads hold five values an element, as few as 1024
+// threads allow.
 RowPlan row_plan(int64_t M, int64_t N, int vec, bool bwd) {
   const bool many = M >= 1024;
   if (many && N <= 128) return {16, 256, 8};
   if (N <= 512) return {64, 256, 8};
   if (many && N <= 1024) return {64, 256, 16};
-  const int most32 = bwd ? 512 : 1024;  // threads of a workgroup whose threads hold 32 elements
-  const int cap = many ? 256 : 1024;
+  const int cap = many && !bwd ? 256 : 1024;
   const int64_t chunks = (N + vec - 1) / vec;
   for (int pass = 0; pass < 2; pass++)
     for (int e = 8; e <= 32; e *= 2) {
+      if (bwd && vec == 1 && e == 32) continue;  // more registers than a thread has
+      const int most = !bwd || (e == 8 && vec > 1) ? 1024 : 512;  // kLnBwdThreads
       const int64_t per = e / vec, need = (chunks + per - 1) / per;
       const int64_t t = (need + 63) / 64 * 64;
-      if (t <= std::min(pass == 0 ? cap : 1024, e == 32 ? most32 : 1024)) return {0, (int)t, e};
+      if (t <= std::min(pass == 0 ? cap : 1024, most)) return {0, (int)t, e};
     }
   return {0, 1024, 0};
 }
 
 // Workgroups of the backward pass, each of which leaves one partial row of
-// 2 N sums: at most 512 (two per CU), and at least four rows each.
+// 2 N sums, of at least four rows each: 512, or 256 where a workgroup has 512
+// threads or more (bf16, 16384 rows: of 5120 columns 94 us with 256 workgroups
+// and 105 with 512, of 2048 columns 70 and 47).
 constexpr int64_t kLnParts = 512;
 int64_t ln_parts(int64_t M) { return std::min<int64_t>(kLnParts, (M + 3) / 4); }
 
@@ -81,9 +85,10 @@ template <class T, int VEC, bool BWD>
 const void *ln_kernel(const RowPlan &p) {
   if (p.tpr == 16) return ln_pick<T, VEC, 16, 8, BWD>();
   if (p.tpr == 64) return p.elems == 8 ? ln_pick<T, VEC, 64, 8, BWD>() : ln_pick<T, VEC, 64, 16, BWD>();
-  return p.elems == 8    ? ln_pick<T, VEC, 0, 8, BWD>()
-         : p.elems == 16 ? ln_pick<T, VEC, 0, 16, BWD>()
-                         : ln_pick<T, VEC, 0, 32, BWD>();
+  if (p.elems == 8) return ln_pick<T, VEC, 0, 8, BWD>();
+  if (p.elems == 16) return ln_pick<T, VEC, 0, 16, BWD>();
+  if constexpr (BWD && VEC == 1) return nullptr;  // not planned
+  else return ln_pick<T, VEC, 0, 32, BWD>();
 }
 
 template <bool BWD>
@@ -382,6 +387,7 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
     g.w_f32 = param_dtype == MXTRAIN_F32;
     const int64_t slots = p.tpr ? 256 / p.tpr : 1;
     parts = std::min<int64_t>(ln_parts(M), (M + slots - 1) / slots);
+    if (p.threads >= 512) parts = std::min<int64_t>(parts, kLnParts / 2);
     const unsigned joined = p.tpr ? (unsigned)(slots * 2 * N * (int64_t)sizeof(float)) : 0u;
     const mxtrain_status run = launch(ln_kernel<true>(p, dtype, vec), parts, p.threads, g, stream, joined);
     if (run != MXTRAIN_OK) return run;

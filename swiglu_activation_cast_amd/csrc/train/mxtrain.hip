@@ -35,6 +35,16 @@ mxtrain_status launch(const void *kernel, int64_t blocks, int threads, const Arg
   return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;
 }
 
+// Compute units of the current device (it decides tile sizes, no result
+// depends on it).
+int cu_count() {
+  int dev = 0, cus = 0;
+  if (hipGetDevice(&dev) != hipSuccess ||
+      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1)
+    return 256;
+  return cus;
+}
+
 // ------------------------------------------------------------- layer norm
 // How a row is spread over threads: `tpr` threads (0: a whole workgroup of
 // `threads`) holding `elems` elements each; elems == 0: the row does not fit
@@ -44,23 +54,24 @@ struct RowPlan {
 };
 
 // Short rows share a workgroup of 256 threads (16 or 64 threads a row); a
-// longer one has a workgroup of just the wavefronts it needs.  In the forward
-// pass over many rows a thread holds as many elements as keep the workgroup at
-// 256 threads (fewer threads to join per row, the other workgroups of the CU
-// hide the waits); with few rows, where one row's latency is the time, and in
-// the backward pass, whose threads hold five values an element, as few as 1024
-// threads allow.
+// longer one has a workgroup of just the wavefronts it needs, with 8 elements a
+// thread as long as 1024 threads suffice.  The forward pass over many rows
+// prefers 16 elements to more than 512 threads, whose joining costs more than
+// it hides (16384 x 8192 bf16: 96 us against 127); the backward pass does not
+// (its threads hold five values an element), nor do rows moved by element
+// (4096 x 4099: 28 us against 45).
 RowPlan row_plan(int64_t M, int64_t N, int vec, bool bwd) {
   const bool many = M >= 1024;
   if (many && N <= 128) return {16, 256, 8};
   if (N <= 512) return {64, 256, 8};
   if (many && N <= 1024) return {64, 256, 16};
-  const int cap = many && !bwd ? 256 : 1024;
+    const int cap = many && !bwd && vec > 1 ? 512 : 1024;
   const int64_t chunks = (N + vec - 1) / vec;
   for (int pass = 0; pass < 2; pass++)
     for (int e = 8; e <= 32; e *= 2) {
       if (bwd && vec == 1 && e == 32) continue;  // more registers than a thread has
-      const int most = !bwd || (e == 8 && vec > 1) ? 1024 : 512;  // kLnBwdThreads
+      // the kernels' launch bounds
+      const int most = bwd ? (e == 8 && vec > 1 ? 1024 : 512) : e <= 16 ? 1024 : 512;
       const int64_t per = e / vec, need = (chunks + per - 1) / per;
       const int64_t t = (need + 63) / 64 * 64;
       if (t <= std::min(pass == 0 ? cap : 1024, most)) return {0, (int)t, e};
@@ -133,16 +144,6 @@ bool ln_vec(const void *const *mats, const int64_t *lds, int n, int64_t N, int d
 
 // -------------------------------------------------- the experts' products
 constexpr int64_t kMaxGroups = 65535;
-
-// Compute units of the current device (it decides tile sizes, no result
-// depends on it).
-int cu_count() {
-  int dev = 0, cus = 0;
-  if (hipGetDevice(&dev) != hipSuccess ||
-      hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1)
-    return 256;
-  return cus;
-}
 
 struct GroupKernel {
   const void *k;
@@ -341,9 +342,17 @@ mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *w
   g.M = M;
   g.N = (int32_t)N;
   g.w_f32 = param_dtype == MXTRAIN_F32;
+  g.p_vec = aligned(weight, 16) && aligned(bias, 16);
   g.eps = eps;
   const int64_t rows = p.tpr ? 256 / p.tpr : 1;
-  return launch(ln_kernel<false>(p, dtype, vec), (M + rows - 1) / rows, p.threads, g, stream);
+  // As many workgroups as the CUs hold at once by their registers, each of
+  // which then walks rows: 16 or 32 elements a thread leave room for 1024
+  // threads to a CU, 8 for 1536 or, moved as vectors, 2048 (16384 x 5120 bf16:
+  // 63 us with 1024 threads to a CU, 81 with 1280, more than fit evenly; 16384 x
+  // 2048 27 us with 2048, 33 with 1024).
+  const int per_cu = p.elems > 8 ? 1024 : vec ? 2048 : 1536;
+  const int64_t most = p.elems ? cu_count() * std::max<int64_t>(1, per_cu / p.threads) : M;
+  return launch(ln_kernel<false>(p, dtype, vec), std::min((M + rows - 1) / rows, most), p.threads, g, stream);
 }
 
 int64_t mxtrain_layer_norm_bwd_workspace(int64_t M, int64_t N) {
@@ -385,6 +394,7 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
     g.M = M;
     g.N = (int32_t)N;
     g.w_f32 = param_dtype == MXTRAIN_F32;
+    g.p_vec = aligned(weight, 16);
     const int64_t slots = p.tpr ? 256 / p.tpr : 1;
     parts = std::min<int64_t>(ln_parts(M), (M + slots - 1) / slots);
     if (p.threads >= 512) parts = std::min<int64_t>(parts, kLnParts / 2);

@@ -143,8 +143,6 @@ def _gpu(t, name: str, dtypes, dim: int, device=None) -> torch.Tensor:
 def _ld(t: torch.Tensor, name: str) -> int:
     """Row stride of the last two dimensions, whose columns must be adjacent."""
     rows, cols = t.shape[-2:]
-    if t.is_contiguous():
-        return cols
     if cols > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     return t.stride(-2) if rows > 1 else max(t.stride(-2), cols)

@@ -228,9 +228,9 @@ mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
   const int64_t b = tiles(256) >= cus ? 256 : tiles(128) >= cus / 2 ? 128 : 64;
   p.g.tiles_m = (int32_t)((p.g.M + b - 1) / b);
   p.g.tiles_n = (int32_t)((p.g.N + b - 1) / b);
-  const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, 64, 2, SPLIT>
-                  : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, 64, 2, SPLIT>
-                             : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 64, 4, SPLIT>;
+  const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, SPLIT ? 32 : 64, 2, SPLIT>
+                  : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, SPLIT ? 32 : 64, 2, SPLIT>
+                             : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 64, SPLIT ? 4 : 8, SPLIT>;
   return launch(k, tiles(b), mxt::kThreads, p, stream);
 }
 

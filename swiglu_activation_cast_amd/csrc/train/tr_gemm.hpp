@@ -200,10 +200,11 @@ struct Operand {
 #pragma unroll
     for (int q = 0; q < kLoads; q++) cur[q] = k_of[q] < kmax ? off[q] : tail[q];
   }
-  // Load number Q of the stage at `src`; `slot`: this wavefront's first byte.
-  template <int Q>
+  // Load number Q of the stage at `src`, AT bytes past `slot`, this wavefront's
+  // first byte.
+  template <int Q, int AT>
   __device__ __forceinline__ void load(const uint8_t *src, u32 slot) const {
-    dma16<Q * 1024>(src, cur[Q], slot);
+    dma16<AT + Q * 1024>(src, cur[Q], slot);
   }
   // This lane's part of a landed stage, k >= kmax -> 0.
   __device__ __forceinline__ void clear(MXT_LDS uint8_t *slot, int lane, int kmax) const {
@@ -236,10 +237,9 @@ struct Operand {
   }
 };
 
-// What a tile's workgroup computes: rows [m0, m0 + rows) x columns [n0, n0 +
-// cols) of matrix `entry`, over `k_len` of K from the operands' bases.  With
-// SPLIT, A and B each come as a high and a low plane and the sum runs over
-// high x low, low x high and high x high.
+// What a tile's workgroup computes: `rows` x `cols` of C over `k_len` of K from
+// the operands' bases.  With SPLIT, A and B each come as a high and a low plane
+// and the sum runs over high x low, high x high and low x high.
 struct Tile {
   const uint16_t *a, *b;        // at the tile's first row (column) and k
   const uint16_t *a_lo, *b_lo;  // SPLIT
@@ -251,12 +251,13 @@ template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, 
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint8_t *smem, const Emit &emit) {
   using A = Operand<AL, WI, BK>;
   using B = Operand<BL, WJ, BK>;
-  constexpr int kBK = BK, kKS = BK / 32;
-  constexpr int kSlot = A::kBytes + B::kBytes;
-  constexpr int kLoads = A::kLoads + B::kLoads;
+  constexpr int kBK = BK, kKS = BK / 32, kPl = SPLIT ? 2 : 1;
+  // a slot: A's planes, then B's
+  constexpr int kSlotB = kPl * A::kBytes, kSlot = kSlotB + kPl * B::kBytes;
+  constexpr int kLoads = kPl * (A::kLoads + B::kLoads);
+  static_assert((RING - 1) * kLoads < 64, "the count that wait_vm can hold");
   constexpr int WA = 2 * WI, WB = 2 * WJ;  // 16-row blocks
   constexpr int kMfmas = WA * WB;
-  constexpr int kReads = A::kReads + B::kReads;
   const int lane = threadIdx.x & 63;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w >> 1, wn = w & 1;
@@ -273,9 +274,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
 #pragma unroll
     for (int j = 0; j < WB; j++) acc[i][j] = f32x4_t{};
 
-  const int per = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));  // stages of one pass over K
-  const int n_stage = SPLIT ? 3 * per : per;
-  const int k_tail = (int)(t.k_len - (int64_t)(per - 1) * kBK);  // k in the last stage of a pass, 1 .. kBK
+  const int n_stage = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));
+  const int k_tail = (int)(t.k_len - (int64_t)(n_stage - 1) * kBK);  // k in the last stage, 1 .. kBK
   MXT_LDS uint8_t *lds = (MXT_LDS uint8_t *)smem;
   const u32 lds0 = lds_addr(smem);
 
@@ -285,26 +285,24 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     b_lo = uniform(reinterpret_cast<const uint8_t *>(t.b_lo));
   }
   struct Src {
-    const uint8_t *a, *b;
-    u32 slot_a, slot_b;
+    const uint8_t *a[2], *b[2];  // the stage in each plane
+    u32 slot_a, slot_b;          // where this wavefront's first load of an operand lands
   };
   int kmax = kBK;  // of the stages being loaded
   oa.set_kmax(kmax);
   ob.set_kmax(kmax);
   // Stages past the last re-read it into a slot that is not read again.
   auto source = [&](int st) {
-    int s = min(st, n_stage - 1), pass = 0;
-    if constexpr (SPLIT) {
-      pass = s / per;
-      s -= pass * per;
-    }
+    const int s = min(st, n_stage - 1);
     Src r;
-    r.a = (SPLIT && pass == 1 ? a_lo : oa.base) + s * oa.step;
-    r.b = (SPLIT && pass == 0 ? b_lo : ob.base) + s * ob.step;
+    r.a[0] = oa.base + s * oa.step;
+    r.b[0] = ob.base + s * ob.step;
+    r.a[1] = SPLIT ? a_lo + s * oa.step : nullptr;
+    r.b[1] = SPLIT ? b_lo + s * ob.step : nullptr;
     r.slot_a = lds0 + (u32)(st % RING) * kSlot + oa.lds_w;
-    r.slot_b = lds0 + (u32)(st % RING) * kSlot + A::kBytes + ob.lds_w;
-    const int k = s == per - 1 ? k_tail : kBK;
-    if (k != kmax) {  // uniform; once per pass over K, if K has a partial stage
+    r.slot_b = lds0 + (u32)(st % RING) * kSlot + kSlotB + ob.lds_w;
+    const int k = s == n_stage - 1 ? k_tail : kBK;
+    if (k != kmax) {  // uniform; once, if the last stage is a partial one
       kmax = k;
       oa.set_kmax(k);
       ob.set_kmax(k);
@@ -312,69 +310,86 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     return r;
   };
   auto load = [&](auto q, const Src &r) {
-    constexpr int Q = decltype(q)::value;
-    if constexpr (Q < A::kLoads) oa.template load<Q>(r.a, r.slot_a);
-    else ob.template load<Q - A::kLoads>(r.b, r.slot_b);
+    constexpr int Q = decltype(q)::value, P = Q / (A::kLoads + B::kLoads), R = Q % (A::kLoads + B::kLoads);
+    if constexpr (R < A::kLoads) oa.template load<R, P * A::kBytes>(r.a[P], r.slot_a);
+    else ob.template load<R - A::kLoads, P * B::kBytes>(r.b[P], r.slot_b);
   };
   // Stage st has landed: clear what lies past K (each lane what it loaded).
   auto clear = [&](int st) {
-    if (k_tail == kBK || st >= n_stage || (SPLIT ? (st + 1) % per : st + 1 - per) != 0) return;
+    if (k_tail == kBK || st != n_stage - 1) return;
     MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
-    oa.clear(slot, lane, k_tail);
-    ob.clear(slot + A::kBytes, lane, k_tail);
+#pragma unroll
+    for (int p = 0; p < kPl; p++) {
+      oa.clear(slot + p * A::kBytes, lane, k_tail);
+      ob.clear(slot + kSlotB + p * B::kBytes, lane, k_tail);
+    }
   };
 
-  struct Frags {
-    u32x4_t a[WA], b[WB];
-  };
-  // LDS read number n of step s of the stage in `slot`: A's first block, B's
-  // blocks, A's others, in the order in which the MFMAs need them.
-  auto read = [&](const MXT_LDS uint8_t *slot, int s, int n, Frags &f) {
-    constexpr int a1 = A::kReads / WA;  // reads of one A block
-    if (n < a1) oa.read(slot, s, n, 2, f.a);
-    else if (n < a1 + B::kReads) ob.read(slot + A::kBytes, s, n - a1, 1, f.b);
-    else oa.read(slot, s, n - B::kReads, 2, f.a);
-  };
   using Yes = std::true_type;
   using No = std::false_type;
-  // MFMAs of one step from `cur`; between them the reads of step s of `slot`
-  // into `nxt`, after every other MFMA, and, where asked, all loads of a
-  // stage, spread evenly.  (Loads over the whole stage leave the last of them
-  // too little time to land, 10% slower; packed more densely they queue, 5%.)
-  auto phase = [&](auto do_mfma, auto loads, const MXT_LDS uint8_t *slot, int s, Frags &cur, Frags &nxt,
-                   const Src &src) {
-    constexpr int Q = decltype(loads)::value ? kLoads : 0;
-    constexpr int kEvery = kReads * 2 <= kMfmas ? 2 : 1, kPer = (kReads + kMfmas - 1) / kMfmas;
+  // MFMAs of one step, a times b; between them `n_reads` LDS reads, after every
+  // other MFMA while there are enough, and, where asked, all loads of a stage,
+  // spread evenly.  (Loads over the whole stage leave the last of them too
+  // little time to land, 10% slower; packed more densely they queue, 5%.)
+  auto phase = [&](auto do_mfma, auto loads, auto n_reads, u32x4_t *fa, u32x4_t *fb, const Src &src, auto &&read) {
+    constexpr int Q = decltype(loads)::value ? kLoads : 0, R = decltype(n_reads)::value;
+    constexpr int kEvery = R * 2 <= kMfmas ? 2 : 1, kPer = (R + kMfmas - 1) / kMfmas;
     static_for<kMfmas>([&](auto kk) {
       constexpr int k = decltype(kk)::value, i = k / WB, j = k % WB;
-      if constexpr (decltype(do_mfma)::value) acc[i][j] = mfma<EL>(cur.b[j], cur.a[i], acc[i][j]);
+      if constexpr (decltype(do_mfma)::value) acc[i][j] = mfma<EL>(fb[j], fa[i], acc[i][j]);
       if constexpr (k % kEvery == 0) {
 #pragma unroll
         for (int n = k / kEvery * kPer; n < (k / kEvery + 1) * kPer; n++)
-          if (n < kReads) read(slot, s, n, nxt);
+          if (n < R) read(n);
       }
       static_for<(k + 1) * Q / kMfmas - k * Q / kMfmas>(
           [&](auto q) { load(std::integral_constant<int, k * Q / kMfmas + decltype(q)::value>{}, src); });
       __builtin_amdgcn_sched_barrier(0);  // keep this order
     });
   };
+  // LDS read number n of A and B of step s of a slot, in the order in which the
+  // MFMAs need them: A's first block, B's blocks, A's others.
+  constexpr int kA1 = A::kReads / WA;  // reads of one A block
+  auto read_ab = [&](const MXT_LDS uint8_t *slot_a, const MXT_LDS uint8_t *slot_b, int s, int n, u32x4_t *fa, u32x4_t *fb) {
+    if (n < kA1) oa.read(slot_a, s, n, 2, fa);
+    else if (n < kA1 + B::kReads) ob.read(slot_b, s, n - kA1, 1, fb);
+    else oa.read(slot_a, s, n - B::kReads, 2, fa);
+  };
+  using NA = std::integral_constant<int, A::kReads>;
+  using NB = std::integral_constant<int, B::kReads>;
+  using NAB = std::integral_constant<int, A::kReads + B::kReads>;
 
-  Frags f0, f1;  // the steps alternate between the two
-  static_assert(kKS % 2 == 0, "the last step of a stage leaves its operands in f1");
-  // Stage st: the last step of stage st - 1 (from f1), then its own steps but
-  // the last, which it leaves in f1.  At its end stage st + 1 has landed and
-  // stage st's slot is free.
+  // Fragments: [0], [1] are the two steps in turn, or with SPLIT the high and
+  // low planes of one step.
+  u32x4_t fa[2][WA], fb[2][WB];
+  static_assert(SPLIT || kKS % 2 == 0, "the last step of a stage leaves its operands in [1]");
+  // Stage st: the last MFMAs of stage st - 1, whose operands are in registers,
+  // then its own but the last, whose operands it leaves there.  At its end
+  // stage st + 1 has landed and stage st's slot is free.
   auto stage = [&](auto has_last, int st) {
     const MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
     constexpr bool first = !decltype(has_last)::value;
+    using Loads = std::integral_constant<bool, !first>;
     // the loads of the stage that takes over stage st - 1's slot
     const Src src = first ? Src{} : source(st - 1 + RING);
-    phase(has_last, std::integral_constant<bool, !first>{}, slot, 0, f1, f0, src);
-    phase(Yes{}, No{}, slot, 1, f0, f1, src);
+    if constexpr (SPLIT) {
+      // low x high of the step before while high A and low B are read, then
+      // high x low (reading high B) and high x high (reading low A): three
+      // phases on one set of registers
 #pragma unroll
-    for (int s = 2; s < kKS; s += 2) {
-      phase(Yes{}, No{}, slot, s, f1, f0, src);
-      phase(Yes{}, No{}, slot, s + 1, f0, f1, src);
+      for (int s = 0; s < kKS; s++) {
+        auto rd = [&](int n) { read_ab(slot, slot + kSlotB + B::kBytes, s, n, fa[0], fb[1]); };
+        if (s == 0) phase(has_last, Loads{}, NAB{}, fa[1], fb[0], src, rd);
+        else phase(Yes{}, No{}, NAB{}, fa[1], fb[0], src, rd);
+        phase(Yes{}, No{}, NB{}, fa[0], fb[1], src, [&](int n) { ob.read(slot + kSlotB, s, n, 1, fb[0]); });
+        phase(Yes{}, No{}, NA{}, fa[0], fb[0], src, [&](int n) { oa.read(slot + A::kBytes, s, n, 2, fa[1]); });
+      }
+    } else {
+      phase(has_last, Loads{}, NAB{}, fa[1], fb[1], src, [&](int n) { read_ab(slot, slot + kSlotB, 0, n, fa[0], fb[0]); });
+#pragma unroll
+      for (int s = 1; s < kKS; s++)
+        phase(Yes{}, No{}, NAB{}, fa[(s + 1) & 1], fb[(s + 1) & 1], src,
+              [&](int n) { read_ab(slot, slot + kSlotB, s, n, fa[s & 1], fb[s & 1]); });
     }
 #if __HIP_DEVICE_COMPILE__
     // keep this stage's results in its block
@@ -382,10 +397,10 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     for (int i = 0; i < WA; i++) {
 #pragma unroll
       for (int j = 0; j < WB; j++) asm volatile("" ::"a"(acc[i][j]));
-      asm volatile("" ::"v"(f1.a[i]));
+      asm volatile("" ::"v"(fa[1][i]));
     }
 #pragma unroll
-    for (int j = 0; j < WB; j++) asm volatile("" ::"v"(f1.b[j]));
+    for (int j = 0; j < WB; j++) asm volatile("" ::"v"(fb[SPLIT ? 0 : 1][j]));
 #endif
     // issued so far: stages up to st - 1 + RING
     wait_vm<(RING - 2) * kLoads>();
@@ -404,8 +419,9 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     __syncthreads();
     stage(No{}, 0);
     for (int st = 1; st < n_stage; st++) stage(Yes{}, st);
+    constexpr int last_b = SPLIT ? 0 : 1;
 #pragma unroll
-    for (int k = 0; k < kMfmas; k++) acc[k / WB][k % WB] = mfma<EL>(f1.b[k % WB], f1.a[k / WB], acc[k / WB][k % WB]);
+    for (int k = 0; k < kMfmas; k++) acc[k / WB][k % WB] = mfma<EL>(fb[last_b][k % WB], fa[1][k / WB], acc[k / WB][k % WB]);
     wait_vm<0>();  // nothing may still be landing in LDS when the workgroup ends or goes on
   }
 

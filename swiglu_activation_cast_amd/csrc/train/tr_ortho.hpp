@@ -238,7 +238,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
   constexpr bool SYM = STEP == kGram || STEP == kPoly;
   static_assert(!SYM || WI == WJ, "symmetric results take square tiles");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * 2];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * (SPLIT ? 4 : 2)];
   const GemmArgs &g = p.g;
   const u32 tiles = SYM ? (u32)g.tiles_m * (u32)(g.tiles_m + 1) / 2 : (u32)g.tiles_m * (u32)g.tiles_n;
   const u32 L = mx::xcd_remap(blockIdx.x, gridDim.x);

@@ -153,7 +153,8 @@ struct Operand {
 
   // XOR of the chunk position in LDS row r.
   static __device__ __forceinline__ u32 key(u32 r) {
-    if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
+    if constexpr (L == kKC && BK == 128) return r & 15u;
+    else if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
     else if constexpr (L == kKC) return (r >> 2) & 3u;
     else if constexpr (W == 1) return (((r >> 1) & 1u) | ((r >> 3) & 1u) << 1) << 1;  // 128-byte rows: two per turn of the banks
     else return ((r & 3u) | ((r >> 3) & 1u) << 2) << 1;
@@ -245,6 +246,7 @@ struct Tile {
   const uint16_t *a_lo, *b_lo;  // SPLIT
   int64_t k_len;
   u32 rows, cols;
+  u32 first;                    // any number: which stage of K (modulo them) comes first
 };
 
 template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, class Emit>
@@ -291,9 +293,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   int kmax = kBK;  // of the stages being loaded
   oa.set_kmax(kmax);
   ob.set_kmax(kmax);
+  // The stages of K in turn, from t.first on.
+  const int rot = n_stage > 0 ? __builtin_amdgcn_readfirstlane((int)(t.first % (u32)n_stage)) : 0;
+  auto place = [&](int st) { return st + rot < n_stage ? st + rot : st + rot - n_stage; };
   // Stages past the last re-read it into a slot that is not read again.
   auto source = [&](int st) {
-    const int s = min(st, n_stage - 1);
+    const int s = place(min(st, n_stage - 1));
     Src r;
     r.a[0] = oa.base + s * oa.step;
     r.b[0] = ob.base + s * ob.step;
@@ -302,7 +307,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
     r.slot_a = lds0 + (u32)(st % RING) * kSlot + oa.lds_w;
     r.slot_b = lds0 + (u32)(st % RING) * kSlot + kSlotB + ob.lds_w;
     const int k = s == n_stage - 1 ? k_tail : kBK;
-    if (k != kmax) {  // uniform; once, if the last stage is a partial one
+    if (k != kmax) {  // uniform; only around a partial last stage
       kmax = k;
       oa.set_kmax(k);
       ob.set_kmax(k);
@@ -316,7 +321,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   };
   // Stage st has landed: clear what lies past K (each lane what it loaded).
   auto clear = [&](int st) {
-    if (k_tail == kBK || st != n_stage - 1) return;
+    if (k_tail == kBK || st >= n_stage || place(st) != n_stage - 1) return;
     MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
 #pragma unroll
     for (int p = 0; p < kPl; p++) {
@@ -643,8 +648,7 @@ inline int64_t work_items_bound(int64_t R, int64_t cus) {
 }
 
 // WI = WJ = 4: 256 x 256 tiles, short ones (a group's last rows) and those of a
-// last partial round cut down; WI = WJ = 2: 128 x 128 tiles, two workgroups to
-// a CU.
+// last partial round cut down; smaller tiles, two workgroups to a CU.
 template <int MODE, int AL, int BL, int WI, int WJ, int BK, int RING, bool F32>
 __global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(const GemmArgs g) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
@@ -690,6 +694,11 @@ __global__ __launch_bounds__(kThreads, WI * WJ > 8 ? 1 : 2) void k_group_gemm(co
   t.b += BL == kKC ? n0 * g.ldb : n0;
   t.cols = emit.cols = (u32)min<int64_t>(BN / it.parts, g.N - n0);
   emit.c = F32 ? (void *)(static_cast<float *>(emit.c) + n0) : (void *)(static_cast<uint16_t *>(emit.c) + n0);
+  // Tiles of few rows stream the weights, each its own rows of them, and where
+  // those are a power of two apart, tiles that go through K in step read from
+  // few of the memory channels at a time.  So each starts at another stage (24
+  // tokens over 16 experts, 4096 x 2048: 55 -> 41 us, 5.2 TB/s).
+  if (WI == 1 && BL == kKC) t.first = blockIdx.x;
   if constexpr (kBig) {
     if (it.parts == 4) gemm_tile<kBf16, AL, BL, WI, 1, BK, RING, false>(g, t, smem, emit);
     else if (it.parts == 2) gemm_tile<kBf16, AL, BL, WI, 2, BK, RING, false>(g, t, smem, emit);

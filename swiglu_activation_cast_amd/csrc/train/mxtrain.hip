@@ -237,14 +237,39 @@ mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
     const int64_t tm = (p.g.M + b - 1) / b, tn = (p.g.N + b - 1) / b;
     return batch * (sym ? tm * (tm + 1) / 2 : tm * tn);
   };
-  const int cus = cu_count();
-  const int64_t b = tiles(256) >= cus ? 256 : tiles(128) >= cus / 2 ? 128 : 64;
+  const int64_t cus = cu_count();
+  // Time in units of a round of 256 x 256 tiles, one per CU: a last partial
+  // round runs cut down unless the product is symmetric; 128 x 128 tiles run
+  // two to a CU.  Five steps with one tile throughout and as chosen here, us:
+  //                            256    128     64   chosen
+  //   1 x 256 x 512 fp32       423    204    107      107
+  //   8 x 2048 x 1024 bf16     629    465    838      424
+  //   1 x 2048 x 2048 bf16     676    411    502      423
+  //   4 x 2048 x 2048 bf16     842    940   1586      821
+  //   1 x 8192 x 1024 bf16    1057    658    431      315
+  //   1 x 8192 x 5120 fp32    9242  11154  16711     9180
+  auto cost256 = [&] {
+    const int64_t t = tiles(256), whole = t / cus, tail = t % cus;
+    if (sym) return (double)((t + cus - 1) / cus);
+    return whole + (tail == 0 ? 0.0 : tail <= cus / 4 ? 0.35 : tail <= cus / 2 ? 0.6 : 1.0);
+  };
+  auto cost128 = [&] {
+    const int64_t t = tiles(128);
+    return t <= cus ? 0.42 : 0.67 * (double)((t + 2 * cus - 1) / (2 * cus));
+  };
+  auto cost64 = [&] { return 0.2 * (double)((tiles(64) + cus - 1) / cus); };
+  const double c256 = cost256(), c128 = cost128(), c64 = cost64();
+  const int64_t b = c256 <= c128 && c256 <= c64 ? 256 : c128 <= c64 ? 128 : 64;
   p.g.tiles_m = (int32_t)((p.g.M + b - 1) / b);
   p.g.tiles_n = (int32_t)((p.g.N + b - 1) / b);
+  p.g.G = (int32_t)batch;
+  p.g.cus = (int32_t)cus;
+  int64_t blocks = tiles(b);
+  if (b == 256 && !sym) blocks = mxt::work_items(blocks, cus);
   const void *k = b == 256   ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 4, 4, SPLIT ? 32 : 64, 2, SPLIT>
                   : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, SPLIT ? 32 : 64, 2, SPLIT>
                              : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 64, SPLIT ? 4 : 8, SPLIT>;
-  return launch(k, tiles(b), mxt::kThreads, p, stream);
+  return launch(k, blocks, mxt::kThreads, p, stream);
 }
 
 template <bool SPLIT>

@@ -241,22 +241,39 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * (SPLIT ? 4 : 2)];
   const GemmArgs &g = p.g;
   const u32 tiles = SYM ? (u32)g.tiles_m * (u32)(g.tiles_m + 1) / 2 : (u32)g.tiles_m * (u32)g.tiles_n;
-  const u32 L = mx::xcd_remap(blockIdx.x, gridDim.x);
+  // whole-matrix products of 256 x 256 tiles end in a cut-down round (the
+  // symmetric ones, whose tiles are square, do not)
+  constexpr bool kCut = !SYM && WI == 4 && WJ == 4;
+  Item it{blockIdx.x, 0, 1};
+  const u32 R = tiles * (u32)g.G;
+  if (kCut && !work_item(blockIdx.x, R, (u32)g.cus, it)) return;
+  const u32 whole = kCut ? R - R % (u32)g.cus : R;
+  // matrices of fewer tiles than the CUs compute together: whole ones to an XCD
+  const u32 L = !SYM && tiles >= 256 ? square_order(it.L, whole) : it.L < whole ? mx::xcd_remap(it.L, whole) : it.L;
   const int64_t batch = L / tiles;
   u32 tm, tn;
   if constexpr (SYM) lower_tile(L % tiles, tm, tn);
   else tile_of(L % tiles, (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
   tm = (u32)__builtin_amdgcn_readfirstlane((int)tm);
   tn = (u32)__builtin_amdgcn_readfirstlane((int)tn);
-  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN;
+  const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN + it.part * (BN / it.parts);
+  if (n0 >= g.N) return;  // a part past the last column
   const int64_t a_at = batch * g.stride_a + (AL == kKC ? m0 * g.lda : m0);
   const int64_t b_at = batch * g.stride_b + (BL == kKC ? n0 * g.ldb : n0);
-  Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, g.K, (u32)min<int64_t>(BM, g.M - m0), (u32)min<int64_t>(BN, g.N - n0)};
+  Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, g.K, (u32)min<int64_t>(BM, g.M - m0),
+         (u32)min<int64_t>(BN / it.parts, g.N - n0), 0};
   if constexpr (SPLIT) {
     t.a_lo = p.a_lo + a_at;
     t.b_lo = p.b_lo + b_at;
   }
   const float phi = p.phi ? *mx::gptr(p.phi + batch) : 1.0f;
+  auto run = [&](const auto &e) {
+    if constexpr (kCut) {
+      if (it.parts == 4) return gemm_tile<kF16, AL, BL, WI, 1, BK, RING, SPLIT>(g, t, smem, e);
+      if (it.parts == 2) return gemm_tile<kF16, AL, BL, WI, 2, BK, RING, SPLIT>(g, t, smem, e);
+    }
+    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
+  };
   const int64_t at = batch * g.stride_c + m0 * g.ldc + n0;
   if constexpr (STEP == kLast) {
     EmitLast<SPLIT> e{};
@@ -265,7 +282,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     e.cols = t.cols;
     e.vec = g.vec_c != 0;
     e.f0 = p.scale * phi;
-    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
+    run(e);
   } else {
     EmitNs<STEP, SPLIT> e{};
     e.ld = g.ldc;
@@ -288,7 +305,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     } else {
       e.f0 = STEP == kGram ? p.scale : p.scale * phi;
     }
-    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
+    run(e);
   }
 }
 

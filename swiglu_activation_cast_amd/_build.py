@@ -9,6 +9,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -19,7 +21,8 @@ SOURCES = [os.path.join(CSRC, "mxfp8.hip")]
 STREAM_LIB_PATH = os.path.join(PKG_DIR, "libmxstream.so")
 STREAM_SOURCES = [os.path.join(CSRC, "mx_stream.hip")]
 TRAIN_LIB_PATH = os.path.join(PKG_DIR, "libmxtrain.so")
-TRAIN_SOURCES = [os.path.join(CSRC, "train", "mxtrain.hip")]
+TRAIN_SOURCES = [os.path.join(CSRC, "train", name) for name in (
+    "mxtrain.hip", "mxtrain_gemm.hip", "mxtrain_ortho.hip", "mxtrain_ortho_bf16.hip", "mxtrain_ortho_f32.hip")]
 ARCH = "gfx950"
 
 
@@ -57,10 +60,7 @@ def compile_flags() -> list[str]:
     ]
 
 
-def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
-          sources: list[str] | None = None) -> str:
-    tmp = out + ".tmp"
-    cmd = [hipcc(), *compile_flags(), *(extra_flags or []), "-shared", "-o", tmp, *(sources or SOURCES)]
+def _run(cmd: list[str], verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
@@ -71,6 +71,25 @@ def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bo
         raise RuntimeError(f"hipcc failed ({res.returncode}):\n{text}")
     if verbose and text.strip():
         print(text, flush=True)
+
+
+def build(out: str = LIB_PATH, extra_flags: list[str] | None = None, verbose: bool = False,
+          sources: list[str] | None = None) -> str:
+    """Compiles `sources` into the shared library `out`; several sources are
+    compiled side by side and linked."""
+    tmp = out + ".tmp"
+    sources = sources or SOURCES
+    flags = [*compile_flags(), *(extra_flags or [])]
+    if len(sources) == 1:
+        _run([hipcc(), *flags, "-shared", "-o", tmp, *sources], verbose)
+    else:
+        with tempfile.TemporaryDirectory() as d:
+            objects = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
+            with ThreadPoolExecutor(max_workers=min(len(sources), 8)) as pool:
+                for _ in pool.map(lambda so: _run([hipcc(), *flags, "-c", "-o", so[1], so[0]], verbose),
+                                  zip(sources, objects)):
+                    pass
+            _run([hipcc(), f"--offload-arch={ARCH}", "-shared", "-o", tmp, *objects], verbose)
     os.replace(tmp, out)
     return out
 

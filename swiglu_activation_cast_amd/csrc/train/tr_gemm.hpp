@@ -50,7 +50,7 @@
 
 namespace mxt {
 
-using mx::u32x4_t;
+
 
 enum Layout { kKC = 0, kMC = 1 };
 enum Mode { kBatch = 0, kGroupM = 1, kGroupK = 2 };
@@ -520,13 +520,13 @@ struct EmitC {
     constexpr u32 N = F32 ? 4 : 8;
     uint8_t *p = static_cast<uint8_t *>(c) + ((int64_t)m * ldc + n) * (F32 ? 4 : 2);
     if (vec && n + N <= cols) {
-      *mx::gptr(reinterpret_cast<u32x4_t *>(p)) = v;
+      *gptr(reinterpret_cast<u32x4_t *>(p)) = v;
     } else {
 #pragma unroll
       for (u32 e = 0; e < N; e++)
         if (n + e < cols) {
-          if constexpr (F32) *mx::gptr(reinterpret_cast<u32 *>(p) + e) = v[e];
-          else *mx::gptr(reinterpret_cast<uint16_t *>(p) + e) = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
+          if constexpr (F32) *gptr(reinterpret_cast<u32 *>(p) + e) = v[e];
+          else *gptr(reinterpret_cast<uint16_t *>(p) + e) = (uint16_t)(v[e / 2] >> (16 * (e % 2)));
         }
     }
   }
@@ -551,7 +551,7 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t *ends, int32_t G, i
   int64_t before = 0;
   for (int32_t g0 = 0; g0 < G; g0 += 64) {
     const int32_t m32 = (int32_t)M;
-    int32_t end = g0 + lane < G ? min(max(*mx::gptr(ends + g0 + lane), 0), m32) : 0;
+    int32_t end = g0 + lane < G ? min(max(*gptr(ends + g0 + lane), 0), m32) : 0;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int32_t up = __shfl_up(end, o, 64);
@@ -586,12 +586,12 @@ __device__ __forceinline__ GroupTile find_tile(const int32_t *ends, int32_t G, i
 __device__ __forceinline__ void find_group(const int32_t *ends, int32_t want, int64_t T, int64_t &start, int64_t &end) {
   const int lane = threadIdx.x & 63;
   int32_t below = 0;  // largest end before `want`
-  for (int32_t e = lane; e < want; e += 64) below = max(below, *mx::gptr(ends + e));
+  for (int32_t e = lane; e < want; e += 64) below = max(below, *gptr(ends + e));
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) below = max(below, __shfl_xor(below, o, 64));
   below = __builtin_amdgcn_readfirstlane(below);
   start = min<int64_t>(below, T);
-  end = min<int64_t>(max(below, __builtin_amdgcn_readfirstlane(*mx::gptr(ends + want))), T);
+  end = min<int64_t>(max(below, __builtin_amdgcn_readfirstlane(*gptr(ends + want))), T);
 }
 
 // Position in the tile order -> tile row and column: bands of kTileRows tile

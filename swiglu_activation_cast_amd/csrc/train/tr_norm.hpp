@@ -46,16 +46,16 @@ struct LnArgs {
 template <class T, int VEC>
 __device__ __forceinline__ void load_chunk(const T *p, float *v) {
   if constexpr (VEC == 1) {
-    v[0] = to_f32(*mx::gptr(p));
+    v[0] = to_f32(*gptr(p));
   } else if constexpr (sizeof(T) == 2) {
-    const mx::u32x4_t q = *mx::gptr(reinterpret_cast<const mx::u32x4_t *>(p));
+    const u32x4_t q = *gptr(reinterpret_cast<const u32x4_t *>(p));
 #pragma unroll
     for (int i = 0; i < 4; i++) {
       v[2 * i] = mx::lo_f(q[i]);
       v[2 * i + 1] = mx::hi_f(q[i]);
     }
   } else {
-    const f32x4_t q = *mx::gptr(reinterpret_cast<const f32x4_t *>(p));
+    const f32x4_t q = *gptr(reinterpret_cast<const f32x4_t *>(p));
 #pragma unroll
     for (int i = 0; i < 4; i++) v[i] = q[i];
   }
@@ -64,17 +64,17 @@ __device__ __forceinline__ void load_chunk(const T *p, float *v) {
 template <class T, int VEC>
 __device__ __forceinline__ void store_chunk(T *p, const float *v) {
   if constexpr (VEC == 1) {
-    *mx::gptr(p) = from_f32<T>(v[0]);
+    *gptr(p) = from_f32<T>(v[0]);
   } else if constexpr (sizeof(T) == 2) {
-    mx::u32x4_t q;
+    u32x4_t q;
 #pragma unroll
     for (int i = 0; i < 4; i++) q[i] = mx::pack_bf16(v[2 * i], v[2 * i + 1]);
-    __builtin_nontemporal_store(q, mx::gptr(reinterpret_cast<mx::u32x4_t *>(p)));
+    __builtin_nontemporal_store(q, gptr(reinterpret_cast<u32x4_t *>(p)));
   } else {
     f32x4_t q;
 #pragma unroll
     for (int i = 0; i < 4; i++) q[i] = v[i];
-    __builtin_nontemporal_store(q, mx::gptr(reinterpret_cast<f32x4_t *>(p)));
+    __builtin_nontemporal_store(q, gptr(reinterpret_cast<f32x4_t *>(p)));
   }
 }
 
@@ -91,23 +91,23 @@ __device__ __forceinline__ void load_param(const void *p, bool f32, bool vec, in
     if (VEC >= 4 && vec) {
 #pragma unroll
       for (int i = 0; i < VEC; i += 4) {
-        const f32x4_t u = *mx::gptr(reinterpret_cast<const f32x4_t *>(q + i));
+        const f32x4_t u = *gptr(reinterpret_cast<const f32x4_t *>(q + i));
 #pragma unroll
         for (int j = 0; j < 4 && i + j < VEC; j++) v[i + j] = u[j];
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < VEC; i++) v[i] = *mx::gptr(q + i);
+      for (int i = 0; i < VEC; i++) v[i] = *gptr(q + i);
     }
   } else {
     const uint16_t *q = static_cast<const uint16_t *>(p) + col;
     if (VEC == 8 && vec) {
-      const mx::u32x4_t u = *mx::gptr(reinterpret_cast<const mx::u32x4_t *>(q));
+      const u32x4_t u = *gptr(reinterpret_cast<const u32x4_t *>(q));
 #pragma unroll
       for (int i = 0; i < VEC; i++) v[i] = i % 2 ? mx::hi_f(u[i / 2]) : mx::lo_f(u[i / 2]);
     } else {
 #pragma unroll
-      for (int i = 0; i < VEC; i++) v[i] = to_f32(*mx::gptr(q + i));
+      for (int i = 0; i < VEC; i++) v[i] = to_f32(*gptr(q + i));
     }
   }
 }
@@ -155,10 +155,10 @@ struct Raw {
   u32 w[kWords];
   __device__ __forceinline__ void load(const T *p, u32 off) {
     if constexpr (VEC == 1) {
-      if constexpr (sizeof(T) == 2) w[0] = *mx::gptr(mx::byte_off(p, off));
-      else w[0] = __float_as_uint(*mx::gptr(mx::byte_off(p, off)));
+      if constexpr (sizeof(T) == 2) w[0] = *gptr(byte_off(p, off));
+      else w[0] = __float_as_uint(*gptr(byte_off(p, off)));
     } else {
-      const mx::u32x4_t q = *mx::gptr(reinterpret_cast<const mx::u32x4_t *>(mx::byte_off(p, off)));
+      const u32x4_t q = *gptr(reinterpret_cast<const u32x4_t *>(byte_off(p, off)));
 #pragma unroll
       for (int i = 0; i < 4; i++) w[i] = q[i];
     }
@@ -233,10 +233,10 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : CH * VEC <= 16 ? 1024 : 512)) voi
     for (int i = 0; i < CH; i++) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) v[i][j] = fmaf((v[i][j] - e) * rstd, w[i][j], b[i][j]);
-      if (in(i)) store_chunk<T, VEC>(mx::byte_off(y, off[i]), v[i]);
+      if (in(i)) store_chunk<T, VEC>(byte_off(y, off[i]), v[i]);
     }
-    if (t == 0 && g.mean) *mx::gptr(g.mean + row) = m + e;
-    if (t == 0 && g.rstd) *mx::gptr(g.rstd + row) = rstd;
+    if (t == 0 && g.mean) *gptr(g.mean + row) = m + e;
+    if (t == 0 && g.rstd) *gptr(g.rstd + row) = rstd;
   }
 }
 
@@ -249,11 +249,11 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_long(const LnArgs g) {
   const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
   T *y = static_cast<T *>(g.y) + row * g.ld_y;
   float s = 0.0f, q = 0.0f, e = 0.0f, unused = 0.0f;
-  for (int64_t c = threadIdx.x; c < g.N; c += 1024) s += to_f32(*mx::gptr(x + c));
+  for (int64_t c = threadIdx.x; c < g.N; c += 1024) s += to_f32(*gptr(x + c));
   row_sum2<0>(s, unused, sm[0]);
   const float m = s / (float)g.N;
   for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
-    const float d = to_f32(*mx::gptr(x + c)) - m;
+    const float d = to_f32(*gptr(x + c)) - m;
     e += d;
     q = fmaf(d, d, q);
   }
@@ -263,10 +263,10 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_long(const LnArgs g) {
     float w, b;
     load_param<1>(g.w, g.w_f32, false, (int32_t)c, 1.0f, &w);
     load_param<1>(g.b, g.w_f32, false, (int32_t)c, 0.0f, &b);
-    *mx::gptr(y + c) = from_f32<T>(fmaf((to_f32(*mx::gptr(x + c)) - m - e) * rstd, w, b));
+    *gptr(y + c) = from_f32<T>(fmaf((to_f32(*gptr(x + c)) - m - e) * rstd, w, b));
   }
-  if (threadIdx.x == 0 && g.mean) *mx::gptr(g.mean + row) = m + e;
-  if (threadIdx.x == 0 && g.rstd) *mx::gptr(g.rstd + row) = rstd;
+  if (threadIdx.x == 0 && g.mean) *gptr(g.mean + row) = m + e;
+  if (threadIdx.x == 0 && g.rstd) *gptr(g.rstd + row) = rstd;
 }
 
 // Most threads of a backward workgroup whose threads hold E elements: a thread
@@ -323,8 +323,8 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) 
       rx[i].load(x, off[i]);
       rd[i].load(dy, off[i]);
     }
-    mean = *mx::gptr(g.mean + row);
-    rstd = *mx::gptr(g.rstd + row);
+    mean = *gptr(g.mean + row);
+    rstd = *gptr(g.rstd + row);
   };
   int64_t row = (int64_t)blockIdx.x * kSlots + slot;
   constexpr bool kAhead = CH * VEC <= 16;
@@ -357,7 +357,7 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) 
     for (int i = 0; i < CH; i++) {
 #pragma unroll
       for (int j = 0; j < VEC; j++) d[i][j] = (d[i][j] - fmaf(xh[i][j], c2, c1)) * r;
-      if (in(i)) store_chunk<T, VEC>(mx::byte_off(dx, off[i]), d[i]);
+      if (in(i)) store_chunk<T, VEC>(byte_off(dx, off[i]), d[i]);
     }
   }
   if (!g.part) return;
@@ -369,8 +369,8 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) 
       if (in(i)) {
 #pragma unroll
         for (int j = 0; j < VEC; j++) {
-          *mx::gptr(part + col + j) = aw[i][j];
-          *mx::gptr(part + g.N + col + j) = ab[i][j];
+          *gptr(part + col + j) = aw[i][j];
+          *gptr(part + g.N + col + j) = ab[i][j];
         }
       }
     }
@@ -391,7 +391,7 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) 
       float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < kSlots; k++) s += joined[k * 2 * g.N + c];
-      *mx::gptr(part + c) = s;
+      *gptr(part + c) = s;
     }
   }
 }
@@ -409,18 +409,18 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_long(const LnArgs g) {
     const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
     const T *dy = static_cast<const T *>(g.dy) + row * g.ld_dy;
     T *dx = static_cast<T *>(g.y) + row * g.ld_y;
-    const float mean = *mx::gptr(g.mean + row), rstd = *mx::gptr(g.rstd + row);
+    const float mean = *gptr(g.mean + row), rstd = *gptr(g.rstd + row);
     float s1 = 0.0f, s2 = 0.0f;
     for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
       float w;
       load_param<1>(g.w, g.w_f32, false, (int32_t)c, 1.0f, &w);
-      const float d = to_f32(*mx::gptr(dy + c)), h = (to_f32(*mx::gptr(x + c)) - mean) * rstd;
+      const float d = to_f32(*gptr(dy + c)), h = (to_f32(*gptr(x + c)) - mean) * rstd;
       s1 += d * w;
       s2 = fmaf(d * w, h, s2);
       if (part) {
         const bool first = row == (int64_t)blockIdx.x;
-        *mx::gptr(part + c) = fmaf(d, h, first ? 0.0f : *mx::gptr(part + c));
-        *mx::gptr(part + g.N + c) = d + (first ? 0.0f : *mx::gptr(part + g.N + c));
+        *gptr(part + c) = fmaf(d, h, first ? 0.0f : *gptr(part + c));
+        *gptr(part + g.N + c) = d + (first ? 0.0f : *gptr(part + g.N + c));
       }
     }
     row_sum2<0>(s1, s2, sm[phase]);
@@ -429,8 +429,8 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_long(const LnArgs g) {
     for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
       float w;
       load_param<1>(g.w, g.w_f32, false, (int32_t)c, 1.0f, &w);
-      const float d = to_f32(*mx::gptr(dy + c)), h = (to_f32(*mx::gptr(x + c)) - mean) * rstd;
-      *mx::gptr(dx + c) = from_f32<T>((d * w - fmaf(h, c2, c1)) * rstd);
+      const float d = to_f32(*gptr(dy + c)), h = (to_f32(*gptr(x + c)) - mean) * rstd;
+      *gptr(dx + c) = from_f32<T>((d * w - fmaf(h, c2, c1)) * rstd);
     }
   }
 }
@@ -445,7 +445,7 @@ __global__ __launch_bounds__(1024) void k_ln_join(const float *part, int parts, 
   float a = 0.0f;
   if (col < 2 * (int64_t)N)
 #pragma unroll 4
-    for (int p = s; p < parts; p += 32) a += *mx::gptr(part + (int64_t)p * 2 * N + col);
+    for (int p = s; p < parts; p += 32) a += *gptr(part + (int64_t)p * 2 * N + col);
   sm[s][c] = a;
   __syncthreads();
   if (s == 0 && col < 2 * (int64_t)N) {
@@ -453,9 +453,9 @@ __global__ __launch_bounds__(1024) void k_ln_join(const float *part, int parts, 
 #pragma unroll
     for (int k = 0; k < 32; k++) t += sm[k][c];
     if (col < N) {
-      if (dw) *mx::gptr(dw + col) = t;
+      if (dw) *gptr(dw + col) = t;
     } else {
-      if (db) *mx::gptr(db + col - N) = t;
+      if (db) *gptr(db + col - N) = t;
     }
   }
 }

@@ -46,55 +46,6 @@ struct NsArgs {
   int64_t ld_x, stride_x;
 };
 
-// Eight columns from `col` of a row of G; zeros past its end.
-__device__ __forceinline__ void ns_load8(const NsArgs &n, int64_t row, int64_t col, int64_t batch, float *v) {
-  const int64_t at = batch * n.stride_g + row * n.ld_g + col;
-  if (n.vec && col + 8 <= n.cols) {
-    if (n.g_f32) {
-      const f32x4_t *p = reinterpret_cast<const f32x4_t *>(static_cast<const float *>(n.g) + at);
-      const f32x4_t a = *mx::gptr(p), b = *mx::gptr(p + 1);
-#pragma unroll
-      for (int i = 0; i < 4; i++) v[i] = a[i], v[4 + i] = b[i];
-    } else {
-      const u32x4_t q = *mx::gptr(reinterpret_cast<const u32x4_t *>(static_cast<const uint16_t *>(n.g) + at));
-#pragma unroll
-      for (int i = 0; i < 4; i++) v[2 * i] = mx::lo_f(q[i]), v[2 * i + 1] = mx::hi_f(q[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; i++)
-      v[i] = col + i >= n.cols ? 0.0f
-             : n.g_f32         ? *mx::gptr(static_cast<const float *>(n.g) + at + i)
-                               : to_f32(*mx::gptr(static_cast<const uint16_t *>(n.g) + at + i));
-  }
-}
-
-// Sum over the workgroup's 256 threads, in every thread.
-__device__ __forceinline__ double block_sum(double v, double *sm) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
-  if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
-  __syncthreads();
-  return (sm[0] + sm[1]) + (sm[2] + sm[3]);
-}
-
-// Workgroup (p, batch): the squares of every kNormBlocks-th piece of 256
-// eight-column chunks.
-__global__ __launch_bounds__(256) void k_ns_norm(const NsArgs n) {
-  __shared__ double sm[4];
-  const int64_t cpr = (n.cols + 7) / 8, total = n.rows * cpr, batch = blockIdx.y;
-  double s = 0.0;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)kNormBlocks * 256) {
-    const int64_t row = i / cpr;
-    float v[8];
-    ns_load8(n, row, (i - row * cpr) * 8, batch, v);
-#pragma unroll
-    for (int j = 0; j < 8; j++) s = fma((double)v[j], (double)v[j], s);
-  }
-  s = block_sum(s, sm);
-  if (threadIdx.x == 0) *mx::gptr(n.sums + batch * kNormBlocks + blockIdx.x) = s;
-}
-
 // v as two fp16 numbers.  v is made opaque first: fused with the product it
 // comes from, the compiler may round that straight to fp16 for one use of the
 // high part and by way of fp32 for the other, which near a tie gives two
@@ -105,50 +56,6 @@ __device__ __forceinline__ void split_f16(float v, _Float16 &hi, _Float16 &lo) {
 #endif
   hi = (_Float16)v;
   lo = (_Float16)(v - (float)hi);
-}
-
-// X_0's fp16 form (both planes where x_lo is given) and phi.
-__global__ __launch_bounds__(256) void k_ns_cast(const NsArgs n) {
-  __shared__ double sm[4];
-  const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
-  double norm = threadIdx.x < kNormBlocks ? *mx::gptr(n.sums + batch * kNormBlocks + threadIdx.x) : 0.0;
-  norm = sqrt(block_sum(norm, sm)) + n.eps;
-  // 2^e with norm 2^e in [1/2, 1); 0 or not finite: no scaling (phi carries it)
-  int ex = 0;
-  if (norm > 0.0 && norm < 1e300) frexp(norm, &ex);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *mx::gptr(n.phi + batch) = (float)(1.0 / ldexp(norm, -ex));
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpr, col = (i - row * cpr) * 8;
-    float v[8];
-    ns_load8(n, row, col, batch, v);
-    typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
-    h8_t hi, lo;
-#pragma unroll
-    for (int j = 0; j < 8; j++) {
-      _Float16 a, b;
-      split_f16(ldexpf(v[j], 14 - ex), a, b);
-      hi[j] = a;
-      lo[j] = b;
-    }
-    const int64_t at = batch * n.stride_x + row * n.ld_x + col;
-    *mx::gptr(reinterpret_cast<h8_t *>(n.x + at)) = hi;
-    if (n.x_lo) *mx::gptr(reinterpret_cast<h8_t *>(n.x_lo + at)) = lo;
-  }
-}
-
-// No steps: X_0 itself.
-__global__ __launch_bounds__(256) void k_ns_plain(const NsArgs n, void *out, int64_t ld, int64_t stride, int f32) {
-  const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
-  const float f = *mx::gptr(n.phi + batch) / kXScale;
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpr, col = (i - row * cpr) * 8, at = batch * n.stride_x + row * n.ld_x + col;
-    for (int j = 0; j < 8 && col + j < n.cols; j++) {
-      const float v = ((float)*mx::gptr(n.x + at + j) + (n.x_lo ? (float)*mx::gptr(n.x_lo + at + j) : 0.0f)) * f;
-      const int64_t o = batch * stride + row * ld + col + j;
-      if (f32) *mx::gptr(static_cast<float *>(out) + o) = v;
-      else *mx::gptr(static_cast<uint16_t *>(out) + o) = from_f32<uint16_t>(v);
-    }
-  }
 }
 
 enum NsStep { kGram = 0, kPoly = 1, kNext = 2, kLast = 3 };
@@ -182,9 +89,9 @@ struct EmitNs {
       // past the matrix (rows and columns that are not stored) S is read at
       // the tile's first element
       const int64_t at = m < rows && n < cols ? (int64_t)m * ld + n : 0;
-      const h4_t s = *mx::gptr(reinterpret_cast<const h4_t *>(s_hi + at));
+      const h4_t s = *gptr(reinterpret_cast<const h4_t *>(s_hi + at));
       h4_t sl = {};
-      if constexpr (SPLIT) sl = *mx::gptr(reinterpret_cast<const h4_t *>(s_lo + at));
+      if constexpr (SPLIT) sl = *gptr(reinterpret_cast<const h4_t *>(s_lo + at));
 #pragma unroll
       for (u32 e = 0; e < 4; e++) {
         const float sv = (float)s[e] + (float)sl[e];
@@ -207,10 +114,10 @@ struct EmitNs {
   }
   // Rows are padded to whole chunks of 8, which all fit.
   __device__ __forceinline__ void store(int k, u32 m, u32 n, u32x4_t v) const {
-    *mx::gptr(reinterpret_cast<u32x4_t *>(out[k] + (int64_t)m * ld + n)) = v;
+    *gptr(reinterpret_cast<u32x4_t *>(out[k] + (int64_t)m * ld + n)) = v;
   }
   __device__ __forceinline__ void store_mirror(int k, u32 n, u32 m, u32x4_t v) const {
-    *mx::gptr(reinterpret_cast<u32x4_t *>(mir[k] + (int64_t)n * ld + m)) = v;
+    *gptr(reinterpret_cast<u32x4_t *>(mir[k] + (int64_t)n * ld + m)) = v;
   }
   u32 rows, cols;
 };
@@ -249,7 +156,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   if (kCut && !work_item(blockIdx.x, R, (u32)g.cus, it)) return;
   const u32 whole = kCut ? R - R % (u32)g.cus : R;
   // matrices of fewer tiles than the CUs compute together: whole ones to an XCD
-  const u32 L = !SYM && tiles >= 256 ? square_order(it.L, whole) : it.L < whole ? mx::xcd_remap(it.L, whole) : it.L;
+  const u32 L = !SYM && tiles >= 256 ? square_order(it.L, whole) : it.L < whole ? xcd_remap(it.L, whole) : it.L;
   const int64_t batch = L / tiles;
   u32 tm, tn;
   if constexpr (SYM) lower_tile(L % tiles, tm, tn);
@@ -266,7 +173,7 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     t.a_lo = p.a_lo + a_at;
     t.b_lo = p.b_lo + b_at;
   }
-  const float phi = p.phi ? *mx::gptr(p.phi + batch) : 1.0f;
+  const float phi = p.phi ? *gptr(p.phi + batch) : 1.0f;
   auto run = [&](const auto &e) {
     if constexpr (kCut) {
       if (it.parts == 4) return gemm_tile<kF16, AL, BL, WI, 1, BK, RING, SPLIT>(g, t, smem, e);

@@ -72,8 +72,9 @@ mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *w
  *   mean, rstd : fp32 [M], as the forward pass wrote them.
  *   weight    : param_dtype [N] or NULL (ones).
  *   dweight, dbias : fp32 [N]; either may be NULL (not wanted).
- *   workspace : at least mxtrain_layer_norm_bwd_workspace(M, N) bytes, 4-byte
- *               aligned; may be NULL where dweight and dbias both are.
+ *   workspace : at least mxtrain_layer_norm_bwd_workspace(M, N) bytes (0 for
+ *               few rows), 4-byte aligned; may be NULL where that is 0, or
+ *               dweight and dbias both are NULL.
  * M == 0 writes zeros into dweight and dbias.
  */
 int64_t mxtrain_layer_norm_bwd_workspace(int64_t M, int64_t N);

@@ -224,10 +224,12 @@ def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     dx = _out(out, "out", x.shape, x.dtype, dev)
     dw, pdw = _f32_out(dweight, "dweight", N, dev)
     db, pdb = _f32_out(dbias, "dbias", N, dev)
-    ws = _workspace(_workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N), workspace, dev, stream)
+    nbytes = _workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N)
+    ws = _workspace(nbytes, workspace, dev, stream) if nbytes else None
     _call("mxtrain_layer_norm_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), pm, pr, pw,
           0 if weight is None else _TYPES[weight.dtype], M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
-          pdw, pdb, ws.data_ptr(), ws.numel() * ws.element_size(), _stream_of(dev, stream))
+          pdw, pdb, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
+          _stream_of(dev, stream))
     return dx, dw, db
 
 

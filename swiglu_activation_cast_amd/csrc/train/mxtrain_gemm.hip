@@ -22,7 +22,10 @@ GroupKernel group_kernel(bool f32) {
 
 // The tile for `groups` groups of about `rows` rows of C each (as if tokens
 // were spread evenly: the real ends are on the device).
-//  - 256 x 256 from two thirds of a tile per CU on;
+//  - 256 x 256 from two thirds of a tile per CU on, unless K is so short that
+//    the time is C's (the weight gradient of 61 groups without tokens, 6808 x
+//    360: 79 us, with 128 x 128 tiles, two to a CU, 57; at depth 156 they are
+//    within 5% of each other, at depth 250 90 us against 107);
 //  - 128 x 128 where there is one per CU, or two per CU of groups that fill only
 //    half of its rows (32 groups of 47 rows, 2048 x 2048: 70 us, with 64 rows
 //    72; input gradient 55 against 65);
@@ -32,10 +35,10 @@ GroupKernel group_kernel(bool f32) {
 //    against 30; 7 groups of 75 rows, 504 columns of depth 5120: 27 against 37,
 //    with 128 x 128 tiles 62).
 template <int MODE, int AL, int BL>
-GroupKernel group_pick(int64_t groups, int64_t rows, int64_t N, bool f32) {
+GroupKernel group_pick(int64_t groups, int64_t rows, int64_t N, int64_t depth, bool f32) {
   auto tiles = [&](int64_t bm, int64_t bn) { return groups * ((rows + bm - 1) / bm) * ((N + bn - 1) / bn); };
   const int64_t cus = cu_count();
-  if (rows > 128 && tiles(256, 256) >= cus * 2 / 3) return group_kernel<MODE, AL, BL, 4, 4, 64, 2>(f32);
+  if (rows > 128 && depth > 64 && tiles(256, 256) >= cus * 2 / 3) return group_kernel<MODE, AL, BL, 4, 4, 64, 2>(f32);
   if (rows > 32 && tiles(128, 128) >= (rows > 64 ? cus : 2 * cus)) return group_kernel<MODE, AL, BL, 2, 2, 64, 2>(f32);
   if (tiles(64, 128) >= cus / 2) return group_kernel<MODE, AL, BL, 1, 2, 64, 3>(f32);
   return group_kernel<MODE, AL, BL, 1, 1, 64, 4>(f32);
@@ -76,8 +79,8 @@ mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, i
     return MXTRAIN_ERR_OVERFLOW;
   const bool f32 = c_dtype == MXTRAIN_F32;
   const int64_t groups = std::min(G, M), rows = (M + groups - 1) / groups;  // as if evenly spread
-  const GroupKernel k = transpose_b ? group_pick<mxt::kGroupM, mxt::kKC, mxt::kKC>(groups, rows, N, f32)
-                                    : group_pick<mxt::kGroupM, mxt::kKC, mxt::kMC>(groups, rows, N, f32);
+  const GroupKernel k = transpose_b ? group_pick<mxt::kGroupM, mxt::kKC, mxt::kKC>(groups, rows, N, K, f32)
+                                    : group_pick<mxt::kGroupM, mxt::kKC, mxt::kMC>(groups, rows, N, K, f32);
   // an upper bound of tile rows, each group adding at most one partial one:
   // the host never reads the ends
   const int64_t tiles_m = (M + k.bm - 1) / k.bm + G, tiles_n = (N + k.bn - 1) / k.bn;
@@ -121,7 +124,7 @@ mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b,
   if (!extent_ok(M, N, ldc) || __builtin_mul_overflow(stride_c, G, &all) || all > (INT64_MAX >> 4))
     return MXTRAIN_ERR_OVERFLOW;
   if (G > 1 && stride_c < (M - 1) * ldc + N) return MXTRAIN_ERR_STRIDE;
-  const GroupKernel k = group_pick<mxt::kGroupK, mxt::kMC, mxt::kMC>(G, M, N, c_dtype == MXTRAIN_F32);
+  const GroupKernel k = group_pick<mxt::kGroupK, mxt::kMC, mxt::kMC>(G, M, N, T / G, c_dtype == MXTRAIN_F32);
   const int64_t tiles_m = (M + k.bm - 1) / k.bm, tiles_n = (N + k.bn - 1) / k.bn;
   int64_t blocks;
   if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks) || __builtin_mul_overflow(blocks, G, &blocks))

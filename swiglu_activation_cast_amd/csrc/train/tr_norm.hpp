@@ -32,7 +32,9 @@ struct LnArgs {
   void *y;  // y, or dx in the backward pass
   int64_t ld_x, ld_dy, ld_y;
   float *mean, *rstd;  // written by the forward (may be NULL), read by the backward
-  float *part;         // backward: partial column sums [gridDim.x][2][N], or NULL
+  float *part;         // backward: partial column sums [row_blocks][2][N], or NULL
+  float *dw, *db;      // backward: the column sums, where workgroups of their own take them
+  int64_t row_blocks;  // backward: workgroups that walk rows; those after them take columns
   int64_t M;
   int32_t N;
   int32_t w_f32;  // weight and bias are fp32 (else bf16)
@@ -286,12 +288,50 @@ constexpr int kLnBwdThreads = E <= 8 && VEC > 1 ? 1024 : 512;
 // 16384 x 5120 bf16: 94 us, 5.35 TB/s over dy, x and dx (without the row held
 // ahead and with half the wavefronts 155 us).
 //
+// Few rows: the column sums need no row's reduction, so further workgroups of
+// the same launch take 64 columns each and read them over all rows again (from
+// L2), instead of a second launch over partial rows, which costs a small call
+// more than that.
+//
 // Columns past N: a chunk that lies there is read as the row's first one and
 // its weight and dy count as zero, so that it adds nothing.
+template <class T>
+__device__ __forceinline__ void ln_columns(const LnArgs &g, int64_t strip, float (*sm)[64][2]) {
+  const int c = threadIdx.x & 63, s = threadIdx.x >> 6, n = blockDim.x >> 6;
+  const int64_t col = strip * 64 + c;
+  float aw = 0.0f, ab = 0.0f;
+  if (col < g.N) {
+    const T *x = static_cast<const T *>(g.x) + col, *dy = static_cast<const T *>(g.dy) + col;
+#pragma unroll 8
+    for (int64_t r = s; r < g.M; r += n) {
+      const float d = to_f32(*gptr(dy + r * g.ld_dy));
+      const float h = (to_f32(*gptr(x + r * g.ld_x)) - *gptr(g.mean + r)) * *gptr(g.rstd + r);
+      aw = fmaf(d, h, aw);
+      ab += d;
+    }
+  }
+  sm[s][c][0] = aw;
+  sm[s][c][1] = ab;
+  __syncthreads();
+  if (s == 0 && col < g.N) {
+    for (int k = 1; k < n; k++) {
+      aw += sm[k][c][0];
+      ab += sm[k][c][1];
+    }
+    if (g.dw) *gptr(g.dw + col) = aw;
+    if (g.db) *gptr(g.db + col) = ab;
+  }
+}
+
 template <class T, int VEC, int TPR, int CH>
 __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) void k_ln_bwd(const LnArgs g) {
   __shared__ float sm[2][16][2];
+  __shared__ float col_sm[16][64][2];
   extern __shared__ float joined[];
+  if ((int64_t)blockIdx.x >= g.row_blocks) {
+    ln_columns<T>(g, (int64_t)blockIdx.x - g.row_blocks, col_sm);
+    return;
+  }
   constexpr int kTpr = TPR == 0 ? 1 : TPR;
   constexpr int kSlots = TPR == 0 ? 1 : 256 / kTpr;
   const int tpr = TPR == 0 ? (int)blockDim.x : TPR;
@@ -314,7 +354,7 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) 
   }
   Raw<T, VEC> rx[CH], rd[CH];
   float mean = 0.0f, rstd = 0.0f;
-  const int64_t step = (int64_t)gridDim.x * kSlots;
+  const int64_t step = g.row_blocks * kSlots;
   auto fetch = [&](int64_t row) {
     const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
     const T *dy = static_cast<const T *>(g.dy) + row * g.ld_dy;

@@ -238,6 +238,7 @@ def test_refusals():
     with pytest.raises(ValueError):
         mx.mxtrain_layer_norm_bwd(dy[:2], x, m, m)
     with pytest.raises(ValueError, match="workspace"):
-        mx.mxtrain_layer_norm_bwd(dy, x, m, m, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        big, stats = torch.zeros((2000, 64), device="cuda"), torch.zeros(2000, device="cuda")
+        mx.mxtrain_layer_norm_bwd(big, big, stats, stats, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(mx.MxtrainError):
         mx.mxtrain_layer_norm_fwd(x, eps=float("nan"))

@@ -60,9 +60,10 @@ def test_layer_norm_own_checks():
     assert ln_fwd(y=None) == NULL and ln_fwd(ld_y=1) == STRIDE and ln_fwd(y=A + 1) == ALIGN
     assert ln_fwd(M=0, x=None, y=None) == OK
     assert ln_bwd(mean=None) == NULL and ln_bwd(rstd=None) == NULL and ln_bwd(dy=None) == NULL
-    assert ln_bwd(ws=None) == NULL and ln_bwd(ws=A + 2) == ALIGN and ln_bwd(dw=A + 1) == ALIGN
-    need = mx.train_lib().mxtrain_layer_norm_bwd_workspace(4, 64)
-    assert need > 0 and ln_bwd(bytes=need - 1) == WORKSPACE
+    assert ln_bwd(M=2000, ws=None) == NULL and ln_bwd(M=2000, ws=A + 2) == ALIGN and ln_bwd(dw=A + 1) == ALIGN
+    need = mx.train_lib().mxtrain_layer_norm_bwd_workspace(2000, 64)
+    assert need > 0 and ln_bwd(M=2000, bytes=need - 1) == WORKSPACE
+    assert mx.train_lib().mxtrain_layer_norm_bwd_workspace(4, 64) == 0
     assert ln_bwd(M=0, N=0) == OK
     assert ln_bwd(M=0, dw=None, db=None, ws=None, dy=None, x=None, mean=None, rstd=None, dx=None) == OK
     assert mx.train_lib().mxtrain_layer_norm_bwd_workspace(0, 64) == 0

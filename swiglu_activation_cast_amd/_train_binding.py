@@ -8,9 +8,11 @@ workspaces with torch where the caller passes none, and calls the C entry
 point of the same name on torch's current stream, or on `stream`.  There is no
 CPU or PyTorch fallback.
 
-A workspace that a call allocates itself may be handed out again by torch as
-soon as the call returns, while its kernels still run: on `stream` other than
-the current one it is recorded there, so that it is not reused too early.
+On a `stream` other than the current one, what the call allocates comes from
+the current stream's pool: memory whose last use may still be running there,
+and which torch hands out again once it is freed here.  So the other stream
+first waits for the current one, and outputs and workspace are recorded on it
+(_other_stream).
 """
 from __future__ import annotations
 
@@ -110,20 +112,33 @@ def _workspace_bytes(name: str, *sizes) -> int:
     return _entry(name)(*sizes)
 
 
-def _workspace(nbytes: int, given: Optional[torch.Tensor], device: torch.device, stream) -> torch.Tensor:
-    """`given`, checked, or a new workspace that is safe on `stream`."""
+def _other_stream(device: torch.device, stream, *tensors) -> None:
+    """Makes `stream`, where it is not the current one, wait for the current
+    one, and keeps the tensors' memory from being reused before it is done."""
+    current = torch.cuda.current_stream(device)
+    handle = _stream_of(device, stream)
+    if handle != current.cuda_stream:
+        other = torch.cuda.ExternalStream(handle, device=device)
+        other.wait_stream(current)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(other)
+
+
+def _workspace(nbytes: int, given: Optional[torch.Tensor], device: torch.device) -> Optional[torch.Tensor]:
+    """`given`, checked, or a new workspace."""
     if given is not None:
         if given.device != device or not given.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the inputs' device")
         if given.numel() * given.element_size() < nbytes:
             raise ValueError(f"workspace must hold at least {nbytes} bytes")
         return given
-    ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=device)
-    if stream is not None:
-        handle = _stream_of(device, stream)
-        if handle != torch.cuda.current_stream(device).cuda_stream:
-            ws.record_stream(torch.cuda.ExternalStream(handle, device=device))
-    return ws
+    return torch.empty(nbytes, dtype=torch.uint8, device=device) if nbytes else None
+
+
+def _place(ws: Optional[torch.Tensor]) -> Tuple[Optional[int], int]:
+    """A workspace's address and bytes."""
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def _gpu(t, name: str, dtypes, dim: int, device=None) -> torch.Tensor:
@@ -199,6 +214,8 @@ def mxtrain_layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     y = _out(out, "out", x.shape, x.dtype, dev)
     mean, pm = _f32_out(mean, "mean", M, dev)
     rstd, pr = _f32_out(rstd, "rstd", M, dev)
+    if stream is not None:
+        _other_stream(dev, stream, y, mean, rstd)
     _call("mxtrain_layer_norm_fwd", dev, x.data_ptr(), _ld(x, "x"), pw, pb,
           0 if param is None else _TYPES[param.dtype], M, N, _TYPES[x.dtype], eps, y.data_ptr(), _ld(y, "out"),
           pm, pr, _stream_of(dev, stream))
@@ -224,12 +241,12 @@ def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     dx = _out(out, "out", x.shape, x.dtype, dev)
     dw, pdw = _f32_out(dweight, "dweight", N, dev)
     db, pdb = _f32_out(dbias, "dbias", N, dev)
-    nbytes = _workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N)
-    ws = _workspace(nbytes, workspace, dev, stream) if nbytes else None
+    ws = _workspace(_workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N), workspace, dev)
+    if stream is not None:
+        _other_stream(dev, stream, dx, dw, db, ws)
     _call("mxtrain_layer_norm_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), pm, pr, pw,
           0 if weight is None else _TYPES[weight.dtype], M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
-          pdw, pdb, None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel() * ws.element_size(),
-          _stream_of(dev, stream))
+          pdw, pdb, *_place(ws), _stream_of(dev, stream))
     return dx, dw, db
 
 
@@ -267,6 +284,8 @@ def mxtrain_grouped_gemm(a: torch.Tensor, b: torch.Tensor, group_ends: torch.Ten
         raise ValueError(f"b must be [{G}, N, {K}] (transpose_b) or [{G}, {K}, N], got {tuple(b.shape)}")
     c = _out(out, "out", (M, N), _out_dtype(out, out_dtype), dev)
     ldb = _ld(b, "b")
+    if stream is not None:
+        _other_stream(dev, stream, c)
     _call("mxtrain_grouped_gemm", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), ldb,
           b.stride(0) if G > 1 else 0, int(transpose_b), pe, G, M, N, K, c.data_ptr(), _ld(c, "out"),
           _TYPES[c.dtype], _stream_of(dev, stream))
@@ -288,6 +307,8 @@ def mxtrain_grouped_gemm_k(a: torch.Tensor, b: torch.Tensor, group_ends: torch.T
         raise ValueError("a [T, M] and b [T, N] must have the same tokens")
     c = _out(out, "out", (G, M, N), _out_dtype(out, out_dtype), dev)
     ldc = _ld(c, "out")
+    if stream is not None:
+        _other_stream(dev, stream, c)
     _call("mxtrain_grouped_gemm_k", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), _ld(b, "b"), pe, G, M, N, T,
           c.data_ptr(), ldc, c.stride(0) if G > 1 else max(ldc * M, 1), _TYPES[c.dtype], _stream_of(dev, stream))
     return c
@@ -317,8 +338,10 @@ def mxtrain_newton_schulz(g: torch.Tensor, *, steps: int = 5,
     stride_g = g.stride(0) if several else 0
     stride_c = c.stride(0) if several else 0
     nbytes = _workspace_bytes("mxtrain_newton_schulz_workspace", batch, m, n, _TYPES[c.dtype])
-    ws = _workspace(nbytes, workspace, dev, stream)
+    ws = _workspace(nbytes, workspace, dev)
+    if stream is not None:
+        _other_stream(dev, stream, c, ws)
     _call("mxtrain_newton_schulz", dev, g.data_ptr(), ld_g, stride_g, _TYPES[g.dtype], batch, m, n, int(steps),
-          (ctypes.c_float * 3)(*coeffs), eps, c.data_ptr(), ld_c, stride_c, _TYPES[c.dtype], ws.data_ptr(),
-          ws.numel() * ws.element_size(), _stream_of(dev, stream))
+          (ctypes.c_float * 3)(*coeffs), eps, c.data_ptr(), ld_c, stride_c, _TYPES[c.dtype], *_place(ws),
+          _stream_of(dev, stream))
     return c

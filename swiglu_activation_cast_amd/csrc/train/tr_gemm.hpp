@@ -151,11 +151,15 @@ struct Operand {
   u32 lds_w;            // LDS byte (within a stage's operand) of this wavefront's first load
   u32 rd[L == kKC ? kKS : 2 * W];  // this lane's LDS read offsets
 
-  // XOR of the chunk position in LDS row r.
+  // XOR of the chunk position in LDS row r.  A 16-byte read serves lanes 0-3,
+  // 12-15 and 20-27 at once, then 4-11, 16-19 and 28-31: with four chunks to a
+  // row, rows 4 a .. 4 a + 3 of the first chunk at a = 0 and 3 meet those of the
+  // second at a = 1 and 2, which XOR by -a keeps apart (by a, half of all reads
+  // conflicted).
   static __device__ __forceinline__ u32 key(u32 r) {
     if constexpr (L == kKC && BK == 128) return r & 15u;
     else if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
-    else if constexpr (L == kKC) return (r >> 2) & 3u;
+    else if constexpr (L == kKC) return (0u - (r >> 2)) & 3u;
     else if constexpr (W == 1) return (((r >> 1) & 1u) | ((r >> 3) & 1u) << 1) << 1;  // 128-byte rows: two per turn of the banks
     else return ((r & 3u) | ((r >> 3) & 1u) << 2) << 1;
   }

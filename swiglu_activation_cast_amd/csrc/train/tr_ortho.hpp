@@ -32,7 +32,7 @@ typedef _Float16 h4_t __attribute__((ext_vector_type(4)));
 
 constexpr float kXScale = 16384.0f;  // 2^14: singular values up to 2 stay below fp16's 65504
 constexpr float kSScale = 8192.0f;   // 2^13
-constexpr int kNormBlocks = 128;     // workgroups that share one matrix's sum of squares
+constexpr int kNormBlocks = 512;     // workgroups that share one matrix's sum of squares
 
 struct NsArgs {
   const void *g;

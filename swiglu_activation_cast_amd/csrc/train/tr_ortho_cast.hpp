@@ -29,6 +29,11 @@ __device__ __forceinline__ void ns_load8(const NsArgs &n, int64_t row, int64_t c
   }
 }
 
+// Chunk i of rows of `cpr` chunks: its row (the short division where it does).
+__device__ __forceinline__ int64_t ns_row(int64_t i, int64_t cpr) {
+  return ((uint64_t)i >> 32) == 0 ? (int64_t)((u32)i / (u32)cpr) : i / cpr;
+}
+
 // Sum over the workgroup's 256 threads, in every thread.
 __device__ __forceinline__ double block_sum(double v, double *sm) {
 #pragma unroll
@@ -45,7 +50,7 @@ __global__ __launch_bounds__(256) void k_ns_norm(const NsArgs n) {
   const int64_t cpr = (n.cols + 7) / 8, total = n.rows * cpr, batch = blockIdx.y;
   double s = 0.0;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)kNormBlocks * 256) {
-    const int64_t row = i / cpr;
+    const int64_t row = ns_row(i, cpr);
     float v[8];
     ns_load8(n, row, (i - row * cpr) * 8, batch, v);
 #pragma unroll
@@ -59,14 +64,16 @@ __global__ __launch_bounds__(256) void k_ns_norm(const NsArgs n) {
 __global__ __launch_bounds__(256) void k_ns_cast(const NsArgs n) {
   __shared__ double sm[4];
   const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
-  double norm = threadIdx.x < kNormBlocks ? *gptr(n.sums + batch * kNormBlocks + threadIdx.x) : 0.0;
+  double norm = 0.0;
+#pragma unroll
+  for (int p = 0; p < kNormBlocks; p += 256) norm += *gptr(n.sums + batch * kNormBlocks + p + threadIdx.x);
   norm = sqrt(block_sum(norm, sm)) + n.eps;
   // 2^e with norm 2^e in [1/2, 1); 0 or not finite: no scaling (phi carries it)
   int ex = 0;
   if (norm > 0.0 && norm < 1e300) frexp(norm, &ex);
   if (blockIdx.x == 0 && threadIdx.x == 0) *gptr(n.phi + batch) = (float)(1.0 / ldexp(norm, -ex));
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpr, col = (i - row * cpr) * 8;
+    const int64_t row = ns_row(i, cpr), col = (i - row * cpr) * 8;
     float v[8];
     ns_load8(n, row, col, batch, v);
     typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
@@ -89,7 +96,7 @@ __global__ __launch_bounds__(256) void k_ns_plain(const NsArgs n, void *out, int
   const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;
   const float f = *gptr(n.phi + batch) / kXScale;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-    const int64_t row = i / cpr, col = (i - row * cpr) * 8, at = batch * n.stride_x + row * n.ld_x + col;
+    const int64_t row = ns_row(i, cpr), col = (i - row * cpr) * 8, at = batch * n.stride_x + row * n.ld_x + col;
     for (int j = 0; j < 8 && col + j < n.cols; j++) {
       const float v = ((float)*gptr(n.x + at + j) + (n.x_lo ? (float)*gptr(n.x_lo + at + j) : 0.0f)) * f;
       const int64_t o = batch * stride + row * ld + col + j;

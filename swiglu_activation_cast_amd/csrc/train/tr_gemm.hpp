@@ -52,6 +52,12 @@ namespace mxt {
 
 
 
+// Loads [FROM, TO) of a stage.
+template <int FROM, int TO>
+struct Part {
+  static constexpr int from = FROM, to = TO;
+};
+
 enum Layout { kKC = 0, kMC = 1 };
 enum Mode { kBatch = 0, kGroupM = 1, kGroupK = 2 };
 enum Elem { kBf16 = 0, kF16 = 1 };
@@ -341,7 +347,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   // spread evenly.  (Loads over the whole stage leave the last of them too
   // little time to land, 10% slower; packed more densely they queue, 5%.)
   auto phase = [&](auto do_mfma, auto loads, auto n_reads, u32x4_t *fa, u32x4_t *fb, const Src &src, auto &&read) {
-    constexpr int Q = decltype(loads)::value ? kLoads : 0, R = decltype(n_reads)::value;
+    constexpr int q0 = decltype(loads)::from, Q = decltype(loads)::to - q0, R = decltype(n_reads)::value;
     constexpr int kEvery = R * 2 <= kMfmas ? 2 : 1, kPer = (R + kMfmas - 1) / kMfmas;
     static_for<kMfmas>([&](auto kk) {
       constexpr int k = decltype(kk)::value, i = k / WB, j = k % WB;
@@ -352,7 +358,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
           if (n < R) read(n);
       }
       static_for<(k + 1) * Q / kMfmas - k * Q / kMfmas>(
-          [&](auto q) { load(std::integral_constant<int, k * Q / kMfmas + decltype(q)::value>{}, src); });
+          [&](auto q) { load(std::integral_constant<int, q0 + k * Q / kMfmas + decltype(q)::value>{}, src); });
       __builtin_amdgcn_sched_barrier(0);  // keep this order
     });
   };
@@ -378,7 +384,8 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   auto stage = [&](auto has_last, int st) {
     const MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
     constexpr bool first = !decltype(has_last)::value;
-    using Loads = std::integral_constant<bool, !first>;
+    constexpr int kAll = first ? 0 : kLoads;
+    constexpr int kCut = kAll * 2 / 3;  // SPLIT, whose phases are longer: two thirds in the first, the rest in the second
     // the loads of the stage that takes over stage st - 1's slot
     const Src src = first ? Src{} : source(st - 1 + RING);
     if constexpr (SPLIT) {
@@ -388,16 +395,18 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
 #pragma unroll
       for (int s = 0; s < kKS; s++) {
         auto rd = [&](int n) { read_ab(slot, slot + kSlotB + B::kBytes, s, n, fa[0], fb[1]); };
-        if (s == 0) phase(has_last, Loads{}, NAB{}, fa[1], fb[0], src, rd);
-        else phase(Yes{}, No{}, NAB{}, fa[1], fb[0], src, rd);
-        phase(Yes{}, No{}, NB{}, fa[0], fb[1], src, [&](int n) { ob.read(slot + kSlotB, s, n, 1, fb[0]); });
-        phase(Yes{}, No{}, NA{}, fa[0], fb[0], src, [&](int n) { oa.read(slot + A::kBytes, s, n, 2, fa[1]); });
+        auto rdb = [&](int n) { ob.read(slot + kSlotB, s, n, 1, fb[0]); };
+        if (s == 0) phase(has_last, Part<0, kCut>{}, NAB{}, fa[1], fb[0], src, rd);
+        else phase(Yes{}, Part<0, 0>{}, NAB{}, fa[1], fb[0], src, rd);
+        if (s == 0) phase(Yes{}, Part<kCut, kAll>{}, NB{}, fa[0], fb[1], src, rdb);
+        else phase(Yes{}, Part<0, 0>{}, NB{}, fa[0], fb[1], src, rdb);
+        phase(Yes{}, Part<0, 0>{}, NA{}, fa[0], fb[0], src, [&](int n) { oa.read(slot + A::kBytes, s, n, 2, fa[1]); });
       }
     } else {
-      phase(has_last, Loads{}, NAB{}, fa[1], fb[1], src, [&](int n) { read_ab(slot, slot + kSlotB, 0, n, fa[0], fb[0]); });
+      phase(has_last, Part<0, kAll>{}, NAB{}, fa[1], fb[1], src, [&](int n) { read_ab(slot, slot + kSlotB, 0, n, fa[0], fb[0]); });
 #pragma unroll
       for (int s = 1; s < kKS; s++)
-        phase(Yes{}, No{}, NAB{}, fa[(s + 1) & 1], fb[(s + 1) & 1], src,
+        phase(Yes{}, Part<0, 0>{}, NAB{}, fa[(s + 1) & 1], fb[(s + 1) & 1], src,
               [&](int n) { read_ab(slot, slot + kSlotB, s, n, fa[s & 1], fb[s & 1]); });
     }
 #if __HIP_DEVICE_COMPILE__

@@ -58,7 +58,7 @@ __device__ __forceinline__ void split_f16(float v, _Float16 &hi, _Float16 &lo) {
   lo = (_Float16)(v - (float)hi);
 }
 
-enum NsStep { kGram = 0, kPoly = 1, kNext = 2, kLast = 3 };
+enum NsStep { kGram = 0, kPoly = 1, kNext = 2, kLast = 3, kPart = 4 };  // kPart: a part of S's sum over K
 
 struct NsGemm {
   GemmArgs g;  // a, b: high planes; c: the result's high plane, or the output
@@ -68,6 +68,8 @@ struct NsGemm {
   const float *phi;          // per matrix, or NULL (1)
   float ca, cb, cc;          // kPoly: coefficients times p's scale, b and c over S's scales
   float scale;               // the other steps: of the sums
+  int32_t parts;             // kPart: pieces of K, `part_k` of it each (g.c: fp32 sums, g.stride_c apart)
+  int64_t part_k;
 };
 
 // One step's results at a tile: fp16 planes (high, and low where SPLIT).
@@ -132,6 +134,26 @@ struct EmitLast : EmitC<F32> {
   }
 };
 
+// S from the partial sums of its lower tiles of 64 x 64, in order: a long
+// thin matrix has too few tiles of S to fill the card, so K is dealt to several
+// workgroups.  A thread takes one element.
+template <bool SPLIT>
+__global__ __launch_bounds__(256) void k_ns_join(const NsGemm p) {
+  const GemmArgs &g = p.g;  // a: unused; c: the sums
+  const int64_t batch = blockIdx.y, s = g.M, ld = g.ldc;
+  const float *sums = static_cast<const float *>(g.c) + batch * p.parts * g.stride_c;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < s * s; i += (int64_t)gridDim.x * 256) {
+    const int64_t m = i / s, n = i - m * s;
+    const int64_t at = m / 64 >= n / 64 ? m * ld + n : n * ld + m;
+    float v = 0.0f;
+    for (int k = 0; k < p.parts; k++) v += *gptr(sums + k * g.stride_c + at);
+    _Float16 hi, lo;
+    split_f16(v * p.scale, hi, lo);
+    *gptr(const_cast<_Float16 *>(p.s) + batch * g.stride_c + m * ld + n) = hi;
+    if constexpr (SPLIT) *gptr(const_cast<_Float16 *>(p.s_lo) + batch * g.stride_c + m * ld + n) = lo;
+  }
+}
+
 // Position L in row order of the tiles on and below the diagonal.
 __device__ __forceinline__ void lower_tile(u32 L, u32 &tm, u32 &tn) {
   tm = (u32)((sqrtf(8.0f * (float)L + 1.0f) - 1.0f) * 0.5f);
@@ -143,7 +165,7 @@ __device__ __forceinline__ void lower_tile(u32 L, u32 &tm, u32 &tn) {
 template <int STEP, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT>
 __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
-  constexpr bool SYM = STEP == kGram || STEP == kPoly;
+  constexpr bool SYM = STEP == kGram || STEP == kPoly || STEP == kPart;
   static_assert(!SYM || WI == WJ, "symmetric results take square tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * (SPLIT ? 4 : 2)];
   const GemmArgs &g = p.g;
@@ -152,12 +174,13 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   // symmetric ones, whose tiles are square, do not)
   constexpr bool kCut = !SYM && WI == 4 && WJ == 4;
   Item it{blockIdx.x, 0, 1};
-  const u32 R = tiles * (u32)g.G;
+  const u32 R = tiles * (u32)g.G * (STEP == kPart ? (u32)p.parts : 1u);
   if (kCut && !work_item(blockIdx.x, R, (u32)g.cus, it)) return;
   const u32 whole = kCut ? R - R % (u32)g.cus : R;
   // matrices of fewer tiles than the CUs compute together: whole ones to an XCD
   const u32 L = !SYM && tiles >= 256 ? square_order(it.L, whole) : it.L < whole ? xcd_remap(it.L, whole) : it.L;
-  const int64_t batch = L / tiles;
+  // kPart: matrix `entry` of the partial sums is part entry % parts of matrix batch
+  const int64_t entry = L / tiles, batch = STEP == kPart ? entry / p.parts : entry;
   u32 tm, tn;
   if constexpr (SYM) lower_tile(L % tiles, tm, tn);
   else tile_of(L % tiles, (u32)g.tiles_m, (u32)g.tiles_n, tm, tn);
@@ -165,9 +188,15 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   tn = (u32)__builtin_amdgcn_readfirstlane((int)tn);
   const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BN + it.part * (BN / it.parts);
   if (n0 >= g.N) return;  // a part past the last column
-  const int64_t a_at = batch * g.stride_a + (AL == kKC ? m0 * g.lda : m0);
-  const int64_t b_at = batch * g.stride_b + (BL == kKC ? n0 * g.ldb : n0);
-  Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, g.K, (u32)min<int64_t>(BM, g.M - m0),
+  int64_t k0 = 0, k_len = g.K;
+  if constexpr (STEP == kPart) {
+    k0 = entry % p.parts * p.part_k;
+    k_len = max<int64_t>(min<int64_t>(g.K - k0, p.part_k), 0);
+    if (k_len == 0) k0 = 0;
+  }
+  const int64_t a_at = batch * g.stride_a + (AL == kKC ? m0 * g.lda + k0 : m0 + k0 * g.lda);
+  const int64_t b_at = batch * g.stride_b + (BL == kKC ? n0 * g.ldb + k0 : n0 + k0 * g.ldb);
+  Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, k_len, (u32)min<int64_t>(BM, g.M - m0),
          (u32)min<int64_t>(BN / it.parts, g.N - n0), 0};
   if constexpr (SPLIT) {
     t.a_lo = p.a_lo + a_at;
@@ -181,8 +210,10 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     }
     gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
   };
-  const int64_t at = batch * g.stride_c + m0 * g.ldc + n0;
-  if constexpr (STEP == kLast) {
+  const int64_t at = entry * g.stride_c + m0 * g.ldc + n0;
+  if constexpr (STEP == kPart) {
+    run(EmitC<true>{static_cast<float *>(g.c) + at, g.ldc, t.cols, true});
+  } else if constexpr (STEP == kLast) {
     EmitLast<SPLIT> e{};
     e.c = SPLIT ? (void *)(static_cast<float *>(g.c) + at) : (void *)(static_cast<uint16_t *>(g.c) + at);
     e.ldc = g.ldc;

@@ -16,6 +16,8 @@ struct NsPlan {
   int64_t s;             // the shorter side
   int64_t ld_x, stride_x, ld_s, stride_s;
   int64_t x[2][2], sq[2][2];  // byte offsets: [which][plane]; sq: S, p(S)
+  int parts;                  // pieces of K that S's products are dealt in (1: whole)
+  int64_t part_sums;          // byte offset of their fp32 sums
   int64_t sums, phi, bytes;   // bytes < 0: too large
 };
 
@@ -42,6 +44,13 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int out_dtype) {
       p.x[which][plane] = take(p.stride_x, 2);
       p.sq[which][plane] = take(p.stride_s, 2);
     }
+  // S of at most 16 tiles of 64 x 64 leaves most CUs idle: over 40 stages of K or
+  // more it is dealt to as many as 16 workgroups a tile, at least four stages
+  // each (five steps of 2 x 6881 x 95 bf16: 152 us, 212 without; fp32 168 and
+  // 336; of 8 x 64 x 2048 bf16, 32 stages, 94 and 92).
+  const int64_t ts = (p.s + 63) / 64, tiles = ts * (ts + 1) / 2 * batch, stages = (std::max(m, n) + 63) / 64;
+  p.parts = tiles <= 16 && stages >= 40 ? (int)std::min<int64_t>({16, 256 / tiles, stages / 4}) : 1;
+  p.part_sums = p.parts > 1 ? take(p.stride_s * p.parts, 4) : 0;
   p.sums = take(mxt::kNormBlocks, 8);
   p.phi = take(1, 4);
   p.bytes = ok ? at : -1;
@@ -88,6 +97,30 @@ mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
                   : b == 128 ? (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 2, 2, SPLIT ? 32 : 64, 2, SPLIT>
                              : (const void *)&mxt::k_ns_gemm<STEP, AL, BL, 1, 1, 64, SPLIT ? 4 : 8, SPLIT>;
   return launch(k, blocks, mxt::kThreads, p, stream);
+}
+
+// S in parts of K, and their join.
+template <int AL, bool SPLIT>
+mxtrain_status ns_gram_parts(mxt::NsGemm p, const NsPlan &pl, int64_t batch, uint8_t *ws, void *stream) {
+  const int64_t stages = (p.g.K + 63) / 64;
+  p.s = static_cast<const _Float16 *>(p.g.c);
+  p.s_lo = p.c_lo;
+  p.g.c = ws + pl.part_sums;
+  p.parts = pl.parts;
+  p.part_k = (stages + pl.parts - 1) / pl.parts * 64;
+  p.g.tiles_m = p.g.tiles_n = (int32_t)((pl.s + 63) / 64);
+  p.g.G = (int32_t)batch;
+  p.g.cus = cu_count();
+  const int64_t blocks = batch * pl.parts * (int64_t)p.g.tiles_m * (p.g.tiles_m + 1) / 2;
+  const mxtrain_status st =
+      launch((const void *)&mxt::k_ns_gemm<mxt::kPart, AL, AL, 1, 1, 64, SPLIT ? 4 : 8, SPLIT>, blocks, mxt::kThreads, p, stream);
+  if (st != MXTRAIN_OK) return st;
+  void *kargs[] = {&p};
+  const int64_t grid = std::min<int64_t>((pl.s * pl.s + 255) / 256, std::max<int64_t>(1, 2048 / batch));
+  return hipLaunchKernel((const void *)&mxt::k_ns_join<SPLIT>, dim3((unsigned)grid, (unsigned)batch), dim3(256), kargs,
+                         0, (hipStream_t)stream) == hipSuccess
+             ? MXTRAIN_OK
+             : MXTRAIN_ERR_LAUNCH;
 }
 
 template <bool SPLIT>
@@ -151,8 +184,12 @@ mxtrain_status ns_run(const NsPlan &pl, mxt::NsArgs n, int64_t batch, int64_t m,
     next.phi = step == 0 ? n.phi : nullptr;
     next.scale = (last ? 1.0f / mxt::kXScale : 1.0f) / ps;
     using namespace mxt;
-    st = pl.tall ? ns_gemm<kGram, kMC, kMC, SPLIT>(gram, batch, stream)
-                 : ns_gemm<kGram, kKC, kKC, SPLIT>(gram, batch, stream);
+    if (pl.parts > 1)
+      st = pl.tall ? ns_gram_parts<kMC, SPLIT>(gram, pl, batch, ws, stream)
+                   : ns_gram_parts<kKC, SPLIT>(gram, pl, batch, ws, stream);
+    else
+      st = pl.tall ? ns_gemm<kGram, kMC, kMC, SPLIT>(gram, batch, stream)
+                   : ns_gemm<kGram, kKC, kKC, SPLIT>(gram, batch, stream);
     if (st == MXTRAIN_OK) st = ns_gemm<kPoly, kKC, kKC, SPLIT>(poly, batch, stream);
     if (st == MXTRAIN_OK) {
       if (last)

@@ -91,6 +91,17 @@ def test_against_definition(batch, m, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("batch,m,n", [(2, 3001, 70), (1, 60, 5003), (1, 200, 1090), (3, 1024, 33), (1, 1, 4099), (20, 40, 1100)])
+def test_long_thin_matrices(batch, m, n, dtype):
+    """S's products dealt in parts of K, the last of them shorter or empty."""
+    g = matrix(batch, m, n, dtype, m + 2 * n)
+    for steps in (1, 3):
+        out = mx.mxtrain_newton_schulz(g, steps=steps)
+        check(out, g, steps)
+    assert torch.equal(out, mx.mxtrain_newton_schulz(g, steps=3))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("m,n", [(2304, 4100), (4360, 2200)])
 def test_large_tiles(m, n, dtype):
     """Sizes that run 256 x 256 tiles, cut off on every side."""

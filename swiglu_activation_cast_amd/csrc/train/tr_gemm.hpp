@@ -59,7 +59,7 @@ struct Part {
 };
 
 enum Layout { kKC = 0, kMC = 1 };
-enum Mode { kBatch = 0, kGroupM = 1, kGroupK = 2 };
+enum Mode { kGroupM = 1, kGroupK = 2 };
 enum Elem { kBf16 = 0, kF16 = 1 };
 
 constexpr int kThreads = 256;
@@ -163,8 +163,7 @@ struct Operand {
   // second at a = 1 and 2, which XOR by -a keeps apart (by a, half of all reads
   // conflicted).
   static __device__ __forceinline__ u32 key(u32 r) {
-    if constexpr (L == kKC && BK == 128) return r & 15u;
-    else if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
+    if constexpr (L == kKC && BK == 64) return (r >> 1) & 7u;
     else if constexpr (L == kKC) return (0u - (r >> 2)) & 3u;
     else if constexpr (W == 1) return (((r >> 1) & 1u) | ((r >> 3) & 1u) << 1) << 1;  // 128-byte rows: two per turn of the banks
     else return ((r & 3u) | ((r >> 3) & 1u) << 2) << 1;

@@ -46,24 +46,6 @@ struct LnArgs {
 // column (i * TPR + t) * VEC.  VEC is 16 bytes' worth where every row starts
 // 16-byte aligned and N is a multiple of it, otherwise 1.
 template <class T, int VEC>
-__device__ __forceinline__ void load_chunk(const T *p, float *v) {
-  if constexpr (VEC == 1) {
-    v[0] = to_f32(*gptr(p));
-  } else if constexpr (sizeof(T) == 2) {
-    const u32x4_t q = *gptr(reinterpret_cast<const u32x4_t *>(p));
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-      v[2 * i] = mx::lo_f(q[i]);
-      v[2 * i + 1] = mx::hi_f(q[i]);
-    }
-  } else {
-    const f32x4_t q = *gptr(reinterpret_cast<const f32x4_t *>(p));
-#pragma unroll
-    for (int i = 0; i < 4; i++) v[i] = q[i];
-  }
-}
-
-template <class T, int VEC>
 __device__ __forceinline__ void store_chunk(T *p, const float *v) {
   if constexpr (VEC == 1) {
     *gptr(p) = from_f32<T>(v[0]);

@@ -134,8 +134,9 @@ mxtrain_status mxtrain_grouped_gemm_k(const void *a, int64_t lda, const void *b,
  *         aligned.
  * Requires that the steps keep the singular values at most 2 (they start at
  * most 1); a step that leads past that overflows to infinities or NaN.  An
- * fp32 result is computed to about fp32's accuracy, a bf16 result with 11
- * significant bits between the products.  A matrix with NaN or infinite
+ * fp32 result is computed to about fp32's accuracy; for a bf16 result X is
+ * held with 22 significant bits between the products, S = X X^T and the
+ * polynomial of it with 11.  A matrix with NaN or infinite
  * entries gives NaN everywhere (steps >= 1); the others of the batch are not
  * touched by it.  A zero matrix gives zeros where eps > 0.
  * Any dimensions (the odd ones and single rows among them) and strides;

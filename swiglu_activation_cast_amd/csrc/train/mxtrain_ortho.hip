@@ -55,7 +55,9 @@ mxtrain_status mxtrain_newton_schulz(const void *g, int64_t ld_g, int64_t stride
   a.sums = reinterpret_cast<double *>(ws + pl.sums);
   a.phi = reinterpret_cast<float *>(ws + pl.phi);
   a.x = reinterpret_cast<_Float16 *>(ws + pl.x[0][0]);
-  a.x_lo = pl.split ? reinterpret_cast<_Float16 *>(ws + pl.x[0][1]) : nullptr;
+  // bf16's eight places fit the high plane: below fp16's normal range, where
+  // they do not, the low plane would be zero too
+  a.x_lo = pl.split || a.g_f32 ? reinterpret_cast<_Float16 *>(ws + pl.x[0][1]) : nullptr;
   a.ld_x = pl.ld_x;
   a.stride_x = pl.stride_x;
   void *kargs[] = {&a};

@@ -249,16 +249,20 @@ struct Operand {
 
 // What a tile's workgroup computes: `rows` x `cols` of C over `k_len` of K from
 // the operands' bases.  With SPLIT, A and B each come as a high and a low plane
-// and the sum runs over high x low, high x high and low x high.
+// and the sum runs over high x low, high x high and low x high.  With TWICE, K is
+// gone through twice where `passes` is 2: over a_lo and b_lo, then over a and b
+// (an operand of one plane gives it as both), so that one operand's low plane
+// enters with no other change to a stage.
 struct Tile {
   const uint16_t *a, *b;        // at the tile's first row (column) and k
-  const uint16_t *a_lo, *b_lo;  // SPLIT
+  const uint16_t *a_lo, *b_lo;  // SPLIT, TWICE
   int64_t k_len;
   u32 rows, cols;
-  u32 first;                    // any number: which stage of K (modulo them) comes first
+  u32 first;                    // any number: which stage of K (modulo them) comes first (not with TWICE)
+  int32_t passes;               // TWICE: 1 or 2
 };
 
-template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, class Emit>
+template <int EL, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT, bool TWICE = false, class Emit>
 __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint8_t *smem, const Emit &emit) {
   using A = Operand<AL, WI, BK>;
   using B = Operand<BL, WJ, BK>;
@@ -285,13 +289,15 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
 #pragma unroll
     for (int j = 0; j < WB; j++) acc[i][j] = f32x4_t{};
 
-  const int n_stage = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));
-  const int k_tail = (int)(t.k_len - (int64_t)(n_stage - 1) * kBK);  // k in the last stage, 1 .. kBK
+  static_assert(!(SPLIT && TWICE), "two ways to take a low plane");
+  const int n_pass = __builtin_amdgcn_readfirstlane((int)((t.k_len + kBK - 1) / kBK));  // stages of K
+  const int n_stage = TWICE ? n_pass * __builtin_amdgcn_readfirstlane(t.passes) : n_pass;
+  const int k_tail = (int)(t.k_len - (int64_t)(n_pass - 1) * kBK);  // k in K's last stage, 1 .. kBK
   MXT_LDS uint8_t *lds = (MXT_LDS uint8_t *)smem;
   const u32 lds0 = lds_addr(smem);
 
   const uint8_t *a_lo = nullptr, *b_lo = nullptr;
-  if constexpr (SPLIT) {
+  if constexpr (SPLIT || TWICE) {
     a_lo = uniform(reinterpret_cast<const uint8_t *>(t.a_lo));
     b_lo = uniform(reinterpret_cast<const uint8_t *>(t.b_lo));
   }
@@ -302,20 +308,25 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   int kmax = kBK;  // of the stages being loaded
   oa.set_kmax(kmax);
   ob.set_kmax(kmax);
-  // The stages of K in turn, from t.first on.
-  const int rot = n_stage > 0 ? __builtin_amdgcn_readfirstlane((int)(t.first % (u32)n_stage)) : 0;
-  auto place = [&](int st) { return st + rot < n_stage ? st + rot : st + rot - n_stage; };
+  // The stages of K in turn, from t.first on; with TWICE, the last n_pass of them
+  // are the high planes'.
+  const int rot = !TWICE && n_stage > 0 ? __builtin_amdgcn_readfirstlane((int)(t.first % (u32)n_stage)) : 0;
+  auto high = [&](int st) { return !TWICE || st >= n_stage - n_pass; };
+  auto place = [&](int st) {
+    if constexpr (TWICE) return high(st) ? st - (n_stage - n_pass) : st;
+    else return st + rot < n_stage ? st + rot : st + rot - n_stage;
+  };
   // Stages past the last re-read it into a slot that is not read again.
   auto source = [&](int st) {
-    const int s = place(min(st, n_stage - 1));
+    const int at = min(st, n_stage - 1), s = place(at);
     Src r;
-    r.a[0] = oa.base + s * oa.step;
-    r.b[0] = ob.base + s * ob.step;
+    r.a[0] = (high(at) ? oa.base : a_lo) + s * oa.step;
+    r.b[0] = (high(at) ? ob.base : b_lo) + s * ob.step;
     r.a[1] = SPLIT ? a_lo + s * oa.step : nullptr;
     r.b[1] = SPLIT ? b_lo + s * ob.step : nullptr;
     r.slot_a = lds0 + (u32)(st % RING) * kSlot + oa.lds_w;
     r.slot_b = lds0 + (u32)(st % RING) * kSlot + kSlotB + ob.lds_w;
-    const int k = s == n_stage - 1 ? k_tail : kBK;
+    const int k = s == n_pass - 1 ? k_tail : kBK;
     if (k != kmax) {  // uniform; only around a partial last stage
       kmax = k;
       oa.set_kmax(k);
@@ -330,7 +341,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs &g, const Tile &t, uint
   };
   // Stage st has landed: clear what lies past K (each lane what it loaded).
   auto clear = [&](int st) {
-    if (k_tail == kBK || st >= n_stage || place(st) != n_stage - 1) return;
+    if (k_tail == kBK || st >= n_stage || place(st) != n_pass - 1) return;
     MXT_LDS uint8_t *slot = lds + (st % RING) * kSlot;
 #pragma unroll
     for (int p = 0; p < kPl; p++) {

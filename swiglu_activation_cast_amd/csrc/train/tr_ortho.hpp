@@ -13,11 +13,19 @@
 // Number format.  X, S and p(S) are held between the products as fp16 times a
 // power of two (their entries are bounded, since the singular values are: X by
 // 2^14, S by 2^13, p(S) by a power that keeps its largest possible entry in
-// range).  fp16's 11 places cost a bf16 result nothing that shows beside its
-// own 8.  For an fp32 result each is held as two fp16 numbers, high and low
+// range).  For an fp32 result each is held as two fp16 numbers, high and low
 // part, 22 places, and a product is the sum of high x low, low x high and
 // high x high (low x low lies below 2^-22): three matrix-core passes, where
 // an fp32 product on this card runs at less than a tenth of the 16-bit rate.
+//
+// For a bf16 result S and p(S) have one part, but X two, of which S is taken
+// from the high one and p(S) X from both (K gone through twice).  An error of
+// S or p(S) only moves X within its own row space (columns, if tall), by
+// fp16's 2^-11 beside bf16's 2^-8; one of X lies anywhere, and outside X's
+// space it grows by p(s) / s, 3.4445 a step for the usual quintic: with one part
+// of X the result of a 512 x 1024 matrix of rank 4, 32 or 128 is off by 4.3, 2.2
+// or 1.1% (Frobenius), with two by 0.2%, full rank or not (an fp32 run rounded
+// at its end: 0.17%; all in 64-bit emulation).
 //
 // The first X is G times a power of two 2^e with (|G| + eps) 2^e in [1/2, 1),
 // which is exact for bf16 input; the factor that is left, phi = 1 / ((|G| +
@@ -68,15 +76,16 @@ struct NsGemm {
   const float *phi;          // per matrix, or NULL (1)
   float ca, cb, cc;          // kPoly: coefficients times p's scale, b and c over S's scales
   float scale;               // the other steps: of the sums
+  int32_t passes;            // one plane, kNext and kLast: 2 where X has a low plane (see Tile)
   int32_t parts;             // kPart: pieces of K, `part_k` of it each (g.c: fp32 sums, g.stride_c apart)
   int64_t part_k;
 };
 
-// One step's results at a tile: fp16 planes (high, and low where SPLIT).
-template <int STEP, bool SPLIT>
+// One step's results at a tile: fp16 planes (high, and low where TWO).
+template <int STEP, bool TWO>
 struct EmitNs {
   static constexpr bool kF32 = false, kMirror = STEP != kNext;
-  static constexpr int kPlanes = SPLIT ? 2 : 1;
+  static constexpr int kPlanes = TWO ? 2 : 1;
   _Float16 *out[2];             // at the tile
   _Float16 *mir[2];             // at the transposed tile, or NULL
   const _Float16 *s_hi, *s_lo;  // kPoly: S at the tile
@@ -93,7 +102,7 @@ struct EmitNs {
       const int64_t at = m < rows && n < cols ? (int64_t)m * ld + n : 0;
       const h4_t s = *gptr(reinterpret_cast<const h4_t *>(s_hi + at));
       h4_t sl = {};
-      if constexpr (SPLIT) sl = *gptr(reinterpret_cast<const h4_t *>(s_lo + at));
+      if constexpr (TWO) sl = *gptr(reinterpret_cast<const h4_t *>(s_lo + at));
 #pragma unroll
       for (u32 e = 0; e < 4; e++) {
         const float sv = (float)s[e] + (float)sl[e];
@@ -112,7 +121,7 @@ struct EmitNs {
       b[e] = y;
     }
     p[0] = __builtin_bit_cast(u32x2_t, a);
-    if constexpr (SPLIT) p[1] = __builtin_bit_cast(u32x2_t, b);
+    if constexpr (TWO) p[1] = __builtin_bit_cast(u32x2_t, b);
   }
   // Rows are padded to whole chunks of 8, which all fit.
   __device__ __forceinline__ void store(int k, u32 m, u32 n, u32x4_t v) const {
@@ -166,6 +175,7 @@ template <int STEP, int AL, int BL, int WI, int WJ, int BK, int RING, bool SPLIT
 __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   constexpr int BM = 64 * WI, BN = 64 * WJ;
   constexpr bool SYM = STEP == kGram || STEP == kPoly || STEP == kPart;
+  constexpr bool TWICE = !SPLIT && (STEP == kNext || STEP == kLast);  // p(S) times X's planes in turn
   static_assert(!SYM || WI == WJ, "symmetric results take square tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t smem[RING * (BM + BN) * BK * (SPLIT ? 4 : 2)];
   const GemmArgs &g = p.g;
@@ -197,18 +207,18 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
   const int64_t a_at = batch * g.stride_a + (AL == kKC ? m0 * g.lda + k0 : m0 + k0 * g.lda);
   const int64_t b_at = batch * g.stride_b + (BL == kKC ? n0 * g.ldb + k0 : n0 + k0 * g.ldb);
   Tile t{g.a + a_at, g.b + b_at, nullptr, nullptr, k_len, (u32)min<int64_t>(BM, g.M - m0),
-         (u32)min<int64_t>(BN / it.parts, g.N - n0), 0};
-  if constexpr (SPLIT) {
+         (u32)min<int64_t>(BN / it.parts, g.N - n0), 0, p.passes};
+  if constexpr (SPLIT || TWICE) {
     t.a_lo = p.a_lo + a_at;
     t.b_lo = p.b_lo + b_at;
   }
   const float phi = p.phi ? *gptr(p.phi + batch) : 1.0f;
   auto run = [&](const auto &e) {
     if constexpr (kCut) {
-      if (it.parts == 4) return gemm_tile<kF16, AL, BL, WI, 1, BK, RING, SPLIT>(g, t, smem, e);
-      if (it.parts == 2) return gemm_tile<kF16, AL, BL, WI, 2, BK, RING, SPLIT>(g, t, smem, e);
+      if (it.parts == 4) return gemm_tile<kF16, AL, BL, WI, 1, BK, RING, SPLIT, TWICE>(g, t, smem, e);
+      if (it.parts == 2) return gemm_tile<kF16, AL, BL, WI, 2, BK, RING, SPLIT, TWICE>(g, t, smem, e);
     }
-    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT>(g, t, smem, e);
+    gemm_tile<kF16, AL, BL, WI, WJ, BK, RING, SPLIT, TWICE>(g, t, smem, e);
   };
   const int64_t at = entry * g.stride_c + m0 * g.ldc + n0;
   if constexpr (STEP == kPart) {
@@ -222,16 +232,17 @@ __global__ __launch_bounds__(kThreads, 1) void k_ns_gemm(const NsGemm p) {
     e.f0 = p.scale * phi;
     run(e);
   } else {
-    EmitNs<STEP, SPLIT> e{};
+    constexpr bool TWO = SPLIT || STEP == kNext;
+    EmitNs<STEP, TWO> e{};
     e.ld = g.ldc;
     e.rows = t.rows;
     e.cols = t.cols;
     e.out[0] = static_cast<_Float16 *>(g.c) + at;
-    if (SPLIT) e.out[1] = p.c_lo + at;
+    if (TWO) e.out[1] = p.c_lo + at;
     if (SYM && tm != tn) {
       const int64_t mir = batch * g.stride_c + n0 * g.ldc + m0;
       e.mir[0] = static_cast<_Float16 *>(g.c) + mir;
-      if (SPLIT) e.mir[1] = p.c_lo + mir;
+      if (TWO) e.mir[1] = p.c_lo + mir;
     }
     if constexpr (STEP == kPoly) {
       e.s_hi = p.s + at;

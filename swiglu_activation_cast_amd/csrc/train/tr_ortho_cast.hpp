@@ -60,7 +60,7 @@ __global__ __launch_bounds__(256) void k_ns_norm(const NsArgs n) {
   if (threadIdx.x == 0) *gptr(n.sums + batch * kNormBlocks + blockIdx.x) = s;
 }
 
-// X_0's fp16 form (both planes where x_lo is given) and phi.
+// X_0's fp16 form (both planes where x_lo is given: not for bf16 G and result) and phi.
 __global__ __launch_bounds__(256) void k_ns_cast(const NsArgs n) {
   __shared__ double sm[4];
   const int64_t cpr = n.ld_x / 8, total = n.rows * cpr, batch = blockIdx.y;

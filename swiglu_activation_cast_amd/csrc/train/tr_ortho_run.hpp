@@ -9,8 +9,8 @@
 namespace mxt {
 
 // ------------------------------------------------------- orthogonalisation
-// Workspace: the fp16 planes of X (two, in turn), S and p(S), then the sums
-// of squares and phi.  Every part starts at a multiple of 256 bytes.
+// Workspace: the fp16 planes of X (two of them, high and low, twice, in turn), S and p(S)
+// (low planes for fp32 results only), then the sums of squares and phi.  Every part starts at a multiple of 256 bytes.
 struct NsPlan {
   bool split, tall;
   int64_t s;             // the shorter side
@@ -40,9 +40,9 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int out_dtype) {
     return here;
   };
   for (int which = 0; which < 2; which++)
-    for (int plane = 0; plane < (p.split ? 2 : 1); plane++) {
+    for (int plane = 0; plane < 2; plane++) {
       p.x[which][plane] = take(p.stride_x, 2);
-      p.sq[which][plane] = take(p.stride_s, 2);
+      if (plane == 0 || p.split) p.sq[which][plane] = take(p.stride_s, 2);
     }
   // S of at most 16 tiles of 64 x 64 leaves most CUs idle: over 40 stages of K or
   // more it is dealt to as many as 16 workgroups a tile, at least four stages
@@ -136,7 +136,7 @@ mxtrain_status ns_run(const NsPlan &pl, mxt::NsArgs n, int64_t batch, int64_t m,
   for (int step = 0; step < steps; step++) {
     const int cur = step & 1;
     const bool last = step == steps - 1;
-    const _Float16 *x = plane(pl.x[cur], 0), *x_lo = SPLIT ? plane(pl.x[cur], 1) : nullptr;
+    const _Float16 *x = plane(pl.x[cur], 0), *x_lo = plane(pl.x[cur], 1);
     _Float16 *s = plane(pl.sq[0], 0), *s_lo = SPLIT ? plane(pl.sq[0], 1) : nullptr;
     _Float16 *q = plane(pl.sq[1], 0), *q_lo = SPLIT ? plane(pl.sq[1], 1) : nullptr;
     mxt::NsGemm gram{}, poly{}, next{};
@@ -166,9 +166,10 @@ mxtrain_status ns_run(const NsPlan &pl, mxt::NsArgs n, int64_t batch, int64_t m,
     poly.cc = co[2] * ps / (mxt::kSScale * mxt::kSScale);
     const uint16_t *hx = bits(x), *hq = bits(q), *lx = bits(x_lo), *lq = bits(q_lo);
     next.g.a = pl.tall ? hx : hq;
-    next.a_lo = pl.tall ? lx : lq;
     next.g.b = pl.tall ? hq : hx;
-    next.b_lo = pl.tall ? lq : lx;
+    next.a_lo = pl.tall ? lx : SPLIT ? lq : hq;
+    next.b_lo = pl.tall ? (SPLIT ? lq : hq) : lx;
+    next.passes = step == 0 && !n.x_lo ? 1 : 2;  // a bf16 G has no low plane
     next.g.lda = pl.tall ? pl.ld_x : pl.ld_s;
     next.g.stride_a = pl.tall ? pl.stride_x : pl.stride_s;
     next.g.ldb = pl.tall ? pl.ld_s : pl.ld_x;
@@ -177,7 +178,7 @@ mxtrain_status ns_run(const NsPlan &pl, mxt::NsArgs n, int64_t batch, int64_t m,
     next.g.N = cols;
     next.g.K = pl.s;
     next.g.c = last ? out : plane(pl.x[cur ^ 1], 0);
-    next.c_lo = last || !SPLIT ? nullptr : plane(pl.x[cur ^ 1], 1);
+    next.c_lo = last ? nullptr : plane(pl.x[cur ^ 1], 1);
     next.g.ldc = last ? ld_out : pl.ld_x;
     next.g.stride_c = last ? stride_out : pl.stride_x;
     next.g.vec_c = last && vec_c_ok(out, ld_out, stride_out, SPLIT ? MXTRAIN_F32 : MXTRAIN_BF16);

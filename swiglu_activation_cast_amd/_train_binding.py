@@ -118,7 +118,12 @@ def _other_stream(device: torch.device, stream, *tensors) -> None:
     current = torch.cuda.current_stream(device)
     handle = _stream_of(device, stream)
     if handle != current.cuda_stream:
-        other = torch.cuda.ExternalStream(handle, device=device)
+        if hasattr(stream, "wait_stream"):
+            other = stream
+        elif handle == 0:  # an ExternalStream of handle 0 would be a new stream
+            other = torch.cuda.default_stream(device)
+        else:
+            other = torch.cuda.ExternalStream(handle, device=device)
         other.wait_stream(current)
         for t in tensors:
             if t is not None:

@@ -10,9 +10,9 @@ CPU or PyTorch fallback.
 
 On a `stream` other than the current one, what the call allocates comes from
 the current stream's pool: memory whose last use may still be running there,
-and which torch hands out again once it is freed here.  So the other stream
-first waits for the current one, and outputs and workspace are recorded on it
-(_other_stream).
+and which torch hands out again once it is freed here, as it does an input's
+that the caller drops.  So the other stream first waits for the current one,
+and inputs, outputs and workspace are recorded on it (_other_stream).
 """
 from __future__ import annotations
 
@@ -220,7 +220,7 @@ def mxtrain_layer_norm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = Non
     mean, pm = _f32_out(mean, "mean", M, dev)
     rstd, pr = _f32_out(rstd, "rstd", M, dev)
     if stream is not None:
-        _other_stream(dev, stream, y, mean, rstd)
+        _other_stream(dev, stream, x, weight, bias, y, mean, rstd)
     _call("mxtrain_layer_norm_fwd", dev, x.data_ptr(), _ld(x, "x"), pw, pb,
           0 if param is None else _TYPES[param.dtype], M, N, _TYPES[x.dtype], eps, y.data_ptr(), _ld(y, "out"),
           pm, pr, _stream_of(dev, stream))
@@ -248,7 +248,7 @@ def mxtrain_layer_norm_bwd(dy: torch.Tensor, x: torch.Tensor, mean: torch.Tensor
     db, pdb = _f32_out(dbias, "dbias", N, dev)
     ws = _workspace(_workspace_bytes("mxtrain_layer_norm_bwd_workspace", M, N), workspace, dev)
     if stream is not None:
-        _other_stream(dev, stream, dx, dw, db, ws)
+        _other_stream(dev, stream, dy, x, mean, rstd, weight, dx, dw, db, ws)
     _call("mxtrain_layer_norm_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), x.data_ptr(), _ld(x, "x"), pm, pr, pw,
           0 if weight is None else _TYPES[weight.dtype], M, N, _TYPES[x.dtype], dx.data_ptr(), _ld(dx, "out"),
           pdw, pdb, *_place(ws), _stream_of(dev, stream))
@@ -290,7 +290,7 @@ def mxtrain_grouped_gemm(a: torch.Tensor, b: torch.Tensor, group_ends: torch.Ten
     c = _out(out, "out", (M, N), _out_dtype(out, out_dtype), dev)
     ldb = _ld(b, "b")
     if stream is not None:
-        _other_stream(dev, stream, c)
+        _other_stream(dev, stream, a, b, group_ends, c)
     _call("mxtrain_grouped_gemm", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), ldb,
           b.stride(0) if G > 1 else 0, int(transpose_b), pe, G, M, N, K, c.data_ptr(), _ld(c, "out"),
           _TYPES[c.dtype], _stream_of(dev, stream))
@@ -313,7 +313,7 @@ def mxtrain_grouped_gemm_k(a: torch.Tensor, b: torch.Tensor, group_ends: torch.T
     c = _out(out, "out", (G, M, N), _out_dtype(out, out_dtype), dev)
     ldc = _ld(c, "out")
     if stream is not None:
-        _other_stream(dev, stream, c)
+        _other_stream(dev, stream, a, b, group_ends, c)
     _call("mxtrain_grouped_gemm_k", dev, a.data_ptr(), _ld(a, "a"), b.data_ptr(), _ld(b, "b"), pe, G, M, N, T,
           c.data_ptr(), ldc, c.stride(0) if G > 1 else max(ldc * M, 1), _TYPES[c.dtype], _stream_of(dev, stream))
     return c
@@ -345,7 +345,7 @@ def mxtrain_newton_schulz(g: torch.Tensor, *, steps: int = 5,
     nbytes = _workspace_bytes("mxtrain_newton_schulz_workspace", batch, m, n, _TYPES[c.dtype])
     ws = _workspace(nbytes, workspace, dev)
     if stream is not None:
-        _other_stream(dev, stream, c, ws)
+        _other_stream(dev, stream, g, c, ws)
     _call("mxtrain_newton_schulz", dev, g.data_ptr(), ld_g, stride_g, _TYPES[g.dtype], batch, m, n, int(steps),
           (ctypes.c_float * 3)(*coeffs), eps, c.data_ptr(), ld_c, stride_c, _TYPES[c.dtype], *_place(ws),
           _stream_of(dev, stream))

@@ -64,3 +64,54 @@ def test_the_current_stream_needs_nothing(streams, as_handle):
     t = Tensor()
     tb._other_stream(DEV, 0x1000 if as_handle else streams["current"], t)
     assert not streams["current"].waited and not t.recorded and not streams["made"]
+
+
+# every call of the binding with a stream, on CPU stand-ins: inputs, outputs and
+# workspace
+def _ln():
+    return torch.randn(8, 16), torch.randn(16), torch.randn(16), torch.randn(8), torch.rand(8)
+
+
+def call_ln_fwd():
+    x, w, b, mean, rstd = _ln()
+    return [x, w, b], tb.mxtrain_layer_norm_fwd(x, w, b, stream=7)
+
+
+def call_ln_bwd():
+    x, w, _, mean, rstd = _ln()
+    dy, ws = torch.randn(8, 16), torch.empty(64, dtype=torch.uint8)
+    return [dy, x, mean, rstd, w, ws], tb.mxtrain_layer_norm_bwd(dy, x, mean, rstd, w, workspace=ws, stream=7)
+
+
+def _experts():
+    a, dy = torch.zeros((16, 24), dtype=torch.bfloat16), torch.zeros((16, 32), dtype=torch.bfloat16)
+    return a, dy, torch.zeros((2, 32, 24), dtype=torch.bfloat16), torch.tensor([3, 16], dtype=torch.int32)
+
+
+def call_gemm():
+    a, _, b, ends = _experts()
+    return [a, b, ends], (tb.mxtrain_grouped_gemm(a, b, ends, stream=7),)
+
+
+def call_gemm_k():
+    a, dy, _, ends = _experts()
+    return [dy, a, ends], (tb.mxtrain_grouped_gemm_k(dy, a, ends, stream=7),)
+
+
+def call_newton_schulz():
+    g = torch.randn(2, 8, 16)
+    ws = torch.empty(1 << 20, dtype=torch.uint8)
+    return [g, ws], (tb.mxtrain_newton_schulz(g, workspace=ws, stream=7),)
+
+
+@pytest.mark.parametrize("call", [call_ln_fwd, call_ln_bwd, call_gemm, call_gemm_k, call_newton_schulz])
+def test_everything_a_call_touches_is_recorded_on_its_stream(monkeypatch, call):
+    """An input that the caller drops right after the call goes back to the
+    current stream's pool, like an output or the workspace."""
+    recorded = []
+    monkeypatch.setattr(tb, "_gpu", lambda t, *a, **k: t)
+    monkeypatch.setattr(tb, "_call", lambda *a: None)
+    monkeypatch.setattr(tb, "_other_stream", lambda device, stream, *ts: recorded.extend(ts))
+    inputs, outputs = call()
+    held = {id(t) for t in recorded}
+    assert all(id(t) in held for t in (*inputs, *outputs))

@@ -107,7 +107,8 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
  *
  * Sums are fp32, rounded once into C.  Any dimensions; a and b 16-byte
  * aligned, lda, ldb and stride_b multiples of 8 (16 bytes) and below 2^22
- * (lda, ldb); c aligned to its element.  Elements between a row's end and the
+ * (lda, ldb); a single row's stride, a single expert's and those of operands
+ * without elements (K == 0) may be any; c aligned to its element.  Elements between a row's end and the
  * next multiple of 8 may be read (never used), nothing else outside the
  * matrices.  0 <= G <= 65535; G == 0, or an empty C, returns MXTRAIN_OK and
  * enqueues nothing.

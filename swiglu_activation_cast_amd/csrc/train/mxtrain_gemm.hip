@@ -44,8 +44,11 @@ GroupKernel group_pick(int64_t groups, int64_t rows, int64_t N, int64_t depth, b
   return group_kernel<MODE, AL, BL, 1, 1, 64, 4>(f32);
 }
 
+// Rows of an operand start 16 bytes apart; nothing is read through the stride
+// of a single row, or of a matrix without elements.
 mxtrain_status operand_check(const void *p, int64_t ld, int64_t rows, int64_t cols) {
-  if (ld < cols || ld % 8 != 0) return MXTRAIN_ERR_STRIDE;
+  if (rows == 0 || cols == 0) return MXTRAIN_OK;
+  if (ld < cols || (rows > 1 && ld % 8 != 0)) return MXTRAIN_ERR_STRIDE;
   if (!aligned(p, 16)) return MXTRAIN_ERR_ALIGN;
   if (ld >= mxt::kMaxLd || !extent_ok(rows, cols, ld)) return MXTRAIN_ERR_OVERFLOW;
   return MXTRAIN_OK;
@@ -72,8 +75,8 @@ mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, i
   if (st == MXTRAIN_OK) st = operand_check(b, ldb, b_rows, b_cols);
   if (st != MXTRAIN_OK) return st;
   int64_t all;
-  if (stride_b < 0 || stride_b % 8 != 0 || ldc < N) return MXTRAIN_ERR_STRIDE;
-  if (G > 1 && b_rows > 0 && stride_b < (b_rows - 1) * ldb + b_cols) return MXTRAIN_ERR_STRIDE;
+  if (stride_b < 0 || ldc < N) return MXTRAIN_ERR_STRIDE;
+  if (G > 1 && K > 0 && (stride_b % 8 != 0 || stride_b < (b_rows - 1) * ldb + b_cols)) return MXTRAIN_ERR_STRIDE;
   if (!aligned(group_ends, 4) || !aligned(c, (uintptr_t)size_of(c_dtype))) return MXTRAIN_ERR_ALIGN;
   if (!extent_ok(M, N, ldc) || __builtin_mul_overflow(stride_b, G, &all) || all > (INT64_MAX >> 4))
     return MXTRAIN_ERR_OVERFLOW;

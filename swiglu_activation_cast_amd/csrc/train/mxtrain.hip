@@ -217,8 +217,7 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
   int n_parts = (int)parts;
   int32_t n = (int32_t)N;
   void *kargs[] = {&part, &n_parts, &n, &dweight, &dbias};
-  const int64_t blocks = (2 * N + 31) / 32;
-  if (blocks > INT32_MAX / 1024) return MXTRAIN_ERR_OVERFLOW;
+  const int64_t blocks = std::min<int64_t>((2 * N + 31) / 32, INT32_MAX / 1024);
   const hipError_t err = hipLaunchKernel((const void *)&mxt::k_ln_join, dim3((unsigned)blocks), dim3(1024), kargs, 0,
                                          (hipStream_t)stream);
   return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;

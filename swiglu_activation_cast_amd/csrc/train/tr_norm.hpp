@@ -459,26 +459,30 @@ __global__ __launch_bounds__(1024) void k_ln_bwd_long(const LnArgs g) {
 
 // dw and db: the sums of `parts` partial rows, in row order within each of 32
 // slices and then over the slices.  A workgroup takes 32 columns of the 2 N
-// (dw's, then db's); no rows give zeros.
+// (dw's, then db's) at a time; no rows give zeros.
 __global__ __launch_bounds__(1024) void k_ln_join(const float *part, int parts, int32_t N, float *dw, float *db) {
   __shared__ float sm[32][33];
   const int c = threadIdx.x & 31, s = threadIdx.x >> 5;
-  const int64_t col = (int64_t)blockIdx.x * 32 + c;
-  float a = 0.0f;
-  if (col < 2 * (int64_t)N)
+  const int64_t all = 2 * (int64_t)N;
+  for (int64_t first = (int64_t)blockIdx.x * 32; first < all; first += (int64_t)gridDim.x * 32) {
+    const int64_t col = first + c;
+    float a = 0.0f;
+    if (col < all)
 #pragma unroll 4
-    for (int p = s; p < parts; p += 32) a += *gptr(part + (int64_t)p * 2 * N + col);
-  sm[s][c] = a;
-  __syncthreads();
-  if (s == 0 && col < 2 * (int64_t)N) {
-    float t = 0.0f;
+      for (int p = s; p < parts; p += 32) a += *gptr(part + p * all + col);
+    sm[s][c] = a;
+    __syncthreads();
+    if (s == 0 && col < all) {
+      float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 32; k++) t += sm[k][c];
-    if (col < N) {
-      if (dw) *gptr(dw + col) = t;
-    } else {
-      if (db) *gptr(db + col - N) = t;
+      for (int k = 0; k < 32; k++) t += sm[k][c];
+      if (col < N) {
+        if (dw) *gptr(dw + col) = t;
+      } else {
+        if (db) *gptr(db + col - N) = t;
+      }
     }
+    __syncthreads();  // before sm is written again
   }
 }
 

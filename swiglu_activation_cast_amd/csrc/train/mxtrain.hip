@@ -150,7 +150,9 @@ mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *w
   // 63 us with 1024 threads to a CU, 81 with 1280, more than fit evenly; 16384 x
   // 2048 27 us with 2048, 33 with 1024).
   const int per_cu = p.elems > 8 ? 1024 : vec ? 2048 : 1536;
-  const int64_t most = p.elems ? cu_count() * std::max<int64_t>(1, per_cu / p.threads) : M;
+  // (Long rows leave that to the hardware: a workgroup to a row up to the
+  // largest launch, then rows are walked too.)
+  const int64_t most = p.elems ? cu_count() * std::max<int64_t>(1, per_cu / p.threads) : INT32_MAX / p.threads;
   return launch(ln_kernel<false>(p, dtype, vec), std::min((M + rows - 1) / rows, most), p.threads, g, stream);
 }
 

@@ -229,28 +229,29 @@ __global__ __launch_bounds__((TPR != 0 ? 256 : CH * VEC <= 16 ? 1024 : 512)) voi
 template <class T>
 __global__ __launch_bounds__(1024) void k_ln_fwd_long(const LnArgs g) {
   __shared__ float sm[2][16][2];
-  const int64_t row = blockIdx.x;
-  const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
-  T *y = static_cast<T *>(g.y) + row * g.ld_y;
-  float s = 0.0f, q = 0.0f, e = 0.0f, unused = 0.0f;
-  for (int64_t c = threadIdx.x; c < g.N; c += 1024) s += to_f32(*gptr(x + c));
-  row_sum2<0>(s, unused, sm[0]);
-  const float m = s / (float)g.N;
-  for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
-    const float d = to_f32(*gptr(x + c)) - m;
-    e += d;
-    q = fmaf(d, d, q);
+  for (int64_t row = blockIdx.x; row < g.M; row += gridDim.x) {
+    const T *x = static_cast<const T *>(g.x) + row * g.ld_x;
+    T *y = static_cast<T *>(g.y) + row * g.ld_y;
+    float s = 0.0f, q = 0.0f, e = 0.0f, unused = 0.0f;
+    for (int64_t c = threadIdx.x; c < g.N; c += 1024) s += to_f32(*gptr(x + c));
+    row_sum2<0>(s, unused, sm[0]);
+    const float m = s / (float)g.N;
+    for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+      const float d = to_f32(*gptr(x + c)) - m;
+      e += d;
+      q = fmaf(d, d, q);
+    }
+    row_sum2<0>(q, e, sm[1]);  // its barrier also lies between this row's reads of sm[0] and the next row's writes
+    const float rstd = ln_rstd(m, q, e, g);
+    for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
+      float w, b;
+      load_param<1>(g.w, g.w_f32, false, (int32_t)c, 1.0f, &w);
+      load_param<1>(g.b, g.w_f32, false, (int32_t)c, 0.0f, &b);
+      *gptr(y + c) = from_f32<T>(fmaf((to_f32(*gptr(x + c)) - m - e) * rstd, w, b));
+    }
+    if (threadIdx.x == 0 && g.mean) *gptr(g.mean + row) = m + e;
+    if (threadIdx.x == 0 && g.rstd) *gptr(g.rstd + row) = rstd;
   }
-  row_sum2<0>(q, e, sm[1]);
-  const float rstd = ln_rstd(m, q, e, g);
-  for (int64_t c = threadIdx.x; c < g.N; c += 1024) {
-    float w, b;
-    load_param<1>(g.w, g.w_f32, false, (int32_t)c, 1.0f, &w);
-    load_param<1>(g.b, g.w_f32, false, (int32_t)c, 0.0f, &b);
-    *gptr(y + c) = from_f32<T>(fmaf((to_f32(*gptr(x + c)) - m - e) * rstd, w, b));
-  }
-  if (threadIdx.x == 0 && g.mean) *gptr(g.mean + row) = m + e;
-  if (threadIdx.x == 0 && g.rstd) *gptr(g.rstd + row) = rstd;
 }
 
 // Most threads of a backward workgroup whose threads hold E elements: a thread

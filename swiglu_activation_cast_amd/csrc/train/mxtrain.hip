@@ -119,7 +119,7 @@ mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *w
                                       int64_t ld_y, float *mean, float *rstd, void *stream) {
   if (!type_ok(dtype) || !type_ok(param_dtype)) return MXTRAIN_ERR_TYPE;
   if (!(eps >= 0.0f) || std::isinf(eps)) return MXTRAIN_ERR_VALUE;
-  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX - 4096) return MXTRAIN_ERR_SHAPE;
+  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX) return MXTRAIN_ERR_SHAPE;
   if (M == 0) return MXTRAIN_OK;
   if (N == 0) return MXTRAIN_ERR_SHAPE;
   const void *mats[] = {x, y};
@@ -157,7 +157,7 @@ mxtrain_status mxtrain_layer_norm_fwd(const void *x, int64_t ld_x, const void *w
 }
 
 int64_t mxtrain_layer_norm_bwd_workspace(int64_t M, int64_t N) {
-  if (M <= 0 || N <= 0 || M > INT32_MAX || N > INT32_MAX - 4096) return 0;
+  if (M <= 0 || N <= 0 || M > INT32_MAX || N > INT32_MAX) return 0;
   return ln_columns_apart(M, N) ? 0 : ln_parts(M) * 2 * N * (int64_t)sizeof(float);
 }
 
@@ -166,7 +166,7 @@ mxtrain_status mxtrain_layer_norm_bwd(const void *dy, int64_t ld_dy, const void 
                                       int dtype, void *dx, int64_t ld_dx, float *dweight, float *dbias,
                                       void *workspace, int64_t workspace_bytes, void *stream) {
   if (!type_ok(dtype) || !type_ok(param_dtype)) return MXTRAIN_ERR_TYPE;
-  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX - 4096) return MXTRAIN_ERR_SHAPE;
+  if (M < 0 || N < 0 || M > INT32_MAX || N > INT32_MAX) return MXTRAIN_ERR_SHAPE;
   if (N == 0) return M == 0 ? MXTRAIN_OK : MXTRAIN_ERR_SHAPE;
   if (!aligned(dweight, 4) || !aligned(dbias, 4)) return MXTRAIN_ERR_ALIGN;
   const bool apart = M > 0 && ln_columns_apart(M, N), sums = (dweight || dbias) && !apart;

@@ -38,3 +38,13 @@ def test_a_single_row_has_no_row_stride():
     assert gemm(tb=0, K=1, N=33, lda=8, ldb=33, G=1, sb=0) == ALIGN
     assert gemm_k(T=1, M=60, lda=60, N=33, ldb=33) == ALIGN
     assert gemm(M=1, K=60, lda=59) == STRIDE  # still no shorter than the row
+
+
+def test_layer_norm_takes_every_width_below_2_to_the_31():
+    last = 2**31 - 1
+    lib = mx.train_lib()
+    # a row stride shorter than the row, checked after the sizes
+    assert lib.mxtrain_layer_norm_fwd(A, 64, A, A, F32, 4, last, BF16, 1e-5, A, 64, A, A, None) == STRIDE
+    assert lib.mxtrain_layer_norm_bwd(A, 64, A, 64, A, A, A, F32, 4, last, BF16, A, 64, A, A, A, 1 << 20, None) == STRIDE
+    assert lib.mxtrain_layer_norm_bwd_workspace(4, last) == 2 * last * 4
+    assert lib.mxtrain_layer_norm_fwd(A, 64, A, A, F32, 4, last + 1, BF16, 1e-5, A, 64, A, A, None) == SHAPE

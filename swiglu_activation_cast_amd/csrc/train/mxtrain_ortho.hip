@@ -25,7 +25,7 @@ mxtrain_status mxtrain_newton_schulz(const void *g, int64_t ld_g, int64_t stride
   if (steps < 0 || steps > 100 || !(eps >= 0.0f) || std::isinf(eps)) return MXTRAIN_ERR_VALUE;
   for (int i = 0; i < 3; i++)
     if (!std::isfinite(coeffs[i])) return MXTRAIN_ERR_VALUE;
-  if (batch < 0 || m < 0 || n < 0 || batch > kMaxGroups || m >= mxt::kMaxLd - 8 || n >= mxt::kMaxLd - 8)
+  if (batch < 0 || m < 0 || n < 0 || batch > kMaxGroups || m >= mxt::kMaxLd || n >= mxt::kMaxLd)
     return MXTRAIN_ERR_SHAPE;
   if (batch == 0 || m == 0 || n == 0) return MXTRAIN_OK;
   if (!g || !out || !workspace) return MXTRAIN_ERR_NULL;

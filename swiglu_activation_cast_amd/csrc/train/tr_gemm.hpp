@@ -64,7 +64,7 @@ enum Elem { kBf16 = 0, kF16 = 1 };
 
 constexpr int kThreads = 256;
 constexpr int kTileRows = 16;             // tile rows per band of the tile order
-constexpr int64_t kMaxLd = int64_t(1) << 22;  // 256 rows of this many elements stay below 2^31 bytes
+constexpr int64_t kMaxLd = int64_t(1) << 22;  // 255 rows of as many elements and 512 bytes of the next stay below 2^31 bytes
 
 struct GemmArgs {
   const uint16_t *a, *b;

@@ -48,3 +48,12 @@ def test_layer_norm_takes_every_width_below_2_to_the_31():
     assert lib.mxtrain_layer_norm_bwd(A, 64, A, 64, A, A, A, F32, 4, last, BF16, A, 64, A, A, A, 1 << 20, None) == STRIDE
     assert lib.mxtrain_layer_norm_bwd_workspace(4, last) == 2 * last * 4
     assert lib.mxtrain_layer_norm_fwd(A, 64, A, A, F32, 4, last + 1, BF16, 1e-5, A, 64, A, A, None) == SHAPE
+
+
+def test_newton_schulz_takes_every_side_below_2_to_the_22():
+    lib, co, last = mx.train_lib(), (ctypes.c_float * 3)(3.4445, -4.775, 2.0315), 2**22 - 1
+    for m, n in ((last, 40), (40, last)):
+        need = lib.mxtrain_newton_schulz_workspace(1, m, n, BF16)
+        args = (A, n, 0, F32, 1, m, n, 5, co, 1e-7, A, n, 0, BF16, A)
+        assert need > 0 and lib.mxtrain_newton_schulz(*args, need - 1, None) == WORKSPACE
+    assert lib.mxtrain_newton_schulz(A, 40, 0, F32, 1, last + 1, 40, 5, co, 1e-7, A, 40, 0, BF16, A, 1 << 40, None) == SHAPE

@@ -28,11 +28,11 @@ RowPlan row_plan(int64_t M, int64_t N, int vec, bool bwd) {
   if (many && N <= 128) return {16, 256, 8};
   if (N <= 512) return {64, 256, 8};
   if (many && N <= 1024) return {64, 256, 16};
-    const int cap = many && !bwd && vec > 1 ? 512 : 1024;
+  const int cap = many && !bwd && vec > 1 ? 512 : 1024;
   const int64_t chunks = (N + vec - 1) / vec;
   for (int pass = 0; pass < 2; pass++)
     for (int e = 8; e <= 32; e *= 2) {
-      if (bwd && vec == 1 && e == 32) continue;  // more registers than a thread has
+      if (vec == 1 && e == 32) continue;  // backward: more registers than a thread has; forward: 16 reach as far
       // the kernels' launch bounds
       const int most = bwd ? (e == 8 && vec > 1 ? 1024 : 512) : e <= 16 ? 1024 : 512;
       const int64_t per = e / vec, need = (chunks + per - 1) / per;
@@ -65,9 +65,11 @@ const void *ln_kernel(const RowPlan &p) {
   if (p.tpr == 16) return ln_pick<T, VEC, 16, 8, BWD>();
   if (p.tpr == 64) return p.elems == 8 ? ln_pick<T, VEC, 64, 8, BWD>() : ln_pick<T, VEC, 64, 16, BWD>();
   if (p.elems == 8) return ln_pick<T, VEC, 0, 8, BWD>();
-  if (p.elems == 16) return ln_pick<T, VEC, 0, 16, BWD>();
-  if constexpr (BWD && VEC == 1) return nullptr;  // not planned
-  else return ln_pick<T, VEC, 0, 32, BWD>();
+  // as vectors the backward's 1024 threads of 8 reach as far as its 512 of 16;
+  // by element neither pass is planned 32
+  if constexpr (VEC == 1) return ln_pick<T, 1, 0, 16, BWD>();
+  else if constexpr (BWD) return ln_pick<T, VEC, 0, 32, true>();
+  else return p.elems == 16 ? ln_pick<T, VEC, 0, 16, false>() : ln_pick<T, VEC, 0, 32, false>();
 }
 
 template <bool BWD>

@@ -17,8 +17,9 @@
  *  - Every argument is checked before any launch; a failed check returns a
  *    status and enqueues nothing.
  *  - Outputs and workspaces must not alias inputs or each other (not
- *    checked).  Equal inputs give equal bits: nothing is summed in an order
- *    that changes from call to call.
+ *    checked).  Equal calls give equal bits: nothing is summed in an order
+ *    that changes from call to call.  (The order depends on the sizes, on
+ *    whether rows start 16-byte aligned, and on the device's compute units.)
  *  - Calls are thread-safe; the library keeps no mutable global state.
  */
 #ifndef MXTRAIN_H

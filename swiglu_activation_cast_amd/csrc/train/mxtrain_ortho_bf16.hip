@@ -1,4 +1,5 @@
-// mxtrain_ortho_bf16.hip -- the Newton-Schulz steps for bf16 results: one fp16 plane.
+// mxtrain_ortho_bf16.hip -- the Newton-Schulz steps for bf16 results: X in two
+// fp16 planes, S and p(S) in one.
 #include "tr_ortho_run.hpp"
 
 namespace mxt {

@@ -1,5 +1,5 @@
 // tr_gemm.hpp -- products of 16-bit matrices with fp32 sums on gfx950's matrix
-// cores (v_mfma_f32_32x32x16_bf16 / _f16): the experts' products over ragged
+// cores (v_mfma_f32_16x16x32_bf16 / _f16): the experts' products over ragged
 // groups and the products of the Newton-Schulz steps.
 //
 //   C[m][n] = sum over k of A(m, k) B(n, k)
@@ -24,7 +24,7 @@
 // meet twice as many barriers, 8% slower; two workgroups to a CU with 128 x 256
 // or 128 x 128 tiles read more of each operand, 20-35% slower).
 //
-// The card runs such a product at its power limit, near 1.73 GHz, so what an
+// The card lowers its clock under such a product (1.7 to 1.95 GHz), so what an
 // instruction moves counts beside what it takes: the 16x16x32 MFMA passes
 // half as many accumulator bits through the registers per product as the
 // 32x32x16 one, and is 4-6% faster here.
@@ -49,8 +49,6 @@
 #include "tr_common.hpp"
 
 namespace mxt {
-
-
 
 // Loads [FROM, TO) of a stage.
 template <int FROM, int TO>

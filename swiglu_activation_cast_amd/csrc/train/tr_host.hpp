@@ -31,8 +31,9 @@ mxtrain_status launch(const void *kernel, int64_t blocks, int threads, const Arg
   return err == hipSuccess ? MXTRAIN_OK : MXTRAIN_ERR_LAUNCH;
 }
 
-// Compute units of the current device (it decides tile sizes, no result
-// depends on it).
+// Compute units of the current device.  They decide tile sizes and how many rows
+// a workgroup walks, and with them the order of sums: a result's last bits are
+// those of devices with as many.
 inline int cu_count() {
   int dev = 0, cus = 0;
   if (hipGetDevice(&dev) != hipSuccess ||

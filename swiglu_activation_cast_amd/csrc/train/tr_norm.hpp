@@ -9,10 +9,11 @@
 //
 // Both are bound by HBM: the forward reads x and writes y, the backward reads
 // dy and x and writes dx, each once.  So a row stays in registers between its
-// reductions and its output (up to 32 elements a thread), and the backward's column sums are kept in registers over all the rows that
-// a workgroup walks, written once per workgroup as a partial row and joined
-// by a second kernel in a fixed order (no atomics: equal inputs give equal
-// bits).  All arithmetic is fp32; outputs are rounded once.
+// reductions and its output (up to 32 elements a thread), and the backward's
+// column sums are kept in registers over all the rows that a workgroup walks,
+// written once per workgroup as a partial row and joined by a second kernel in a
+// fixed order (no atomics: equal inputs give equal bits).  All arithmetic is
+// fp32; outputs are rounded once.
 //
 // Rows far off centre: the variance is taken from deviations d = x - m to the
 // mean m already known, and the second reduction sums d beside d^2.  With
@@ -123,7 +124,6 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, float (*sm)[2]) {
   }
 }
 
-// TPR threads per row (0: the whole workgroup) in the kernels below.
 // The correction e and 1 / sqrt(var + eps) from the second reduction's sums.
 __device__ __forceinline__ float ln_rstd(float m, float q, float &e, const LnArgs &g) {
   q /= (float)g.N;
@@ -154,6 +154,8 @@ struct Raw {
   }
 };
 
+// TPR threads to a row, here and below (0: the whole workgroup).
+//
 // Workgroup b walks rows b, b + gridDim.x, ... (groups of 256 / TPR rows),
 // with the weight and bias in registers and a row's loads issued while the row
 // before it is reduced.  16384 x 8192 bf16: 96 us, 5.6 TB/s over x and y (a
@@ -261,23 +263,10 @@ __global__ __launch_bounds__(1024) void k_ln_fwd_long(const LnArgs g) {
 template <int VEC, int E>
 constexpr int kLnBwdThreads = E <= 8 && VEC > 1 ? 1024 : 512;
 
-// Backward.  Workgroup b walks rows b, b + gridDim.x, ... (TPR == 0) or the
-// same for groups of 256 / TPR rows; every thread keeps its columns' sums of
-// dy xh and dy over all of them.  A row's loads are issued before the
-// reduction of the row before it, which they would otherwise wait for.  With
-// TPR > 0 the row slots of a workgroup are joined in LDS (dynamic: slots * 2 *
-// N floats) before the partial row is written.
-//
-// 16384 x 5120 bf16: 94 us, 5.35 TB/s over dy, x and dx (without the row held
-// ahead and with half the wavefronts 155 us).
-//
-// Few rows: the column sums need no row's reduction, so further workgroups of
-// the same launch take 64 columns each and read them over all rows again (from
-// L2), instead of a second launch over partial rows, which costs a small call
-// more than that.
-//
-// Columns past N: a chunk that lies there is read as the row's first one and
-// its weight and dy count as zero, so that it adds nothing.
+// The column sums of few rows.  They need no row's reduction, so further
+// workgroups of the backward's launch take 64 columns each and read them over all
+// rows again (from L2), instead of a second launch over partial rows, which
+// costs a small call more than that.
 template <class T>
 __device__ __forceinline__ void ln_columns(const LnArgs &g, int64_t strip, float (*sm)[64][2]) {
   const int c = threadIdx.x & 63, s = threadIdx.x >> 6, n = blockDim.x >> 6;
@@ -306,6 +295,20 @@ __device__ __forceinline__ void ln_columns(const LnArgs &g, int64_t strip, float
   }
 }
 
+// Backward.  Workgroup b walks rows b, b + gridDim.x, ... (TPR == 0) or the
+// same for groups of 256 / TPR rows; every thread keeps its columns' sums of
+// dy xh and dy over all of them.  A row's loads are issued before the
+// reduction of the row before it, which they would otherwise wait for.  With
+// TPR > 0 the row slots of a workgroup are joined in LDS (dynamic: slots * 2 *
+// N floats) before the partial row is written.
+//
+// 16384 x 5120 bf16: 94 us, 5.35 TB/s over dy, x and dx (without the row held
+// ahead and with half the wavefronts 155 us).
+//
+// Workgroups past row_blocks take columns (ln_columns).
+//
+// Columns past N: a chunk that lies there is read as the row's first one and
+// its weight and dy count as zero, so that it adds nothing.
 template <class T, int VEC, int TPR, int CH>
 __global__ __launch_bounds__((TPR != 0 ? 256 : kLnBwdThreads<VEC, (CH * VEC)>)) void k_ln_bwd(const LnArgs g) {
   __shared__ float sm[2][16][2];

@@ -46,8 +46,8 @@ inline NsPlan ns_plan(int64_t batch, int64_t m, int64_t n, int out_dtype) {
     }
   // S of at most 16 tiles of 64 x 64 leaves most CUs idle: over 40 stages of K or
   // more it is dealt to as many as 16 workgroups a tile, at least four stages
-  // each (five steps of 2 x 6881 x 95 bf16: 152 us, 212 without; fp32 168 and
-  // 336; of 8 x 64 x 2048 bf16, 32 stages, 94 and 92).
+  // each (five steps of 2 x 6881 x 95 bf16: 161 us, 223 without; fp32 169 and
+  // 334; of 8 x 64 x 2048 bf16, 32 stages, either way 94 +- 2).
   const int64_t ts = (p.s + 63) / 64, tiles = ts * (ts + 1) / 2 * batch, stages = (std::max(m, n) + 63) / 64;
   p.parts = tiles <= 16 && stages >= 40 ? (int)std::min<int64_t>({16, 256 / tiles, stages / 4}) : 1;
   p.part_sums = p.parts > 1 ? take(p.stride_s * p.parts, 4) : 0;
@@ -69,12 +69,12 @@ mxtrain_status ns_gemm(mxt::NsGemm &p, int64_t batch, void *stream) {
   // round runs cut down unless the product is symmetric; 128 x 128 tiles run
   // two to a CU.  Five steps with one tile throughout and as chosen here, us:
   //                            256    128     64   chosen
-  //   1 x 256 x 512 fp32       423    204    107      107
-  //   8 x 2048 x 1024 bf16     629    465    838      424
-  //   1 x 2048 x 2048 bf16     676    411    502      423
-  //   4 x 2048 x 2048 bf16     842    940   1586      821
-  //   1 x 8192 x 1024 bf16    1057    658    431      315
-  //   1 x 8192 x 5120 fp32    9242  11154  16711     9180
+  //   1 x 256 x 512 fp32       416    203    103      102
+  //   8 x 2048 x 1024 bf16     723    600   1053      540
+  //   1 x 2048 x 2048 bf16     778    502    616      524
+  //   4 x 2048 x 2048 bf16    1044   1192   2073     1042
+  //   1 x 8192 x 1024 bf16    1107    708    533      374
+  //   1 x 8192 x 5120 fp32    8753  10762  16288     8785
   auto cost256 = [&] {
     const int64_t t = tiles(256), whole = t / cus, tail = t % cus;
     if (sym) return (double)((t + cus - 1) / cus);

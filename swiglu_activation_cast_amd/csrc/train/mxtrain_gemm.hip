@@ -84,9 +84,9 @@ mxtrain_status mxtrain_grouped_gemm(const void *a, int64_t lda, const void *b, i
   const int64_t groups = std::min(G, M), rows = (M + groups - 1) / groups;  // as if evenly spread
   const GroupKernel k = transpose_b ? group_pick<mxt::kGroupM, mxt::kKC, mxt::kKC>(groups, rows, N, K, f32)
                                     : group_pick<mxt::kGroupM, mxt::kKC, mxt::kMC>(groups, rows, N, K, f32);
-  // an upper bound of tile rows, each group adding at most one partial one:
-  // the host never reads the ends
-  const int64_t tiles_m = (M + k.bm - 1) / k.bm + G, tiles_n = (N + k.bn - 1) / k.bn;
+  // an upper bound of tile rows, each group that has rows (M of them at most)
+  // adding at most one partial one: the host never reads the ends
+  const int64_t tiles_m = (M + k.bm - 1) / k.bm + groups, tiles_n = (N + k.bn - 1) / k.bn;
   int64_t blocks;
   if (__builtin_mul_overflow(tiles_m, tiles_n, &blocks)) return MXTRAIN_ERR_OVERFLOW;
   mxt::GemmArgs g{};

@@ -1,4 +1,5 @@
-"""The experts' products at their smallest operands: no K, a single row."""
+"""The experts' products at their smallest operands (no K, a single row) and with
+far more experts than rows."""
 import pytest
 import torch
 
@@ -46,3 +47,21 @@ def test_a_single_contiguous_row_of_any_length(K, dtype):
     dy = whole((1, 33), K + 6)
     got = mx.mxtrain_grouped_gemm_k(dy, x, one, out_dtype=dtype)
     assert not got[0].any() and torch.equal(got[1], (dy.double().T @ x.double()).to(dtype))
+
+
+def test_far_more_experts_than_rows():
+    """As many tiles as rows can fill are launched, not as many as experts
+    (65535 experts of 16392 columns would be more than a launch holds)."""
+    G, T, N, K = 65535, 70, 16392, 8
+    print(f"case: {T} rows over {G} experts", flush=True)
+    g = torch.Generator()
+    g.manual_seed(11)
+    owner = torch.sort(torch.randint(0, G, (T,), generator=g)).values
+    owner[-1] = G - 1
+    ends = torch.bincount(owner, minlength=G).cumsum(0).to(torch.int32).cuda()
+    owner = owner.cuda()
+    x, used = whole((T, K), 10), whole((T, N, K), 9)
+    w = torch.full((G, N, K), float("nan"), dtype=BF16, device="cuda")  # 17 GB
+    w[owner] = used
+    y = mx.mxtrain_grouped_gemm(x, w, ends, out_dtype=F32)
+    assert torch.equal(y, (w[owner].float() * x.float()[:, None, :]).sum(2))

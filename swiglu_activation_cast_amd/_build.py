@@ -1,6 +1,7 @@
 """Compiles the gfx950 HIP libraries in-tree with hipcc: libmxfp8.so (the
 casts and their consumer, behind include/mxfp8.h), libmxtrain.so (the 16- and
-32-bit operators of a training step beside them, behind include/mxtrain.h) and
+32-bit operators of a training step beside them, behind include/mxtrain.h and
+include/mxtrain_tokens.h) and
 libmxstream.so (the streaming bandwidth probe behind include/mxstream.h,
 measurement only)."""
 from __future__ import annotations
@@ -22,7 +23,8 @@ STREAM_LIB_PATH = os.path.join(PKG_DIR, "libmxstream.so")
 STREAM_SOURCES = [os.path.join(CSRC, "mx_stream.hip")]
 TRAIN_LIB_PATH = os.path.join(PKG_DIR, "libmxtrain.so")
 TRAIN_SOURCES = [os.path.join(CSRC, "train", name) for name in (
-    "mxtrain.hip", "mxtrain_gemm.hip", "mxtrain_ortho.hip", "mxtrain_ortho_bf16.hip", "mxtrain_ortho_f32.hip")]
+    "mxtrain.hip", "mxtrain_gemm.hip", "mxtrain_ortho.hip", "mxtrain_ortho_bf16.hip", "mxtrain_ortho_f32.hip",
+    "mxtrain_sort.hip", "mxtrain_route.hip", "mxtrain_embed.hip", "mxtrain_dropout.hip")]
 ARCH = "gfx950"
 
 

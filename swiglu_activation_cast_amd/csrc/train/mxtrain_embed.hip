@@ -1,0 +1,150 @@
+// mxtrain_embed.hip -- C ABI of the embedding lookup and its gradient.
+// Nothing is allocated, synchronized or read back, and no exception can leave
+// an entry point (nothing here throws).
+#include "mxtrain_tokens.h"
+#include "tr_embed.hpp"
+#include "tr_sort_run.hpp"
+
+using namespace mxt;
+
+namespace mxt {
+namespace {
+
+mxtrain_status embed_check(const void *table, int64_t ld_w, int w_type, const void *ids, int64_t id_stride,
+                           int id_type, const void *tokens, int64_t ld_t, int t_type, int64_t T, int64_t first,
+                           float scale, int64_t V, int64_t H) {
+  if (!type_ok(w_type) || !type_ok(t_type) || (id_type != MXTRAIN_I32 && id_type != MXTRAIN_I64))
+    return MXTRAIN_ERR_TYPE;
+  if (!std::isfinite(scale)) return MXTRAIN_ERR_VALUE;
+  if (T < 0 || V < 0 || H < 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return MXTRAIN_ERR_SHAPE;
+  if (first > INT64_MAX - V) return MXTRAIN_ERR_VALUE;
+  const bool has_t = T > 0 && H > 0, has_w = V > 0 && H > 0;
+  if ((T > 0 && !ids) || (has_t && !tokens) || (has_w && !table)) return MXTRAIN_ERR_NULL;
+  if ((has_t && ld_t < H) || (has_w && ld_w < H) || (T > 1 && id_stride < 0)) return MXTRAIN_ERR_STRIDE;
+  if (!aligned(ids, id_type == MXTRAIN_I64 ? 8 : 4) || !aligned(tokens, (uintptr_t)size_of(t_type)) ||
+      !aligned(table, (uintptr_t)size_of(w_type)))
+    return MXTRAIN_ERR_ALIGN;
+  if ((has_t && !extent_ok(T, H, ld_t)) || (has_w && !extent_ok(V, H, ld_w)) || !extent_ok(T, 1, id_stride))
+    return MXTRAIN_ERR_OVERFLOW;
+  return MXTRAIN_OK;
+}
+
+int64_t embed_vec(int t, int u) { return t == MXTRAIN_F32 && u == MXTRAIN_F32 ? 4 : 8; }
+
+// How the gradient cuts its work: chunks of 64 tokens, or fewer where that
+// leaves less than sixteen wavefronts to a compute unit.
+struct EmbedPlan {
+  uint32_t rows, chunks, strips;
+  int64_t part, bytes;
+};
+
+EmbedPlan embed_plan(const SortPlan &sort, int64_t T, int64_t H, int64_t vec) {
+  EmbedPlan p{};
+  const int64_t strips = ((H + vec - 1) / vec + 63) / 64;
+  int64_t rows = 64;
+  while (rows > 8 && (T + rows - 1) / rows * strips < 4096) rows /= 2;
+  p.rows = (uint32_t)rows;
+  p.chunks = (uint32_t)((T + rows - 1) / rows);
+  p.strips = (uint32_t)strips;
+  p.part = sort.bytes;
+  p.bytes = p.part + (p.chunks > 1 ? (int64_t)p.chunks * 2 * strips * 64 * vec * 4 : 0);
+  return p;
+}
+
+}  // namespace
+}  // namespace mxt
+
+extern "C" {
+
+mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weight_type, int64_t V, int64_t H,
+                                     const void *ids, int64_t id_stride, int id_type, int64_t T, int64_t first,
+                                     float scale, void *y, int64_t ld_y, int y_type, void *stream) {
+  const mxtrain_status st = embed_check(weight, ld_w, weight_type, ids, id_stride, id_type, y, ld_y, y_type, T, first,
+                                        scale, V, H);
+  if (st != MXTRAIN_OK) return st;
+  if (T == 0 || H == 0) return MXTRAIN_OK;
+  EmbedArgs a{};
+  a.in = weight;
+  a.out = y;
+  a.ld_in = ld_w;
+  a.ld_out = ld_y;
+  a.ids = ids;
+  a.id_stride = id_stride;
+  a.ids_i64 = id_type == MXTRAIN_I64;
+  a.first = first;
+  a.V = (u32)V;
+  a.H = (u32)H;
+  a.T = (u32)T;
+  a.scale = scale;
+  const bool f = weight_type == MXTRAIN_F32, g = y_type == MXTRAIN_F32;
+  const int64_t vec = embed_vec(weight_type, y_type), per = (H + vec - 1) / vec;
+  a.pieces = {T * per, divider((uint32_t)per)};
+  const void *kernel = f ? (g ? (const void *)&k_embed<float, float> : (const void *)&k_embed<float, uint16_t>)
+                         : (g ? (const void *)&k_embed<uint16_t, float> : (const void *)&k_embed<uint16_t, uint16_t>);
+  return launch(kernel, std::min<int64_t>((a.pieces.total + 255) / 256, INT32_MAX / 256), 256, a, stream);
+}
+
+int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_type, int dw_type) {
+  if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
+  return embed_plan(sort_plan(T, V, true), T, H, embed_vec(dy_type, dw_type)).bytes;
+}
+
+mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type, const void *ids, int64_t id_stride,
+                                     int id_type, int64_t T, int64_t first, float scale, int64_t V, int64_t H,
+                                     void *dweight, int64_t ld_dw, int dw_type, int accumulate, void *workspace,
+                                     int64_t workspace_bytes, void *stream) {
+  mxtrain_status st = embed_check(dweight, ld_dw, dw_type, ids, id_stride, id_type, dy, ld_dy, dy_type, T, first, scale,
+                                  V, H);
+  if (st != MXTRAIN_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return MXTRAIN_ERR_VALUE;
+  if (V == 0 || H == 0 || (T == 0 && accumulate)) return MXTRAIN_OK;
+  const SortPlan sp = sort_plan(T, V, true);
+  const EmbedPlan ep = embed_plan(sp, T, H, embed_vec(dy_type, dw_type));
+  if (T > 0 && !workspace) return MXTRAIN_ERR_NULL;
+  if (T > 0 && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
+  if (T > 0 && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
+  const int64_t sum_blocks = ((int64_t)ep.chunks * ep.strips + 3) / 4, zero_blocks = accumulate ? 0 : (V + 63) / 64;
+  if (sum_blocks + zero_blocks > INT32_MAX / 256 || (int64_t)ep.chunks * ep.strips > INT32_MAX / 64)
+    return MXTRAIN_ERR_OVERFLOW;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  EmbedArgs a{};
+  a.in = dy;
+  a.out = dweight;
+  a.ld_in = ld_dy;
+  a.ld_out = ld_dw;
+  a.V = (u32)V;
+  a.H = (u32)H;
+  a.T = (u32)T;
+  a.scale = scale;
+  a.keys = reinterpret_cast<u32 *>(ws + sp.keys);
+  a.order = reinterpret_cast<u32 *>(ws + sp.order);
+  a.part = reinterpret_cast<float *>(ws + ep.part);
+  a.rows = ep.rows;
+  a.chunks = ep.chunks;
+  a.strips = ep.strips;
+  a.sum_blocks = (u32)sum_blocks;
+  a.accumulate = accumulate;
+  if (T > 0) {
+    SortArgs s{};
+    s.ids = ids;
+    s.ld = id_stride;
+    s.first = first;
+    s.k = divider(1);
+    s.ids_i64 = id_type == MXTRAIN_I64;
+    s.n = (u32)T;
+    s.n_keys = (u32)V;
+    s.order = reinterpret_cast<int32_t *>(ws + sp.order);
+    s.key_out = reinterpret_cast<u32 *>(ws + sp.keys);
+    if ((st = sort_run(sp, s, ws, stream)) != MXTRAIN_OK) return st;
+  }
+  const bool f = dy_type == MXTRAIN_F32, g = dw_type == MXTRAIN_F32;
+  const void *sum = f ? (g ? (const void *)&k_embed_bwd<float, float> : (const void *)&k_embed_bwd<float, uint16_t>)
+                      : (g ? (const void *)&k_embed_bwd<uint16_t, float> : (const void *)&k_embed_bwd<uint16_t, uint16_t>);
+  st = launch(sum, sum_blocks + zero_blocks, 256, a, stream);
+  if (st != MXTRAIN_OK || ep.chunks <= 1) return st;
+  const void *join = f ? (g ? (const void *)&k_embed_join<float, float> : (const void *)&k_embed_join<float, uint16_t>)
+                       : (g ? (const void *)&k_embed_join<uint16_t, float> : (const void *)&k_embed_join<uint16_t, uint16_t>);
+  return launch(join, (int64_t)ep.chunks * ep.strips, 64, a, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,178 @@
+// mxtrain_sort.hip -- the stable sort's kernels and launches.
+#include "tr_sort_run.hpp"
+
+namespace mxt {
+
+// One workgroup sorts everything (n <= kSortTile).
+__global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
+  __shared__ SortShared<16> sm;
+  __shared__ u32 keys[kSortTile];
+  __shared__ uint16_t items[kSortTile];
+  const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, mask = (1u << a.bits) - 1;
+  // as few items a thread as hold n, so that the wavefronts share them
+  const u32 each = (a.n + kSortThreads - 1) / kSortThreads;
+  u32 key[kSortItems], item[kSortItems], digit[kSortItems], place[kSortItems];
+  u32 total = 0, base = 0;
+#pragma unroll
+  for (int i = 0; i < kSortItems; i++) {
+    const u32 p = (w * each + i) * 64 + lane;
+    item[i] = (u32)i < each && p < a.n ? p : ~0u;
+    key[i] = item[i] != ~0u ? sort_key(a, p) : 0;
+  }
+  for (u32 pass = 0; pass < a.passes; pass++) {
+    if (pass) {
+#pragma unroll
+      for (int i = 0; i < kSortItems; i++) {
+        const u32 p = (w * each + i) * 64 + lane;
+        if (item[i] == ~0u) continue;
+        key[i] = keys[p];
+        item[i] = items[p];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kSortItems; i++) digit[i] = item[i] != ~0u ? key[i] >> (pass * a.bits) & mask : ~0u;
+    total = rank_tile<16, kSortItems>(sm, digit, place, a.bits);
+    base = block_scan<16>(total, sm.wave);
+    if (threadIdx.x <= mask) sm.base[threadIdx.x] = base;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kSortItems; i++) {
+      if (item[i] == ~0u) continue;
+      const u32 to = sm.base[digit[i]] + place[i];
+      if (pass + 1 < a.passes || (a.passes > 1 && a.ends)) {
+        keys[to] = key[i];
+        items[to] = (uint16_t)item[i];
+      }
+      if (pass + 1 == a.passes) sort_result(a, item[i], key[i], to);
+    }
+    __syncthreads();
+  }
+  if (!a.ends) return;
+  if (a.passes == 1) {
+    if (threadIdx.x < a.n_keys) *gptr(a.ends + threadIdx.x) = (int32_t)(base + total);
+  } else {
+    for (u32 v = threadIdx.x; v < a.n_keys; v += kSortThreads) *gptr(a.ends + v) = (int32_t)keys_up_to(keys, a.n, v);
+  }
+}
+
+__device__ __forceinline__ u32 sort_source(const SortArgs &a, u32 p, u32 &item) {
+  item = a.is_first ? p : *gptr(a.item_in + p);
+  return a.is_first ? sort_key(a, p) : *gptr(a.key_in + p);
+}
+
+// counts[b][d]: items of workgroup b's range with digit d.
+__global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
+  __shared__ u32 count[1 << kSortBits];
+  const u32 bins = 1u << a.bits, lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
+  if (threadIdx.x < bins) count[threadIdx.x] = 0;
+  __syncthreads();
+  for (u32 p = lo + threadIdx.x; p < hi; p += kSortThreads) {
+    const u32 key = a.is_first ? sort_key(a, p) : *gptr(a.key_in + p);
+    atomicAdd(&count[key >> a.shift & (bins - 1)], 1u);
+  }
+  __syncthreads();
+  if (threadIdx.x < bins) *gptr(a.counts + (blockIdx.x << a.bits) + threadIdx.x) = count[threadIdx.x];
+}
+
+// Moves workgroup b's range to its places.
+__global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
+  __shared__ SortShared<16> sm;
+  __shared__ u32 sums[2][kSortThreads];
+  const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, bins = 1u << a.bits, mask = bins - 1;
+  {
+    // thread (part, d): digit d in every (1024 / bins)-th workgroup's counts
+    const u32 d = threadIdx.x & mask, parts = kSortThreads >> a.bits;
+    u32 all = 0, before = 0;
+#pragma unroll 8
+    for (u32 b = threadIdx.x >> a.bits; b < a.blocks; b += parts) {
+      const u32 c = *gptr(a.counts + (b << a.bits) + d);
+      all += c;
+      before += b < blockIdx.x ? c : 0;
+    }
+    sums[0][threadIdx.x] = all;
+    sums[1][threadIdx.x] = before;
+    __syncthreads();
+    all = before = 0;
+    if (threadIdx.x < bins)
+      for (u32 i = 0; i < parts; i++) {
+        all += sums[0][(i << a.bits) + threadIdx.x];
+        before += sums[1][(i << a.bits) + threadIdx.x];
+      }
+    const u32 base = block_scan<16>(all, sm.wave);
+    if (threadIdx.x < bins) sm.base[threadIdx.x] = base + before;
+    if (a.ends && blockIdx.x == 0 && threadIdx.x < a.n_keys) *gptr(a.ends + threadIdx.x) = (int32_t)(base + all);
+  }
+  const u32 lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
+  for (u32 tile = lo; tile < hi; tile += kSortTile) {
+    const u32 here = min(hi - tile, (u32)kSortTile), each = (here + kSortThreads - 1) / kSortThreads;
+    u32 key[kSortItems], item[kSortItems], digit[kSortItems], place[kSortItems];
+#pragma unroll
+    for (int i = 0; i < kSortItems; i++) {
+      const u32 p = (w * each + i) * 64 + lane;
+      digit[i] = ~0u;
+      if ((u32)i < each && p < here) {
+        key[i] = sort_source(a, tile + p, item[i]);
+        digit[i] = key[i] >> a.shift & mask;
+      }
+    }
+    const u32 total = rank_tile<16, kSortItems>(sm, digit, place, a.bits);
+    // rank_tile's barriers also lie between sm.base's last write and here
+#pragma unroll
+    for (int i = 0; i < kSortItems; i++) {
+      if (digit[i] == ~0u) continue;
+      const u32 to = sm.base[digit[i]] + place[i];
+      if (a.is_last) {
+        sort_result(a, item[i], key[i], to);
+      } else {
+        *gptr(a.key_out + to) = key[i];
+        *gptr(a.item_out + to) = item[i];
+      }
+    }
+    __syncthreads();
+    if (threadIdx.x < bins) sm.base[threadIdx.x] += total;
+  }
+}
+
+// ends[v] from the n sorted keys.
+__global__ __launch_bounds__(256) void k_sort_ends(const u32 *keys, u32 n, u32 n_keys, int32_t *ends) {
+  for (u32 v = blockIdx.x * 256 + threadIdx.x; v < n_keys; v += gridDim.x * 256)
+    *gptr(ends + v) = (int32_t)keys_up_to(gptr(keys), n, v);
+}
+
+mxtrain_status sort_run(const SortPlan &p, SortArgs a, uint8_t *ws, void *stream) {
+  a.adjacent = a.ld == (int64_t)a.k.d;
+  a.bits = p.bits;
+  a.passes = p.passes;
+  if (p.small) return launch((const void *)&k_sort_small, 1, kSortThreads, a, stream);
+  a.blocks = p.blocks;
+  a.per = p.per;
+  a.counts = reinterpret_cast<u32 *>(ws + p.counts);
+  int32_t *const ends = a.ends;
+  u32 *const sorted = a.key_out ? a.key_out : p.passes > 1 ? reinterpret_cast<u32 *>(ws + p.keys) : nullptr;
+  if (p.passes > 1) a.ends = nullptr;
+  for (uint32_t pass = 0; pass < p.passes; pass++) {
+    a.is_first = pass == 0;
+    a.is_last = pass + 1 == p.passes;
+    a.shift = pass * p.bits;
+    if (!a.is_first) {
+      a.key_in = reinterpret_cast<u32 *>(ws + p.pair[(pass - 1) % 2]);
+      a.item_in = a.key_in + a.n;
+    }
+    a.key_out = a.is_last ? sorted : reinterpret_cast<u32 *>(ws + p.pair[pass % 2]);
+    a.item_out = a.is_last ? nullptr : a.key_out + a.n;
+    mxtrain_status st = launch((const void *)&k_sort_count, p.blocks, kSortThreads, a, stream);
+    if (st == MXTRAIN_OK) st = launch((const void *)&k_sort_move, p.blocks, kSortThreads, a, stream);
+    if (st != MXTRAIN_OK) return st;
+  }
+  if (!ends || p.passes == 1) return MXTRAIN_OK;
+  const u32 *keys = sorted;
+  u32 n = a.n, n_keys = a.n_keys;
+  int32_t *out = ends;
+  void *kargs[] = {&keys, &n, &n_keys, &out};
+  const unsigned grid = (unsigned)std::min<int64_t>((n_keys + 255) / 256, 2048);
+  return hipLaunchKernel((const void *)&k_sort_ends, dim3(grid), dim3(256), kargs, 0, (hipStream_t)stream) == hipSuccess
+             ? MXTRAIN_OK
+             : MXTRAIN_ERR_LAUNCH;
+}
+
+}  // namespace mxt

@@ -1,0 +1,71 @@
+// tr_dropout.hpp -- dropout with a recomputed mask (gfx950).
+//
+//   y = residual + (r >= border ? x scale : 0),
+//   border = p 65536, scale = 65536 / (65536 - border),
+// where r are 16 bits of the Philox4x32-10 block of the element's eight
+// columns (Salmon, Moraes, Dror and Shaw, 2011: ten rounds, each two 32 x 32 ->
+// 64 bit products and four exclusive ors, with a key that grows by two constants).
+//
+// Bound by HBM as long as the block's cost, twenty products for eight elements,
+// stays below the time of their bytes.
+#pragma once
+#include "tr_rows.hpp"
+
+namespace mxt {
+
+struct DropArgs {
+  const void *x, *res;
+  void *y;
+  int64_t ld_x, ld_res, ld_y;
+  Pieces pieces;  // of eight columns
+  u32 N, border;
+  float scale;
+  uint64_t seed, offset;
+  const uint64_t *state;
+};
+
+__device__ __forceinline__ void philox(u32 (&c)[4], u32 k0, u32 k1) {
+#pragma unroll
+  for (int r = 0; r < 10; r++) {
+    const uint64_t a = (uint64_t)c[0] * 0xD2511F53u, b = (uint64_t)c[2] * 0xCD9E8D57u;
+    c[0] = (u32)(b >> 32) ^ c[1] ^ k0;
+    c[1] = (u32)b;
+    c[2] = (u32)(a >> 32) ^ c[3] ^ k1;
+    c[3] = (u32)a;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+}
+
+template <class T, bool RES>
+__global__ __launch_bounds__(256) void k_dropout(const DropArgs a) {
+  uint64_t seed = a.seed, offset = a.offset;
+  if (a.state) {
+    seed += *gptr(a.state);
+    offset += *gptr(a.state + 1);
+  }
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= a.pieces.total) continue;
+    int64_t row;
+    u32 piece;
+    place_of(a.pieces, first, threadIdx.x, row, piece);
+    const u32 col = piece * 8;
+    const int n = (int)min(8u, a.N - col);
+    Piece<T, 8> x, r;
+    x.load(static_cast<const T *>(a.x) + row * a.ld_x + col, n);
+    if constexpr (RES) r.load(static_cast<const T *>(a.res) + row * a.ld_res + col, n);
+    u32 c[4] = {piece, (u32)row, (u32)offset, (u32)(offset >> 32)};
+    philox(c, (u32)seed, (u32)(seed >> 32));
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+      const u32 bits = i % 2 ? c[i / 2] >> 16 : c[i / 2] & 0xffffu;
+      y[i] = bits >= a.border ? x.get(i) * a.scale : 0.0f;
+      if constexpr (RES) y[i] += r.get(i);
+    }
+    x.set(y);
+    x.store(static_cast<T *>(a.y) + row * a.ld_y + col, n);
+  }
+}
+
+}  // namespace mxt

@@ -1,0 +1,153 @@
+// tr_sort.hpp -- stable sort of small integer keys (gfx950): tokens by expert,
+// tokens by word.
+//
+// A pass sorts by one digit of at most 10 bits, least significant first: an
+// item's place is the number of items with a smaller digit plus the number of
+// earlier ones with the same.  A key is id - first, or n_keys where that is
+// not in [0, n_keys): dropped items come last.
+//
+// Within a wavefront, the lanes with the same digit find each other by one
+// ballot for each bit; a lane's place among them is the number of lower lanes,
+// and the lowest adds their number to the wavefront's count of that digit.  The
+// wavefronts' counts are then summed in order.  No order of execution enters, so
+// the result is the one stable order.
+//
+// Up to 8192 items, one workgroup does all passes in LDS.  More are dealt to
+// up to 256 workgroups in contiguous ranges, and a pass is two launches: each
+// workgroup counts its digits, and then each adds up the counts of all
+// workgroups (from L2) to know its first place for every digit, and moves
+// its items.
+#pragma once
+#include "tr_rows.hpp"
+
+namespace mxt {
+
+constexpr int kSortBits = 10;               // most bits of a digit
+constexpr int kSortThreads = 1024;          // and, one digit a thread, of most digits
+constexpr int kSortItems = 8;               // items a thread in one tile
+constexpr int kSortTile = kSortThreads * kSortItems;
+constexpr int kSortBlocks = 256;
+
+struct SortArgs {
+  const void *ids;  // the keys' source in the first pass: [n / k, k] with row stride ld
+  int64_t ld, first;
+  Divider k;
+  int32_t ids_i64, adjacent;  // int64 ids; ld == k
+  u32 n, n_keys;
+  const u32 *key_in, *item_in;  // the source of later passes
+  u32 *key_out, *item_out;      // the next pass's source; in the last pass the sorted keys, or NULL
+  int32_t *order, *rank, *ends;  // written by the last pass, each may be NULL; ends only where one pass does
+  u32 *counts;                   // [blocks][1 << bits]
+  u32 shift, bits, blocks, per;  // this pass's digit; workgroups and items of each (a multiple of 1024)
+  u32 passes;                    // one workgroup: passes of `bits` bits each
+  int32_t is_first, is_last;
+};
+
+__device__ __forceinline__ u32 sort_key(const SortArgs &a, u32 item) {
+  int64_t at = item;
+  if (!a.adjacent) {
+    const u32 t = a.k.div(item);
+    at = (int64_t)t * a.ld + (item - t * a.k.d);
+  }
+  const int64_t id = a.ids_i64 ? *gptr(static_cast<const int64_t *>(a.ids) + at)
+                               : (int64_t)*gptr(static_cast<const int32_t *>(a.ids) + at);
+  // (first + n_keys fits 64 bits, so a difference that wraps is not below n_keys)
+  const uint64_t key = (uint64_t)id - (uint64_t)a.first;
+  return key < a.n_keys ? (u32)key : a.n_keys;
+}
+
+// LDS of a workgroup of W wavefronts that ranks a tile.
+template <int W>
+struct SortShared {
+  uint16_t count[W][W * 64];  // a tile has at most 8192 items
+  u32 base[W * 64];           // first place of each digit
+  u32 wave[W];
+};
+
+// Exclusive sum of v over the threads of the workgroup (one barrier inside; `sm`
+// must not be in use).
+template <int W>
+__device__ __forceinline__ u32 block_scan(u32 v, u32 *sm) {
+  const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  u32 s = v;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const u32 t = __shfl_up(s, o, 64);
+    if (lane >= (u32)o) s += t;
+  }
+  if (lane == 63) sm[w] = s;
+  __syncthreads();
+  u32 before = 0;
+#pragma unroll
+  for (int i = 0; i < W; i++) before += i < (int)w ? sm[i] : 0;
+  return before + s - v;
+}
+
+// Ranks one tile: digit[i] of this thread's item i (~0u: none), items in the order
+// (wavefront, i, lane).  place[i] becomes the number of earlier items of the tile
+// with that digit; thread d of those below 1 << bits gets digit d's number of
+// items.  Ends with a barrier.
+template <int W, int ITEMS>
+__device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u32 *place, u32 bits) {
+  const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, bins = 1u << bits;
+  for (u32 d = lane; d < bins; d += 64) sm.count[w][d] = 0;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) {
+    const bool have = digit[i] != ~0u;
+    uint64_t same = __ballot(have);
+    if (same == 0) break;
+    for (u32 b = 0; b < bits; b++) {
+      const bool one = digit[i] >> b & 1u;
+      const uint64_t with = __ballot(one);
+      same &= one ? with : ~with;
+    }
+    const u32 lower = __popcll(same & ((1ull << lane) - 1));
+    if (have) {
+      const u32 before = sm.count[w][digit[i]];
+      place[i] = before + lower;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (lower == 0) sm.count[w][digit[i]] = (uint16_t)(before + __popcll(same));
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  u32 total = 0;
+  if (threadIdx.x < bins) {
+#pragma unroll
+    for (int i = 0; i < W; i++) {
+      const u32 c = sm.count[i][threadIdx.x];
+      sm.count[i][threadIdx.x] = (uint16_t)total;
+      total += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++)
+    if (digit[i] != ~0u) place[i] += sm.count[w][digit[i]];
+  return total;
+}
+
+// Writes what the last pass leaves: `item` of key `key` goes to `place`.
+__device__ __forceinline__ void sort_result(const SortArgs &a, u32 item, u32 key, u32 place) {
+  const bool kept = key < a.n_keys;
+  if (a.order) *gptr(a.order + place) = kept ? (int32_t)item : -1;
+  if (a.rank) *gptr(a.rank + item) = kept ? (int32_t)place : -1;
+  if (a.key_out) *gptr(a.key_out + place) = key;
+}
+
+// Number of the n ascending keys that are at most `v`.
+template <class P>
+__device__ __forceinline__ u32 keys_up_to(P keys, u32 n, u32 v) {
+  u32 lo = 0, hi = n;
+  while (lo < hi) {
+    const u32 mid = lo + (hi - lo) / 2;
+    if (keys[mid] <= v) lo = mid + 1;
+    else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace mxt

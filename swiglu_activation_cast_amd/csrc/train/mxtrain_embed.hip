@@ -29,7 +29,33 @@ mxtrain_status embed_check(const void *table, int64_t ld_w, int w_type, const vo
   return MXTRAIN_OK;
 }
 
-int64_t embed_vec(int t, int u) { return t == MXTRAIN_F32 && u == MXTRAIN_F32 ? 4 : 8; }
+// Columns that a thread holds.
+int64_t embed_vec(int t, int u, int64_t H) {
+  const int64_t vec = t == MXTRAIN_F32 && u == MXTRAIN_F32 ? 4 : 8;
+  return H < vec ? 1 : vec;
+}
+
+// fn<T, U, VEC>(...) for the rows' and the results' types.
+#define EMBED_PICK(fn, vec, t_f32, u_f32, ...)                                                             \
+  ((vec) == 1 ? (t_f32 ? (u_f32 ? fn<float, float, 1>(__VA_ARGS__) : fn<float, uint16_t, 1>(__VA_ARGS__))  \
+                       : (u_f32 ? fn<uint16_t, float, 1>(__VA_ARGS__) : fn<uint16_t, uint16_t, 1>(__VA_ARGS__))) \
+              : (t_f32 ? (u_f32 ? fn<float, float, 4>(__VA_ARGS__) : fn<float, uint16_t, 8>(__VA_ARGS__))  \
+                       : (u_f32 ? fn<uint16_t, float, 8>(__VA_ARGS__) : fn<uint16_t, uint16_t, 8>(__VA_ARGS__))))
+
+template <class T, class U, int VEC>
+const void *lookup_kernel(bool many) {
+  return many ? (const void *)&k_embed<T, U, VEC, 2> : (const void *)&k_embed<T, U, VEC, 1>;
+}
+
+template <class T, class U, int VEC>
+const void *sum_kernel() {
+  return (const void *)&k_embed_bwd<T, U, VEC>;
+}
+
+template <class T, class U, int VEC>
+const void *join_kernel() {
+  return (const void *)&k_embed_join<T, U, VEC>;
+}
 
 // How the gradient cuts its work: chunks of 64 tokens, or fewer where that
 // leaves less than sixteen wavefronts to a compute unit.
@@ -77,16 +103,20 @@ mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weigh
   a.T = (u32)T;
   a.scale = scale;
   const bool f = weight_type == MXTRAIN_F32, g = y_type == MXTRAIN_F32;
-  const int64_t vec = embed_vec(weight_type, y_type), per = (H + vec - 1) / vec;
+  const int64_t vec = embed_vec(weight_type, y_type, H), per = (H + vec - 1) / vec;
   a.pieces = {T * per, divider((uint32_t)per)};
-  const void *kernel = f ? (g ? (const void *)&k_embed<float, float> : (const void *)&k_embed<float, uint16_t>)
-                         : (g ? (const void *)&k_embed<uint16_t, float> : (const void *)&k_embed<uint16_t, uint16_t>);
-  return launch(kernel, std::min<int64_t>((a.pieces.total + 255) / 256, INT32_MAX / 256), 256, a, stream);
+  // two pieces a thread where that leaves every compute unit eight workgroups:
+  // 16640 rows of 5120 bf16 51 us, 60 with one and 50 with four; 65537 of 2050 61
+  // with two and 71 with four
+  const bool many = a.pieces.total >= 2 * 256 * 2048;
+  const void *kernel = EMBED_PICK(lookup_kernel, vec, f, g, many);
+  const int64_t step = many ? 512 : 256;
+  return launch(kernel, std::min<int64_t>((a.pieces.total + step - 1) / step, INT32_MAX / 256), 256, a, stream);
 }
 
 int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_type, int dw_type) {
   if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
-  return embed_plan(sort_plan(T, V, true), T, H, embed_vec(dy_type, dw_type)).bytes;
+  return embed_plan(sort_plan(T, V, true), T, H, embed_vec(dy_type, dw_type, H)).bytes;
 }
 
 mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type, const void *ids, int64_t id_stride,
@@ -99,12 +129,15 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   if (accumulate != 0 && accumulate != 1) return MXTRAIN_ERR_VALUE;
   if (V == 0 || H == 0 || (T == 0 && accumulate)) return MXTRAIN_OK;
   const SortPlan sp = sort_plan(T, V, true);
-  const EmbedPlan ep = embed_plan(sp, T, H, embed_vec(dy_type, dw_type));
+  const EmbedPlan ep = embed_plan(sp, T, H, embed_vec(dy_type, dw_type, H));
   if (T > 0 && !workspace) return MXTRAIN_ERR_NULL;
   if (T > 0 && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
   if (T > 0 && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
-  const int64_t sum_blocks = ((int64_t)ep.chunks * ep.strips + 3) / 4, zero_blocks = accumulate ? 0 : (V + 63) / 64;
-  if (sum_blocks + zero_blocks > INT32_MAX / 256 || (int64_t)ep.chunks * ep.strips > INT32_MAX / 64)
+  // words whose rows a workgroup clears: few enough for 2048 workgroups
+  int64_t zero_rows = 4;
+  while (zero_rows < 64 && V > zero_rows * 4096) zero_rows *= 2;
+  const int64_t sum_blocks = ((int64_t)ep.chunks * ep.strips + 3) / 4, zero_blocks = accumulate ? 0 : (V + zero_rows - 1) / zero_rows;
+  if (sum_blocks + zero_blocks > INT32_MAX / 256 || (int64_t)ep.chunks * ep.strips > INT32_MAX / 256)
     return MXTRAIN_ERR_OVERFLOW;
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   EmbedArgs a{};
@@ -123,6 +156,7 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   a.chunks = ep.chunks;
   a.strips = ep.strips;
   a.sum_blocks = (u32)sum_blocks;
+  a.zero_rows = (u32)zero_rows;
   a.accumulate = accumulate;
   if (T > 0) {
     SortArgs s{};
@@ -138,13 +172,10 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
     if ((st = sort_run(sp, s, ws, stream)) != MXTRAIN_OK) return st;
   }
   const bool f = dy_type == MXTRAIN_F32, g = dw_type == MXTRAIN_F32;
-  const void *sum = f ? (g ? (const void *)&k_embed_bwd<float, float> : (const void *)&k_embed_bwd<float, uint16_t>)
-                      : (g ? (const void *)&k_embed_bwd<uint16_t, float> : (const void *)&k_embed_bwd<uint16_t, uint16_t>);
-  st = launch(sum, sum_blocks + zero_blocks, 256, a, stream);
+  const int64_t vec = embed_vec(dy_type, dw_type, H);
+  st = launch(EMBED_PICK(sum_kernel, vec, f, g), sum_blocks + zero_blocks, 256, a, stream);
   if (st != MXTRAIN_OK || ep.chunks <= 1) return st;
-  const void *join = f ? (g ? (const void *)&k_embed_join<float, float> : (const void *)&k_embed_join<float, uint16_t>)
-                       : (g ? (const void *)&k_embed_join<uint16_t, float> : (const void *)&k_embed_join<uint16_t, uint16_t>);
-  return launch(join, (int64_t)ep.chunks * ep.strips, 64, a, stream);
+  return launch(EMBED_PICK(join_kernel, vec, f, g), (int64_t)ep.chunks * ep.strips, 256, a, stream);
 }
 
 }  // extern "C"

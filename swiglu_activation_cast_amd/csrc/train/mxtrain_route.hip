@@ -4,7 +4,6 @@
 #include "mxtrain_tokens.h"
 #include "tr_route.hpp"
 #include "tr_sort_run.hpp"
-
 using namespace mxt;
 
 namespace mxt {
@@ -70,9 +69,15 @@ mxtrain_status route_check(const void *tokens, int64_t ld_t, const void *rows, i
   return matrix_check(rows, R, H, ld_r, dtype);
 }
 
+// Elements of a piece of rows of H: 16 bytes' worth, or single ones.
+int64_t route_vec(int dtype, int64_t H) {
+  const int64_t vec = 16 / size_of(dtype);
+  return H < vec ? 1 : vec;
+}
+
 RouteArgs route_args(const int32_t *rank, int dtype, int64_t T, int64_t k, int64_t H, int64_t R) {
   RouteArgs a{};
-  const int64_t vec = 16 / size_of(dtype), per = (H + vec - 1) / vec;
+  const int64_t vec = route_vec(dtype, H), per = (H + vec - 1) / vec;
   a.rank = rank;
   a.T = T;
   a.k = (u32)k;
@@ -82,8 +87,45 @@ RouteArgs route_args(const int32_t *rank, int dtype, int64_t T, int64_t k, int64
   return a;
 }
 
-mxtrain_status route_launch(const void *f32, const void *bf16, int dtype, const RouteArgs &a, void *stream) {
-  return launch(dtype == MXTRAIN_F32 ? f32 : bf16, std::min((a.pieces.total + 255) / 256, kMaxGrid), 256, a, stream);
+template <class T, int VEC>
+const void *dispatch_kernel() {
+  return (const void *)&k_dispatch<T, VEC>;
+}
+
+// wtype: the weights', -1: none.
+template <class T, int VEC, bool NT>
+const void *combine_kernel_nt(int wtype) {
+  return wtype < 0 ? (const void *)&k_combine<T, void, VEC, NT>
+         : wtype == MXTRAIN_F32 ? (const void *)&k_combine<T, float, VEC, NT>
+                                : (const void *)&k_combine<T, uint16_t, VEC, NT>;
+}
+
+template <class T, int VEC>
+const void *combine_kernel(int wtype, bool nt) {
+  if constexpr (VEC > 1)
+    if (nt) return combine_kernel_nt<T, VEC, true>(wtype);
+  return combine_kernel_nt<T, VEC, false>(wtype);
+}
+
+template <class T, int VEC>
+const void *combine_bwd_kernel(int wtype) {
+  return wtype == MXTRAIN_F32 ? (const void *)&k_combine_bwd<T, float, VEC> : (const void *)&k_combine_bwd<T, uint16_t, VEC>;
+}
+
+// fn<T, VEC>(...) for the rows' type and width.
+#define ROUTE_PICK(fn, dtype, H, ...)                                                          \
+  (dtype == MXTRAIN_F32 ? (route_vec(dtype, H) > 1 ? fn<float, 4>(__VA_ARGS__) : fn<float, 1>(__VA_ARGS__)) \
+                        : (route_vec(dtype, H) > 1 ? fn<uint16_t, 8>(__VA_ARGS__) : fn<uint16_t, 1>(__VA_ARGS__)))
+
+mxtrain_status route_launch(const void *kernel, const RouteArgs &a, void *stream) {
+  return launch(kernel, std::min((a.pieces.total + 255) / 256, kMaxGrid), 256, a, stream);
+}
+
+// Whether combine reads past the caches: rows of 128 MB or more (half the last
+// level's 256 MB).  16384 x 8 rows of 2048 bf16 126 us otherwise, 117 so; 4096 x
+// 8 29 and 26; but 2048 x 8 13.5 and 14.0, and odd fp32 rows of 43 MB 14.0 and 15.7.
+bool route_past_caches(int dtype, int64_t T, int64_t k, int64_t H) {
+  return (double)T * (double)k * (double)H * size_of(dtype) >= (double)(1 << 27);
 }
 
 }  // namespace
@@ -117,7 +159,7 @@ mxtrain_status mxtrain_dispatch_fwd(const void *x, int64_t ld_x, int dtype, cons
   a.ld_in = ld_x;
   a.out = xs;
   a.ld_out = ld_xs;
-  return route_launch((const void *)&k_dispatch<float>, (const void *)&k_dispatch<uint16_t>, dtype, a, stream);
+  return route_launch(ROUTE_PICK(dispatch_kernel, dtype, H), a, stream);
 }
 
 mxtrain_status mxtrain_sort_dispatch(const void *x, int64_t ld_x, int dtype, const void *ids, int64_t ld_ids,
@@ -150,8 +192,7 @@ mxtrain_status mxtrain_combine_fwd(const void *ys, int64_t ld_ys, int dtype, con
   a.out = y;
   a.ld_out = ld_y;
   a.weights = weights;
-  a.w_f32 = weight_type == MXTRAIN_F32;
-  return route_launch((const void *)&k_combine<float>, (const void *)&k_combine<uint16_t>, dtype, a, stream);
+  return route_launch(ROUTE_PICK(combine_kernel, dtype, H, weight_type, route_past_caches(dtype, T, k, H)), a, stream);
 }
 
 mxtrain_status mxtrain_dispatch_bwd(const void *dxs, int64_t ld_dxs, int dtype, const int32_t *rank, int64_t T,
@@ -164,7 +205,7 @@ mxtrain_status mxtrain_dispatch_bwd(const void *dxs, int64_t ld_dxs, int dtype, 
   a.ld_in = ld_dxs;
   a.out = dx;
   a.ld_out = ld_dx;
-  return route_launch((const void *)&k_combine<float>, (const void *)&k_combine<uint16_t>, dtype, a, stream);
+  return route_launch(ROUTE_PICK(combine_kernel, dtype, H, -1, route_past_caches(dtype, T, k, H)), a, stream);
 }
 
 mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys, int64_t ld_ys, int dtype,
@@ -185,11 +226,17 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
   a.out = dys;
   a.ld_out = ld_dys;
   a.weights = weights;
-  a.w_f32 = weight_type == MXTRAIN_F32;
   a.dw = dweights;
   if (H == 0) a.pieces.per.d = 0;
-  return launch(dtype == MXTRAIN_F32 ? (const void *)&k_combine_bwd<float> : (const void *)&k_combine_bwd<uint16_t>,
-                std::min((T + 3) / 4, kMaxGrid), 256, a, stream);
+  // Wavefronts of a token: about four, so that each walks its pieces in equal
+  // steps of one; more, up to one a step, where there are few tokens.
+  // (16384 x 8 rows of 2048 bf16: one wavefront 243 us, four 226.  1021 x 2 rows of
+  // 2049 fp32: sixteen 18 us, four 13.)
+  const int64_t per = a.pieces.per.d;
+  int64_t steps = std::max<int64_t>(1, (per + 128) / 256);
+  while (steps > 1 && T * ((per + 64 * steps - 1) / (64 * steps)) < 1024) steps--;
+  const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (per + 64 * steps - 1) / (64 * steps)));
+  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type), std::min(T, kMaxGrid), 64 * waves, a, stream);
 }
 
 }  // extern "C"

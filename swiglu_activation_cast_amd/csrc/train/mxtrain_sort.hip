@@ -17,8 +17,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
   for (int i = 0; i < kSortItems; i++) {
     const u32 p = (w * each + i) * 64 + lane;
     item[i] = (u32)i < each && p < a.n ? p : ~0u;
-    key[i] = item[i] != ~0u ? sort_key(a, p) : 0;
   }
+  sort_keys<kSortItems>(a, item, key);
   for (u32 pass = 0; pass < a.passes; pass++) {
     if (pass) {
 #pragma unroll
@@ -55,9 +55,21 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
   }
 }
 
-__device__ __forceinline__ u32 sort_source(const SortArgs &a, u32 p, u32 &item) {
-  item = a.is_first ? p : *gptr(a.item_in + p);
-  return a.is_first ? sort_key(a, p) : *gptr(a.key_in + p);
+// Keys and items of the places p[i] (~0u: none) of a pass's source.
+template <int ITEMS>
+__device__ __forceinline__ void sort_source(const SortArgs &a, const u32 *p, u32 *key, u32 *item) {
+  if (a.is_first) {
+    sort_keys<ITEMS>(a, p, key);
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++) item[i] = p[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++)
+      if (p[i] != ~0u) {
+        key[i] = *gptr(a.key_in + p[i]);
+        item[i] = *gptr(a.item_in + p[i]);
+      }
+  }
 }
 
 // counts[b][d]: items of workgroup b's range with digit d.
@@ -67,7 +79,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
   if (threadIdx.x < bins) count[threadIdx.x] = 0;
   __syncthreads();
   for (u32 p = lo + threadIdx.x; p < hi; p += kSortThreads) {
-    const u32 key = a.is_first ? sort_key(a, p) : *gptr(a.key_in + p);
+    u32 key, item;
+    sort_source<1>(a, &p, &key, &item);
     atomicAdd(&count[key >> a.shift & (bins - 1)], 1u);
   }
   __syncthreads();
@@ -79,6 +92,19 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   __shared__ SortShared<16> sm;
   __shared__ u32 sums[2][kSortThreads];
   const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, bins = 1u << a.bits, mask = bins - 1;
+  const u32 lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
+  u32 key[kSortItems], item[kSortItems], digit[kSortItems], place[kSortItems];
+  // the places of a tile that this thread takes
+  auto fetch = [&](u32 tile) {
+    const u32 here = min(hi - tile, (u32)kSortTile), each = (here + kSortThreads - 1) / kSortThreads;
+#pragma unroll
+    for (int i = 0; i < kSortItems; i++) {
+      const u32 p = (w * each + i) * 64 + lane;
+      digit[i] = (u32)i < each && p < here ? tile + p : ~0u;
+    }
+    sort_source<kSortItems>(a, digit, key, item);
+  };
+  fetch(lo);  // in flight while the counts are added up
   {
     // thread (part, d): digit d in every (1024 / bins)-th workgroup's counts
     const u32 d = threadIdx.x & mask, parts = kSortThreads >> a.bits;
@@ -102,19 +128,11 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
     if (threadIdx.x < bins) sm.base[threadIdx.x] = base + before;
     if (a.ends && blockIdx.x == 0 && threadIdx.x < a.n_keys) *gptr(a.ends + threadIdx.x) = (int32_t)(base + all);
   }
-  const u32 lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
   for (u32 tile = lo; tile < hi; tile += kSortTile) {
-    const u32 here = min(hi - tile, (u32)kSortTile), each = (here + kSortThreads - 1) / kSortThreads;
-    u32 key[kSortItems], item[kSortItems], digit[kSortItems], place[kSortItems];
+    if (tile > lo) fetch(tile);
 #pragma unroll
-    for (int i = 0; i < kSortItems; i++) {
-      const u32 p = (w * each + i) * 64 + lane;
-      digit[i] = ~0u;
-      if ((u32)i < each && p < here) {
-        key[i] = sort_source(a, tile + p, item[i]);
-        digit[i] = key[i] >> a.shift & mask;
-      }
-    }
+    for (int i = 0; i < kSortItems; i++)
+      if (digit[i] != ~0u) digit[i] = key[i] >> a.shift & mask;
     const u32 total = rank_tile<16, kSortItems>(sm, digit, place, a.bits);
     // rank_tile's barriers also lie between sm.base's last write and here
 #pragma unroll

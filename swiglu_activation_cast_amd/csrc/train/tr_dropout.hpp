@@ -17,7 +17,7 @@ struct DropArgs {
   const void *x, *res;
   void *y;
   int64_t ld_x, ld_res, ld_y;
-  Pieces pieces;  // of eight columns
+  Pieces pieces;  // of 16 bytes
   u32 N, border;
   float scale;
   uint64_t seed, offset;
@@ -37,8 +37,12 @@ __device__ __forceinline__ void philox(u32 (&c)[4], u32 k0, u32 k1) {
   }
 }
 
-template <class T, bool RES>
+// A piece is 16 bytes: eight bf16 columns and their block, or four fp32 ones and
+// half of theirs (which the neighbouring lane computes too: as much of the
+// generator for a byte).
+template <class T, bool RES, bool NT>
 __global__ __launch_bounds__(256) void k_dropout(const DropArgs a) {
+  constexpr int VEC = 16 / (int)sizeof(T);
   uint64_t seed = a.seed, offset = a.offset;
   if (a.state) {
     seed += *gptr(a.state);
@@ -49,22 +53,35 @@ __global__ __launch_bounds__(256) void k_dropout(const DropArgs a) {
     int64_t row;
     u32 piece;
     place_of(a.pieces, first, threadIdx.x, row, piece);
-    const u32 col = piece * 8;
-    const int n = (int)min(8u, a.N - col);
-    Piece<T, 8> x, r;
-    x.load(static_cast<const T *>(a.x) + row * a.ld_x + col, n);
-    if constexpr (RES) r.load(static_cast<const T *>(a.res) + row * a.ld_res + col, n);
-    u32 c[4] = {piece, (u32)row, (u32)offset, (u32)(offset >> 32)};
+    const u32 col = piece * VEC;
+    const int n = (int)min((u32)VEC, a.N - col);
+    const T *px = static_cast<const T *>(a.x) + row * a.ld_x + col;
+    const T *pr = RES ? static_cast<const T *>(a.res) + row * a.ld_res + col : nullptr;
+    Piece<T, VEC> x, r;
+    if (n == VEC) {
+      x.template load<NT>(px);
+      if constexpr (RES) r.template load<NT>(pr);
+    } else {
+      x.load(px, n);
+      if constexpr (RES) r.load(pr, n);
+    }
+    u32 c[4] = {col / 8, (u32)row, (u32)offset, (u32)(offset >> 32)};
     philox(c, (u32)seed, (u32)(seed >> 32));
-    float y[8];
+    if (VEC == 4 && piece % 2) {
+      c[0] = c[2];
+      c[1] = c[3];
+    }
+    float y[VEC];
 #pragma unroll
-    for (int i = 0; i < 8; i++) {
+    for (int i = 0; i < VEC; i++) {
       const u32 bits = i % 2 ? c[i / 2] >> 16 : c[i / 2] & 0xffffu;
       y[i] = bits >= a.border ? x.get(i) * a.scale : 0.0f;
       if constexpr (RES) y[i] += r.get(i);
     }
     x.set(y);
-    x.store(static_cast<T *>(a.y) + row * a.ld_y + col, n);
+    T *py = static_cast<T *>(a.y) + row * a.ld_y + col;
+    if (n == VEC) x.store(py);
+    else x.store(py, 0, n);
   }
 }
 

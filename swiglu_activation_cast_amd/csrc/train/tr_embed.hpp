@@ -31,85 +31,117 @@ struct EmbedArgs {
   u32 rows;                 // tokens of a chunk
   u32 chunks, strips;       // and of the columns, 64 pieces each
   u32 sum_blocks;           // workgroups that sum; those after them write zeros
+  u32 zero_rows;            // to the rows of so many words each, at most 64
   int32_t accumulate;
 };
 
-// Columns that a thread holds: 16 bytes of the narrower type.
-template <class T, class U>
-constexpr int kEmbedVec = sizeof(T) == 4 && sizeof(U) == 4 ? 4 : 8;
-
-template <class T, class U>
+// VEC, here and below: columns that a thread holds, 16 bytes of the narrower type,
+// or 1 where rows are shorter than that.
+template <class T, class U, int VEC, int N>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
-  constexpr int VEC = kEmbedVec<T, U>;
-  for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
-    if (first + threadIdx.x >= a.pieces.total) continue;
-    int64_t t;
-    u32 c;
-    place_of(a.pieces, first, threadIdx.x, t, c);
-    const u32 col = c * VEC;
-    const int n = (int)min((u32)VEC, a.H - col);
-    const int64_t at = t * a.id_stride;
-    const int64_t id = a.ids_i64 ? *gptr(static_cast<const int64_t *>(a.ids) + at)
-                                 : (int64_t)*gptr(static_cast<const int32_t *>(a.ids) + at);
-    const uint64_t key = (uint64_t)id - (uint64_t)a.first;
-    Piece<T, VEC> w;
-    w.clear();
-    if (key < a.V) w.load(static_cast<const T *>(a.in) + (int64_t)key * a.ld_in + col, n);
-    float v[VEC];
+  for (int64_t first = (int64_t)blockIdx.x * (256 * N); first < a.pieces.total; first += (int64_t)gridDim.x * (256 * N)) {
+    int64_t t[N];
+    u32 col[N];
+    uint64_t key[N];
+    Piece<T, VEC> w[N];
+    const int have = (int)min((int64_t)N, (a.pieces.total - first - threadIdx.x + 255) / 256);
 #pragma unroll
-    for (int i = 0; i < VEC; i++) v[i] = key < a.V ? w.get(i) * a.scale : 0.0f;
-    Piece<U, VEC> y;
-    y.set(v);
-    y.store(static_cast<U *>(a.out) + t * a.ld_out + col, n);
+    for (int u = 0; u < N; u++) {
+      if (u >= have) break;
+      u32 c;
+      place_of(a.pieces, first, u * 256 + threadIdx.x, t[u], c);
+      col[u] = piece_col<VEC>(c, a.H);
+      const int64_t at = t[u] * a.id_stride;
+      const int64_t id = a.ids_i64 ? *gptr(static_cast<const int64_t *>(a.ids) + at)
+                                   : (int64_t)*gptr(static_cast<const int32_t *>(a.ids) + at);
+      key[u] = (uint64_t)id - (uint64_t)a.first;
+    }
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      w[u].clear();
+      if (u < have && key[u] < a.V)
+        w[u].load(static_cast<const T *>(a.in) + (int64_t)key[u] * a.ld_in + col[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      if (u >= have) break;
+      float v[VEC];
+#pragma unroll
+      for (int i = 0; i < VEC; i++) v[i] = key[u] < a.V ? w[u].get(i) * a.scale : 0.0f;
+      Piece<U, VEC> y;
+      y.set(v);
+      y.store(static_cast<U *>(a.out) + t[u] * a.ld_out + col[u]);
+    }
   }
 }
 
-// scale sum (+ what is there) into row `word`.
+// scale sum (+ what is there) into row `word`, at `piece`; elements that the
+// piece before has too are added to by that one alone.
 template <class U, int VEC>
-__device__ __forceinline__ void embed_write(const EmbedArgs &a, u32 word, u32 col, int n, const float *sum) {
+__device__ __forceinline__ void embed_write(const EmbedArgs &a, u32 word, u32 piece, const float *sum) {
+  const u32 col = piece_col<VEC>(piece, a.H);
   U *out = static_cast<U *>(a.out) + (int64_t)word * a.ld_out + col;
   float v[VEC];
   Piece<U, VEC> p;
   if (a.accumulate) {
-    p.load(out, n);
+    p.load(out);
 #pragma unroll
     for (int i = 0; i < VEC; i++) v[i] = fmaf(a.scale, sum[i], p.get(i));
+    p.set(v);
+    if (col == piece * VEC) p.store(out);
+    else p.store(out, (int)(piece * VEC - col), VEC);
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; i++) v[i] = a.scale * sum[i];
+    p.set(v);
+    p.store(out);
   }
-  p.set(v);
-  p.store(out, n);
 }
 
+// The parts of a chunk, at a piece's own place.
 template <int VEC>
-__device__ __forceinline__ float *embed_part(const EmbedArgs &a, u32 chunk, u32 which, u32 col) {
-  return a.part + ((int64_t)chunk * 2 + which) * a.strips * (64 * VEC) + col;
+__device__ __forceinline__ float *embed_part(const EmbedArgs &a, u32 chunk, u32 which, u32 piece) {
+  return a.part + ((int64_t)chunk * 2 + which) * a.strips * (64 * VEC) + piece * VEC;
 }
 
-// Zeros in the rows of words without tokens, 64 words a workgroup.
-template <class U>
+// Number of the ascending keys that are below v, by a whole wavefront: 64 probes
+// at a time.
+__device__ __forceinline__ u32 keys_below(const u32 *keys, u32 n, u32 v) {
+  u32 lo = 0, hi = n;  // it is in [lo, hi]
+  while (lo < hi) {
+    const u32 step = (hi - lo + 63) / 64, at = lo + (threadIdx.x & 63) * step;
+    const u32 c = __popcll(__ballot(at < hi && *gptr(keys + at) < v));
+    hi = min(hi, lo + c * step);
+    if (c) lo += (c - 1) * step + 1;
+  }
+  return lo;
+}
+
+// Zeros in the rows of words without tokens, a.zero_rows words a workgroup.
+template <class U, int VEC>
 __device__ __forceinline__ void embed_zeros(const EmbedArgs &a, u32 block) {
-  constexpr int VEC = 16 / (int)sizeof(U);
-  const u32 lane = threadIdx.x & 63, v0 = block * 64, v = v0 + lane;
-  const u32 upto = keys_up_to(gptr(a.keys), a.T, v);
-  const uint64_t named = __ballot(v >= a.V || (upto > 0 && *gptr(a.keys + upto - 1) == v));
-  Piece<U, VEC> zero;
+  constexpr int Z = VEC == 1 ? 1 : 16 / (int)sizeof(U);
+  const u32 lane = threadIdx.x & 63, v0 = block * a.zero_rows, rows = min(a.zero_rows, a.V - v0);
+  // lane i looks for word v0 + i among the keys of this workgroup's words
+  const u32 from = keys_below(a.keys, a.T, v0), to = keys_below(a.keys, a.T, v0 + rows);
+  const u32 v = v0 + min(lane, rows - 1), upto = from + keys_up_to(gptr(a.keys + from), to - from, v);
+  const uint64_t named = __ballot(upto > from && *gptr(a.keys + upto - 1) == v);
+  Piece<U, Z> zero;
   zero.clear();
-  for (u32 i = threadIdx.x >> 6; i < 64; i += 4) {
+  for (u32 i = threadIdx.x >> 6; i < rows; i += 4) {
     if (named >> i & 1) continue;
     U *row = static_cast<U *>(a.out) + (int64_t)(v0 + i) * a.ld_out;
-    for (u32 col = lane * VEC; col < a.H; col += 64 * VEC) zero.store(row + col, (int)min((u32)VEC, a.H - col));
+#pragma unroll 4
+    for (u32 c = lane; c * Z < a.H; c += 64) zero.store(row + piece_col<Z>(c, a.H));
   }
 }
 
 // Part 0 of a chunk belongs to a word that began in an earlier chunk, part 1 to
 // one that begins here and goes on in the next.
-template <class T, class U>
+template <class T, class U, int VEC>
 __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
-  constexpr int VEC = kEmbedVec<T, U>;
   if (blockIdx.x >= a.sum_blocks) {
-    embed_zeros<U>(a, blockIdx.x - a.sum_blocks);
+    embed_zeros<U, VEC>(a, blockIdx.x - a.sum_blocks);
     return;
   }
   const u32 lane = threadIdx.x & 63;
@@ -117,73 +149,105 @@ __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   const u32 chunk = job / a.strips, strip = job - chunk * a.strips;
   if (chunk >= a.chunks) return;
   const u32 lo = chunk * a.rows, count = min(a.rows, a.T - lo);
-  const u32 col = (strip * 64 + lane) * VEC;
-  const bool in = col < a.H;
-  const int n = in ? (int)min((u32)VEC, a.H - col) : 1;
-  // lane i holds token i of the chunk, and its word
+  // lane i holds token i of the chunk, and its word; those outside are sorted last
   const u32 mine = min(lane, count - 1);
   const u32 my_key = *gptr(a.keys + lo + mine), my_token = *gptr(a.order + lo + mine);
+  const u32 valid = __popcll(__ballot(lane < count && my_key < a.V));
+  if (valid == 0) return;
   const u32 before = lo ? *gptr(a.keys + lo - 1) : ~0u;
   const u32 after = lo + count < a.T ? *gptr(a.keys + lo + count) : ~0u;
+  const u32 piece = strip * 64 + lane;
+  const bool in = piece * VEC < a.H;
+  const T *dy = static_cast<const T *>(a.in) + piece_col<VEC>(in ? piece : 0, a.H);
   float sum[VEC] = {};
-  bool began = false;  // the running word began in this chunk
   u32 word = __builtin_amdgcn_readlane(my_key, 0);
-  began = word != before;
+  bool began = word != before;  // the running word began in this chunk
   auto leave = [&](bool goes_on) {
     if (in) {
       if (!began || goes_on) {
-        float *to = embed_part<VEC>(a, chunk, began ? 1 : 0, col);
-#pragma unroll
-        for (int i = 0; i < VEC; i += 4)
-          *gptr(reinterpret_cast<f32x4_t *>(to + i)) = f32x4_t{sum[i], sum[i + 1], sum[i + 2], sum[i + 3]};
+        float *to = embed_part<VEC>(a, chunk, began ? 1 : 0, piece);
+        Piece<float, VEC> p;
+        p.set(sum);
+        p.store(to);
       } else {
-        embed_write<U, VEC>(a, word, col, n, sum);
+        embed_write<U, VEC>(a, word, piece, sum);
       }
     }
 #pragma unroll
     for (int i = 0; i < VEC; i++) sum[i] = 0.0f;
   };
-  for (u32 i = 0; i < count; i++) {
-    const u32 key = __builtin_amdgcn_readlane(my_key, i), token = __builtin_amdgcn_readlane(my_token, i);
-    if (key != word) {
-      if (word < a.V) leave(false);
-      word = key;
-      began = true;
-    }
-    if (word >= a.V) break;  // sorted last
-    if (in) {
-      Piece<T, VEC> d;
-      d.load(static_cast<const T *>(a.in) + (int64_t)token * a.ld_in + col, n);
+  // eight rows in flight; past the last one it is read again and not added
+  constexpr int N = 8;
+  for (u32 i0 = 0; i0 < valid; i0 += N) {
+    Piece<T, VEC> d[N];
 #pragma unroll
-      for (int j = 0; j < VEC; j++) sum[j] += d.get(j);
+    for (int u = 0; u < N; u++) {
+      const u32 token = __builtin_amdgcn_readlane(my_token, min(i0 + u, valid - 1));
+      d[u].load(dy + (int64_t)token * a.ld_in);
+    }
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      if (i0 + u >= valid) break;
+      const u32 key = __builtin_amdgcn_readlane(my_key, i0 + u);
+      if (key != word) {
+        leave(false);
+        word = key;
+        began = true;
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; j++) sum[j] += d[u].get(j);
     }
   }
-  if (word < a.V) leave(word == after);
+  leave(word == after);
 }
 
 // Joins the parts of the word that begins in chunk blockIdx.x / strips and goes
 // on: part 1 there, then part 0 of the chunks after it as far as the word goes.
-template <class T, class U>
-__global__ __launch_bounds__(64) void k_embed_join(const EmbedArgs a) {
-  constexpr int VEC = kEmbedVec<T, U>;
+// The four wavefronts take every fourth part, eight at a time, and their sums are
+// added in order.
+template <class T, class U, int VEC>
+__global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
+  __shared__ float sm[4][64 * VEC];
   const u32 chunk = blockIdx.x / a.strips, strip = blockIdx.x - chunk * a.strips;
+  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const u32 lo = chunk * a.rows, next = lo + a.rows;
   if (next >= a.T) return;
   const u32 word = *gptr(a.keys + next);
   if (word >= a.V || *gptr(a.keys + next - 1) != word) return;  // nothing goes on
-  if (*gptr(a.keys + lo) == word && lo > 0 && *gptr(a.keys + lo - 1) == word) return;  // it began earlier
-  const u32 col = (strip * 64 + threadIdx.x) * VEC;
-  if (col >= a.H) return;
-  float sum[VEC];
-  const float *p = embed_part<VEC>(a, chunk, 1, col);
-#pragma unroll
-  for (int i = 0; i < VEC; i++) sum[i] = *gptr(p + i);
-  for (u32 c = chunk + 1; c < a.chunks && *gptr(a.keys + c * a.rows) == word; c++) {
-    p = embed_part<VEC>(a, c, 0, col);
-#pragma unroll
-    for (int i = 0; i < VEC; i++) sum[i] += *gptr(p + i);
+  if (lo > 0 && *gptr(a.keys + lo) == word && *gptr(a.keys + lo - 1) == word) return;  // it began earlier
+  // chunks that begin with this word: those after `chunk` up to the first that does not
+  u32 parts = 1;
+  for (;;) {
+    const u32 c = chunk + parts + lane;
+    const uint64_t same = __ballot(c < a.chunks && *gptr(a.keys + min(c, a.chunks - 1) * a.rows) == word);
+    const u32 n = same == ~0ull ? 64 : __builtin_ctzll(~same);
+    parts += n;
+    if (n < 64) break;
   }
-  embed_write<U, VEC>(a, word, col, (int)min((u32)VEC, a.H - col), sum);
+  const u32 piece = strip * 64 + lane;
+  const bool in = piece * VEC < a.H;
+  constexpr int N = VEC == 8 ? 4 : 8;
+  float sum[VEC] = {};
+  for (u32 i0 = wave; i0 < parts; i0 += 4 * N) {
+    Piece<float, VEC> p[N];
+#pragma unroll
+    for (int u = 0; u < N; u++) {
+      const u32 i = min(i0 + 4 * u, parts - 1);
+      p[u].load(embed_part<VEC>(a, chunk + i, i == 0 ? 1 : 0, in ? piece : 0));
+    }
+#pragma unroll
+    for (int u = 0; u < N; u++)
+      if (i0 + 4 * u < parts)
+#pragma unroll
+        for (int j = 0; j < VEC; j++) sum[j] += p[u].get(j);
+  }
+#pragma unroll
+  for (int j = 0; j < VEC; j++) sm[wave][j * 64 + lane] = sum[j];
+  __syncthreads();
+  if (wave != 0 || !in) return;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) sum[j] = ((sum[j] + sm[1][j * 64 + lane]) + sm[2][j * 64 + lane]) + sm[3][j * 64 + lane];
+  embed_write<U, VEC>(a, word, piece, sum);
 }
 
 }  // namespace mxt

@@ -9,6 +9,8 @@
 // read or written once and its k sorted rows, contiguous pieces of them, once
 // each, so that nothing moves twice and no sum needs an order of its own.
 #pragma once
+#include <type_traits>
+
 #include "tr_sort.hpp"
 
 namespace mxt {
@@ -19,111 +21,148 @@ struct RouteArgs {
   void *out;             // xs, y, dys
   int64_t ld_in, ld_other, ld_out;
   const int32_t *rank;
-  const void *weights;   // NULL: ones
+  const void *weights;
   float *dw;
   Pieces pieces;         // of the T rows
   int64_t T;
   u32 k, H, R;
-  int32_t w_f32;
 };
 
+// Weight of pair `pair`; W void: none, ones.
+template <class W>
 __device__ __forceinline__ float route_weight(const RouteArgs &a, int64_t pair) {
-  if (!a.weights) return 1.0f;
-  return a.w_f32 ? *gptr(static_cast<const float *>(a.weights) + pair)
-                 : to_f32(*gptr(static_cast<const uint16_t *>(a.weights) + pair));
+  if constexpr (std::is_void_v<W>) return 1.0f;
+  else return to_f32(*gptr(static_cast<const W *>(a.weights) + pair));
 }
 
 // The row of pair `pair`: at least R where it is dropped.
 __device__ __forceinline__ u32 route_row(const RouteArgs &a, int64_t pair) { return (u32)*gptr(a.rank + pair); }
 
-template <class T>
+template <class T, int VEC>
 __global__ __launch_bounds__(256) void k_dispatch(const RouteArgs a) {
-  constexpr int VEC = 16 / (int)sizeof(T);
   for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= a.pieces.total) continue;
     int64_t t;
     u32 c;
     place_of(a.pieces, first, threadIdx.x, t, c);
-    const u32 col = c * VEC;
-    const int n = (int)min((u32)VEC, a.H - col);
+    const u32 col = piece_col<VEC>(c, a.H);
     Piece<T, VEC> v;
-    v.load(static_cast<const T *>(a.in) + t * a.ld_in + col, n);
+    v.load(static_cast<const T *>(a.in) + t * a.ld_in + col);
     for (u32 j = 0; j < a.k; j++) {
       const u32 r = route_row(a, t * a.k + j);
-      if (r < a.R) v.store(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col, n);
+      if (r < a.R) v.store(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col);
     }
   }
 }
 
-template <class T>
+template <class T, class W, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_combine(const RouteArgs a) {
-  constexpr int VEC = 16 / (int)sizeof(T);
+  constexpr int K = 4;
   for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= a.pieces.total) continue;
     int64_t t;
     u32 c;
     place_of(a.pieces, first, threadIdx.x, t, c);
-    const u32 col = c * VEC;
-    const int n = (int)min((u32)VEC, a.H - col);
+    const u32 col = piece_col<VEC>(c, a.H);
     float acc[VEC] = {};
-    for (u32 j = 0; j < a.k; j++) {
-      const int64_t pair = t * a.k + j;
-      const u32 r = route_row(a, pair);
-      if (r >= a.R) continue;
-      const float w = route_weight(a, pair);
-      Piece<T, VEC> v;
-      v.load(static_cast<const T *>(a.in) + (int64_t)r * a.ld_in + col, n);
+    for (u32 j0 = 0; j0 < a.k; j0 += K) {
+      u32 r[K];
+      float w[K];
+      Piece<T, VEC> v[K];
 #pragma unroll
-      for (int i = 0; i < VEC; i++) acc[i] = fmaf(w, v.get(i), acc[i]);
+      for (int j = 0; j < K; j++) {
+        const int64_t pair = t * a.k + min(j0 + j, a.k - 1);
+        const u32 row = route_row(a, pair);
+        r[j] = j0 + j < a.k ? row : ~0u;
+        w[j] = route_weight<W>(a, pair);
+      }
+#pragma unroll
+      for (int j = 0; j < K; j++) {
+        v[j].clear();
+        if (r[j] < a.R) v[j].template load<NT>(static_cast<const T *>(a.in) + (int64_t)r[j] * a.ld_in + col);
+      }
+#pragma unroll
+      for (int j = 0; j < K; j++)
+        if (r[j] < a.R)
+#pragma unroll
+          for (int i = 0; i < VEC; i++) acc[i] = fmaf(w[j], v[j].get(i), acc[i]);
     }
     Piece<T, VEC> y;
     if (a.other) {
-      y.load(static_cast<const T *>(a.other) + t * a.ld_other + col, n);
+      y.template load<NT>(static_cast<const T *>(a.other) + t * a.ld_other + col);
 #pragma unroll
       for (int i = 0; i < VEC; i++) acc[i] += y.get(i);
     }
     y.set(acc);
-    y.store(static_cast<T *>(a.out) + t * a.ld_out + col, n);
+    y.store(static_cast<T *>(a.out) + t * a.ld_out + col);
   }
 }
 
-// Combine's gradients: a wavefront takes a token, its lanes the pieces of the
-// row, and up to 8 choices at a time.
-template <class T>
-__global__ __launch_bounds__(256) void k_combine_bwd(const RouteArgs a) {
-  constexpr int VEC = 16 / (int)sizeof(T), K = 8;
-  const u32 lane = threadIdx.x & 63, C = a.pieces.per.d;
-  for (int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); t < a.T; t += (int64_t)gridDim.x * 4) {
+// Combine's gradients: a workgroup takes a token, its lanes the pieces of the
+// row, and up to 8 choices at a time.  Lane j loads choice j's rank and weight, which
+// are then uniform values: a dropped pair is a branch.
+template <class T, class W, int VEC>
+__global__ __launch_bounds__(1024) void k_combine_bwd(const RouteArgs a) {
+  constexpr int K = 8;
+  __shared__ float sm[16][K];
+  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, C = a.pieces.per.d;
+  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
     for (u32 j0 = 0; j0 < a.k; j0 += K) {
-      float dot[K] = {};
-      for (u32 c = lane; c < C; c += 64) {
-        const u32 col = c * VEC;
-        const int n = (int)min((u32)VEC, a.H - col);
-        Piece<T, VEC> d;
-        d.load(static_cast<const T *>(a.other) + t * a.ld_other + col, n);
+      u32 r[K];
+      float w[K], dot[K] = {};
+      {
+        const int64_t pair = t * a.k + min(j0 + lane, a.k - 1);
+        const u32 row = route_row(a, pair);
+        const float weight = route_weight<W>(a, pair);
 #pragma unroll
         for (int j = 0; j < K; j++) {
-          const int64_t pair = t * a.k + j0 + j;
-          const u32 r = j0 + j < a.k ? route_row(a, pair) : ~0u;
-          if (r >= a.R) continue;
-          const float w = route_weight(a, pair);
-          Piece<T, VEC> v;
-          v.load(static_cast<const T *>(a.in) + (int64_t)r * a.ld_in + col, n);
+          r[j] = j0 + j < a.k ? __builtin_amdgcn_readlane(row, j) : ~0u;
+          w[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
+        }
+      }
+      for (u32 c = threadIdx.x; c < C; c += blockDim.x) {
+        const u32 col = piece_col<VEC>(c, a.H);
+        Piece<T, VEC> d, v[K];
+        d.load(static_cast<const T *>(a.other) + t * a.ld_other + col);
+#pragma unroll
+        for (int j = 0; j < K; j++)
+          if (r[j] < a.R) v[j].load(static_cast<const T *>(a.in) + (int64_t)r[j] * a.ld_in + col);
+        const int shared = (int)(c * VEC - col);  // elements that the piece before counts
+#pragma unroll
+        for (int j = 0; j < K; j++) {
+          if (r[j] >= a.R) continue;
           float o[VEC];
 #pragma unroll
-          for (int i = 0; i < VEC; i++) {
-            dot[j] = fmaf(d.get(i), v.get(i), dot[j]);
-            o[i] = w * d.get(i);
+          for (int i = 0; i < VEC; i++) o[i] = w[j] * d.get(i);
+          Piece<T, VEC> q;
+          q.set(o);
+          q.store(static_cast<T *>(a.out) + (int64_t)r[j] * a.ld_out + col);
+          if (a.H % VEC == 0) {
+#pragma unroll
+            for (int i = 0; i < VEC; i++) dot[j] = fmaf(d.get(i), v[j].get(i), dot[j]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < VEC; i++)
+              dot[j] = i >= shared ? fmaf(d.get(i), v[j].get(i), dot[j]) : dot[j];
           }
-          v.set(o);
-          v.store(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col, n);
         }
       }
 #pragma unroll
       for (int j = 0; j < K; j++) {
+        if (j0 + j >= a.k) break;
 #pragma unroll
         for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, 64);
-        if (lane == 0 && j0 + j < a.k) *gptr(a.dw + t * a.k + j0 + j) = dot[j];
+        if (waves == 1 && lane == 0) *gptr(a.dw + t * a.k + j0 + j) = dot[j];
+        if (waves > 1 && lane == 0) sm[wave][j] = dot[j];
+      }
+      if (waves > 1) {
+        __syncthreads();
+        if (threadIdx.x < K && j0 + threadIdx.x < a.k) {
+          float sum = 0.0f;
+          for (u32 i = 0; i < waves; i++) sum += sm[i][threadIdx.x];
+          *gptr(a.dw + t * a.k + j0 + threadIdx.x) = sum;
+        }
+        __syncthreads();
       }
     }
   }

@@ -43,17 +43,34 @@ struct SortArgs {
   int32_t is_first, is_last;
 };
 
-__device__ __forceinline__ u32 sort_key(const SortArgs &a, u32 item) {
-  int64_t at = item;
-  if (!a.adjacent) {
-    const u32 t = a.k.div(item);
-    at = (int64_t)t * a.ld + (item - t * a.k.d);
-  }
-  const int64_t id = a.ids_i64 ? *gptr(static_cast<const int64_t *>(a.ids) + at)
-                               : (int64_t)*gptr(static_cast<const int32_t *>(a.ids) + at);
-  // (first + n_keys fits 64 bits, so a difference that wraps is not below n_keys)
+// Where item p's id is.
+__device__ __forceinline__ int64_t sort_at(const SortArgs &a, u32 p) {
+  if (a.adjacent) return p;
+  const u32 t = a.k.div(p);
+  return (int64_t)t * a.ld + (p - t * a.k.d);
+}
+
+// (first + n_keys fits 64 bits, so a difference that wraps is not below n_keys)
+__device__ __forceinline__ u32 sort_key(const SortArgs &a, int64_t id) {
   const uint64_t key = (uint64_t)id - (uint64_t)a.first;
   return key < a.n_keys ? (u32)key : a.n_keys;
+}
+
+// Keys of the items p[i] of this thread (~0u: none), all loads in flight together.
+template <int ITEMS>
+__device__ __forceinline__ void sort_keys(const SortArgs &a, const u32 *p, u32 *key) {
+  int64_t id[ITEMS];
+  if (a.ids_i64) {
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++)
+      if (p[i] != ~0u) id[i] = *gptr(static_cast<const int64_t *>(a.ids) + sort_at(a, p[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < ITEMS; i++)
+      if (p[i] != ~0u) id[i] = *gptr(static_cast<const int32_t *>(a.ids) + sort_at(a, p[i]));
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) key[i] = p[i] != ~0u ? sort_key(a, id[i]) : 0;
 }
 
 // LDS of a workgroup of W wavefronts that ranks a tile.

@@ -20,7 +20,9 @@ inline SortPlan sort_plan(int64_t n, int64_t n_keys, bool keep) {
   while (all < 32 && (n_keys >> all) != 0) all++;  // n_keys itself is a key: the dropped items'
   p.passes = (all + kSortBits - 1) / kSortBits;
   p.bits = (all + p.passes - 1) / p.passes;
-  p.small = n <= kSortTile;
+  // One workgroup's pass over 8192 items takes longer than two launches (12 us
+  // against 9), over 4096 less (8); two passes over 8192 about as long as four.
+  p.small = n <= (p.passes == 1 ? kSortTile / 2 : kSortTile);
   int64_t at = 0;
   auto take = [&](int64_t words) {
     const int64_t here = at;

@@ -36,7 +36,7 @@ enum { MXTRAIN_I32 = 0, MXTRAIN_I64 = 1 };
  *   order : int32 [T k], the pair in each row, -1 in rows past the last; may
  *           be NULL
  *   workspace : at least mxtrain_expert_sort_workspace(T k, G) bytes (0 for few
- *           pairs, then it may be NULL), 4-byte aligned
+ *           pairs, then it may be NULL), 16-byte aligned
  * T k < 2^31, G <= 65535; G == 0 drops every pair, T k == 0 leaves zeros in ends.
  */
 int64_t mxtrain_expert_sort_workspace(int64_t pairs, int64_t G);

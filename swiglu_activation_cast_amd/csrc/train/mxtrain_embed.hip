@@ -61,10 +61,10 @@ const void *join_kernel() {
 // leaves less than sixteen wavefronts to a compute unit.
 struct EmbedPlan {
   uint32_t rows, chunks, strips;
-  int64_t part, bytes;
+  int64_t flags, part, bytes;
 };
 
-EmbedPlan embed_plan(const SortPlan &sort, int64_t T, int64_t H, int64_t vec) {
+EmbedPlan embed_plan(const SortPlan &sort, int64_t T, int64_t V, int64_t H, int64_t vec) {
   EmbedPlan p{};
   const int64_t strips = ((H + vec - 1) / vec + 63) / 64;
   int64_t rows = 64;
@@ -72,7 +72,8 @@ EmbedPlan embed_plan(const SortPlan &sort, int64_t T, int64_t H, int64_t vec) {
   p.rows = (uint32_t)rows;
   p.chunks = (uint32_t)((T + rows - 1) / rows);
   p.strips = (uint32_t)strips;
-  p.part = sort.bytes;
+  p.flags = sort.bytes;
+  p.part = p.flags + (V + 15) / 16 * 16;
   p.bytes = p.part + (p.chunks > 1 ? (int64_t)p.chunks * 2 * strips * 64 * vec * 4 : 0);
   return p;
 }
@@ -116,7 +117,7 @@ mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weigh
 
 int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_type, int dw_type) {
   if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0 || T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
-  return embed_plan(sort_plan(T, V, true), T, H, embed_vec(dy_type, dw_type, H)).bytes;
+  return embed_plan(sort_plan(T, V, true), T, V, H, embed_vec(dy_type, dw_type, H)).bytes;
 }
 
 mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type, const void *ids, int64_t id_stride,
@@ -129,16 +130,15 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   if (accumulate != 0 && accumulate != 1) return MXTRAIN_ERR_VALUE;
   if (V == 0 || H == 0 || (T == 0 && accumulate)) return MXTRAIN_OK;
   const SortPlan sp = sort_plan(T, V, true);
-  const EmbedPlan ep = embed_plan(sp, T, H, embed_vec(dy_type, dw_type, H));
+  const EmbedPlan ep = embed_plan(sp, T, V, H, embed_vec(dy_type, dw_type, H));
   if (T > 0 && !workspace) return MXTRAIN_ERR_NULL;
   if (T > 0 && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
   if (T > 0 && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
-  // words whose rows a workgroup clears: few enough for 2048 workgroups
-  int64_t zero_rows = 4;
-  while (zero_rows < 64 && V > zero_rows * 4096) zero_rows *= 2;
-  const int64_t sum_blocks = ((int64_t)ep.chunks * ep.strips + 3) / 4, zero_blocks = accumulate ? 0 : (V + zero_rows - 1) / zero_rows;
-  if (sum_blocks + zero_blocks > INT32_MAX / 256 || (int64_t)ep.chunks * ep.strips > INT32_MAX / 256)
-    return MXTRAIN_ERR_OVERFLOW;
+  const int64_t vec = embed_vec(dy_type, dw_type, H), zero_vec = vec == 1 ? 1 : 16 / size_of(dw_type);
+  const int64_t zero_per = (H + zero_vec - 1) / zero_vec, zeros = accumulate ? 0 : V * zero_per;
+  const int64_t jobs = (int64_t)ep.chunks * ep.strips, sum_blocks = (jobs + 3) / 4;
+  if (jobs > INT32_MAX / 256) return MXTRAIN_ERR_OVERFLOW;
+  const int64_t zero_blocks = std::min<int64_t>((zeros + 255) / 256, INT32_MAX / 512);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   EmbedArgs a{};
   a.in = dy;
@@ -156,7 +156,8 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   a.chunks = ep.chunks;
   a.strips = ep.strips;
   a.sum_blocks = (u32)sum_blocks;
-  a.zero_rows = (u32)zero_rows;
+  a.zeros = {zeros, divider((uint32_t)zero_per)};
+  a.flags = T > 0 ? ws + ep.flags : nullptr;
   a.accumulate = accumulate;
   if (T > 0) {
     SortArgs s{};
@@ -167,15 +168,15 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
     s.ids_i64 = id_type == MXTRAIN_I64;
     s.n = (u32)T;
     s.n_keys = (u32)V;
+    s.flags = accumulate ? nullptr : ws + ep.flags;
     s.order = reinterpret_cast<int32_t *>(ws + sp.order);
     s.key_out = reinterpret_cast<u32 *>(ws + sp.keys);
     if ((st = sort_run(sp, s, ws, stream)) != MXTRAIN_OK) return st;
   }
   const bool f = dy_type == MXTRAIN_F32, g = dw_type == MXTRAIN_F32;
-  const int64_t vec = embed_vec(dy_type, dw_type, H);
   st = launch(EMBED_PICK(sum_kernel, vec, f, g), sum_blocks + zero_blocks, 256, a, stream);
   if (st != MXTRAIN_OK || ep.chunks <= 1) return st;
-  return launch(EMBED_PICK(join_kernel, vec, f, g), (int64_t)ep.chunks * ep.strips, 256, a, stream);
+  return launch(EMBED_PICK(join_kernel, vec, f, g), jobs, 256, a, stream);
 }
 
 }  // extern "C"

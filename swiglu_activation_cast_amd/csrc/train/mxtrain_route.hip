@@ -35,7 +35,7 @@ mxtrain_status sort_check(const void *ids, int64_t ld, int id_type, int64_t T, i
   if ((n > 0 && (!ids || !rank)) || (G > 0 && !ends) || (need > 0 && !ws)) return MXTRAIN_ERR_NULL;
   if (n > 0 && ld < k) return MXTRAIN_ERR_STRIDE;
   if (!aligned(ids, id_type == MXTRAIN_I64 ? 8 : 4) || !aligned(rank, 4) || !aligned(ends, 4) || !aligned(order, 4) ||
-      (need > 0 && !aligned(ws, 4)))
+      (need > 0 && !aligned(ws, 16)))
     return MXTRAIN_ERR_ALIGN;
   if (!extent_ok(T, k, ld)) return MXTRAIN_ERR_OVERFLOW;
   return ws_bytes < need ? MXTRAIN_ERR_WORKSPACE : MXTRAIN_OK;

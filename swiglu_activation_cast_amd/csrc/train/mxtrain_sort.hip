@@ -18,7 +18,12 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
     const u32 p = (w * each + i) * 64 + lane;
     item[i] = (u32)i < each && p < a.n ? p : ~0u;
   }
+  sort_clear_flags(a);
   sort_keys<kSortItems>(a, item, key);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortItems; i++)
+    if (item[i] != ~0u) sort_set_flag(a, key[i]);
   for (u32 pass = 0; pass < a.passes; pass++) {
     if (pass) {
 #pragma unroll
@@ -39,14 +44,14 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
     for (int i = 0; i < kSortItems; i++) {
       if (item[i] == ~0u) continue;
       const u32 to = sm.base[digit[i]] + place[i];
-      if (pass + 1 < a.passes || (a.passes > 1 && a.ends)) {
-        keys[to] = key[i];
-        items[to] = (uint16_t)item[i];
-      }
-      if (pass + 1 == a.passes) sort_result(a, item[i], key[i], to);
+      keys[to] = key[i];
+      items[to] = (uint16_t)item[i];
+      if (pass + 1 == a.passes) sort_rank(a, item[i], key[i], to);
     }
     __syncthreads();
   }
+  // from LDS in order: scattered stores take the compute unit a cycle each
+  for (u32 p = threadIdx.x; p < a.n; p += kSortThreads) sort_place(a, items[p], keys[p], p);
   if (!a.ends) return;
   if (a.passes == 1) {
     if (threadIdx.x < a.n_keys) *gptr(a.ends + threadIdx.x) = (int32_t)(base + total);
@@ -77,6 +82,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
   __shared__ u32 count[1 << kSortBits];
   const u32 bins = 1u << a.bits, lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
   if (threadIdx.x < bins) count[threadIdx.x] = 0;
+  if (a.is_first) sort_clear_flags(a);
   __syncthreads();
   for (u32 p = lo + threadIdx.x; p < hi; p += kSortThreads) {
     u32 key, item;
@@ -90,7 +96,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
 // Moves workgroup b's range to its places.
 __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   __shared__ SortShared<16> sm;
-  __shared__ u32 sums[2][kSortThreads];
+  __shared__ u32 sums[2][4 * kSortThreads];  // [groups][bins]
   const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, bins = 1u << a.bits, mask = bins - 1;
   const u32 lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
   u32 key[kSortItems], item[kSortItems], digit[kSortItems], place[kSortItems];
@@ -106,23 +112,36 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   };
   fetch(lo);  // in flight while the counts are added up
   {
-    // thread (part, d): digit d in every (1024 / bins)-th workgroup's counts
-    const u32 d = threadIdx.x & mask, parts = kSortThreads >> a.bits;
-    u32 all = 0, before = 0;
+    // A thread reads four digits' counts of every `rows`-th workgroup.  Lanes of a
+    // wavefront with the same digits are added up there, then the wavefronts, or
+    // groups of them that share a row, over LDS.
+    const u32 quads = bins / 4, row = threadIdx.x / quads, rows = kSortThreads / quads;
+    const u32 d = threadIdx.x % quads * 4, groups = min(16u, rows), group = min(row, w);
+    u32x4_t all4 = {}, before4 = {};
 #pragma unroll 8
-    for (u32 b = threadIdx.x >> a.bits; b < a.blocks; b += parts) {
-      const u32 c = *gptr(a.counts + (b << a.bits) + d);
-      all += c;
-      before += b < blockIdx.x ? c : 0;
+    for (u32 b = row; b < a.blocks; b += rows) {
+      const u32x4_t c = *gptr(reinterpret_cast<const u32x4_t *>(a.counts + (b << a.bits) + d));
+      all4 += c;
+      if (b < blockIdx.x) before4 += c;
     }
-    sums[0][threadIdx.x] = all;
-    sums[1][threadIdx.x] = before;
+    for (u32 o = 32; o >= quads; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        all4[i] += __shfl_xor(all4[i], o, 64);
+        before4[i] += __shfl_xor(before4[i], o, 64);
+      }
+    if (quads >= 64 || lane < quads)
+#pragma unroll
+      for (int i = 0; i < 4; i++) {
+        sums[0][group * bins + d + i] = all4[i];
+        sums[1][group * bins + d + i] = before4[i];
+      }
     __syncthreads();
-    all = before = 0;
+    u32 all = 0, before = 0;
     if (threadIdx.x < bins)
-      for (u32 i = 0; i < parts; i++) {
-        all += sums[0][(i << a.bits) + threadIdx.x];
-        before += sums[1][(i << a.bits) + threadIdx.x];
+      for (u32 i = 0; i < groups; i++) {
+        all += sums[0][i * bins + threadIdx.x];
+        before += sums[1][i * bins + threadIdx.x];
       }
     const u32 base = block_scan<16>(all, sm.wave);
     if (threadIdx.x < bins) sm.base[threadIdx.x] = base + before;
@@ -131,8 +150,11 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   for (u32 tile = lo; tile < hi; tile += kSortTile) {
     if (tile > lo) fetch(tile);
 #pragma unroll
-    for (int i = 0; i < kSortItems; i++)
-      if (digit[i] != ~0u) digit[i] = key[i] >> a.shift & mask;
+    for (int i = 0; i < kSortItems; i++) {
+      if (digit[i] == ~0u) continue;
+      if (a.is_first) sort_set_flag(a, key[i]);
+      digit[i] = key[i] >> a.shift & mask;
+    }
     const u32 total = rank_tile<16, kSortItems>(sm, digit, place, a.bits);
     // rank_tile's barriers also lie between sm.base's last write and here
 #pragma unroll
@@ -140,7 +162,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
       if (digit[i] == ~0u) continue;
       const u32 to = sm.base[digit[i]] + place[i];
       if (a.is_last) {
-        sort_result(a, item[i], key[i], to);
+        sort_place(a, item[i], key[i], to);
+        sort_rank(a, item[i], key[i], to);
       } else {
         *gptr(a.key_out + to) = key[i];
         *gptr(a.item_out + to) = item[i];

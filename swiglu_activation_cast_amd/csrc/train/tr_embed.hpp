@@ -8,8 +8,9 @@
 // are cut into chunks of at most 64; a wavefront takes a chunk and 64 pieces of the
 // columns, keeps the running sum in registers and writes it where the word
 // changes.  A word whose rows lie in several chunks leaves an fp32 part in each,
-// and a second kernel joins them in order.  Words without tokens get their zeros
-// from further workgroups of the first launch.
+// and a second kernel joins them in order.  Words without tokens (the sort
+// flags those that have some) get their zeros from further workgroups of the first
+// launch.
 #pragma once
 #include "tr_sort.hpp"
 
@@ -30,8 +31,9 @@ struct EmbedArgs {
   float *part;              // [chunks][2][strips * 64 * VEC]
   u32 rows;                 // tokens of a chunk
   u32 chunks, strips;       // and of the columns, 64 pieces each
+  const uint8_t *flags;     // [V], 1: the word has tokens; NULL: none has
+  Pieces zeros;             // of dW's rows, 16 bytes each
   u32 sum_blocks;           // workgroups that sum; those after them write zeros
-  u32 zero_rows;            // to the rows of so many words each, at most 64
   int32_t accumulate;
 };
 
@@ -104,35 +106,23 @@ __device__ __forceinline__ float *embed_part(const EmbedArgs &a, u32 chunk, u32 
   return a.part + ((int64_t)chunk * 2 + which) * a.strips * (64 * VEC) + piece * VEC;
 }
 
-// Number of the ascending keys that are below v, by a whole wavefront: 64 probes
-// at a time.
-__device__ __forceinline__ u32 keys_below(const u32 *keys, u32 n, u32 v) {
-  u32 lo = 0, hi = n;  // it is in [lo, hi]
-  while (lo < hi) {
-    const u32 step = (hi - lo + 63) / 64, at = lo + (threadIdx.x & 63) * step;
-    const u32 c = __popcll(__ballot(at < hi && *gptr(keys + at) < v));
-    hi = min(hi, lo + c * step);
-    if (c) lo += (c - 1) * step + 1;
-  }
-  return lo;
-}
-
-// Zeros in the rows of words without tokens, a.zero_rows words a workgroup.
+// Zeros in the rows of words without tokens.  One store a thread, workgroup after
+// workgroup: 16384 tokens on 65536 words x 5120 fp32 take 267 us so, 325 where
+// wavefronts walk rows of their own (a front of single stores fills 1.3 GB at
+// 6.5-6.8 TB/s, such rows at 5.3) and 374 with stores through the caches.
 template <class U, int VEC>
-__device__ __forceinline__ void embed_zeros(const EmbedArgs &a, u32 block) {
+__device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
   constexpr int Z = VEC == 1 ? 1 : 16 / (int)sizeof(U);
-  const u32 lane = threadIdx.x & 63, v0 = block * a.zero_rows, rows = min(a.zero_rows, a.V - v0);
-  // lane i looks for word v0 + i among the keys of this workgroup's words
-  const u32 from = keys_below(a.keys, a.T, v0), to = keys_below(a.keys, a.T, v0 + rows);
-  const u32 v = v0 + min(lane, rows - 1), upto = from + keys_up_to(gptr(a.keys + from), to - from, v);
-  const uint64_t named = __ballot(upto > from && *gptr(a.keys + upto - 1) == v);
   Piece<U, Z> zero;
   zero.clear();
-  for (u32 i = threadIdx.x >> 6; i < rows; i += 4) {
-    if (named >> i & 1) continue;
-    U *row = static_cast<U *>(a.out) + (int64_t)(v0 + i) * a.ld_out;
-#pragma unroll 4
-    for (u32 c = lane; c * Z < a.H; c += 64) zero.store(row + piece_col<Z>(c, a.H));
+  const int64_t step = (int64_t)(gridDim.x - a.sum_blocks) * 256;
+  for (int64_t first = (int64_t)(blockIdx.x - a.sum_blocks) * 256; first < a.zeros.total; first += step) {
+    if (first + threadIdx.x >= a.zeros.total) continue;
+    int64_t v;
+    u32 c;
+    place_of(a.zeros, first, threadIdx.x, v, c);
+    if (a.flags && *gptr(a.flags + v)) continue;
+    zero.store(static_cast<U *>(a.out) + v * a.ld_out + piece_col<Z>(c, a.H));
   }
 }
 
@@ -141,7 +131,7 @@ __device__ __forceinline__ void embed_zeros(const EmbedArgs &a, u32 block) {
 template <class T, class U, int VEC>
 __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   if (blockIdx.x >= a.sum_blocks) {
-    embed_zeros<U, VEC>(a, blockIdx.x - a.sum_blocks);
+    embed_zeros<U, VEC>(a);
     return;
   }
   const u32 lane = threadIdx.x & 63;

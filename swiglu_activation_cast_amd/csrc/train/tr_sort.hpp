@@ -37,6 +37,7 @@ struct SortArgs {
   const u32 *key_in, *item_in;  // the source of later passes
   u32 *key_out, *item_out;      // the next pass's source; in the last pass the sorted keys, or NULL
   int32_t *order, *rank, *ends;  // written by the last pass, each may be NULL; ends only where one pass does
+  uint8_t *flags;                // [n_keys], 1 where an item has that key; may be NULL
   u32 *counts;                   // [blocks][1 << bits]
   u32 shift, bits, blocks, per;  // this pass's digit; workgroups and items of each (a multiple of 1024)
   u32 passes;                    // one workgroup: passes of `bits` bits each
@@ -116,9 +117,8 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
     uint64_t same = __ballot(have);
     if (same == 0) break;
     for (u32 b = 0; b < bits; b++) {
-      const bool one = digit[i] >> b & 1u;
-      const uint64_t with = __ballot(one);
-      same &= one ? with : ~with;
+      const int one = __builtin_amdgcn_sbfe((int)digit[i], b, 1);  // 0 or -1
+      same &= __ballot(one == 0) ^ (uint64_t)(int64_t)one;
     }
     const u32 lower = __popcll(same & ((1ull << lane) - 1));
     if (have) {
@@ -147,12 +147,26 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
   return total;
 }
 
-// Writes what the last pass leaves: `item` of key `key` goes to `place`.
-__device__ __forceinline__ void sort_result(const SortArgs &a, u32 item, u32 key, u32 place) {
-  const bool kept = key < a.n_keys;
-  if (a.order) *gptr(a.order + place) = kept ? (int32_t)item : -1;
-  if (a.rank) *gptr(a.rank + item) = kept ? (int32_t)place : -1;
+// The flags are cleared by the first kernel (the first part of one workgroup's)
+// and set by the second.
+__device__ __forceinline__ void sort_clear_flags(const SortArgs &a) {
+  if (!a.flags) return;  // 16 bytes at a time: they begin and end on multiples of it
+  for (int64_t i = (int64_t)(blockIdx.x * kSortThreads + threadIdx.x) * 16; i < a.n_keys; i += (int64_t)gridDim.x * kSortThreads * 16)
+    *gptr(reinterpret_cast<u32x4_t *>(a.flags + i)) = u32x4_t{};
+}
+
+__device__ __forceinline__ void sort_set_flag(const SortArgs &a, u32 key) {
+  if (a.flags && key < a.n_keys) *gptr(a.flags + key) = 1;
+}
+
+// Writes what the last pass leaves: the item of key `key` at `place` of the order.
+__device__ __forceinline__ void sort_place(const SortArgs &a, u32 item, u32 key, u32 place) {
+  if (a.order) *gptr(a.order + place) = key < a.n_keys ? (int32_t)item : -1;
   if (a.key_out) *gptr(a.key_out + place) = key;
+}
+
+__device__ __forceinline__ void sort_rank(const SortArgs &a, u32 item, u32 key, u32 place) {
+  if (a.rank) *gptr(a.rank + item) = key < a.n_keys ? (int32_t)place : -1;
 }
 
 // Number of the n ascending keys that are at most `v`.

@@ -19,7 +19,7 @@ inline SortPlan sort_plan(int64_t n, int64_t n_keys, bool keep) {
   uint32_t all = 1;
   while (all < 32 && (n_keys >> all) != 0) all++;  // n_keys itself is a key: the dropped items'
   p.passes = (all + kSortBits - 1) / kSortBits;
-  p.bits = (all + p.passes - 1) / p.passes;
+  p.bits = std::max(2u, (all + p.passes - 1) / p.passes);  // counts are read four digits at a time
   // One workgroup's pass over 8192 items takes longer than two launches (12 us
   // against 9), over 4096 less (8); two passes over 8192 about as long as four.
   p.small = n <= (p.passes == 1 ? kSortTile / 2 : kSortTile);

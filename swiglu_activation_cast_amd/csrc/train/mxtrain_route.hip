@@ -107,9 +107,24 @@ const void *combine_kernel(int wtype, bool nt) {
   return combine_kernel_nt<T, VEC, false>(wtype);
 }
 
+// lanes: of a token, at least its row's pieces where fewer than 64.
+template <class T, class W, int VEC>
+const void *combine_bwd_lanes(int lanes) {
+  return lanes == 16 ? (const void *)&k_combine_bwd<T, W, VEC, 16>
+         : lanes == 32 ? (const void *)&k_combine_bwd<T, W, VEC, 32>
+                       : (const void *)&k_combine_bwd<T, W, VEC, 64>;
+}
+
 template <class T, int VEC>
-const void *combine_bwd_kernel(int wtype) {
-  return wtype == MXTRAIN_F32 ? (const void *)&k_combine_bwd<T, float, VEC> : (const void *)&k_combine_bwd<T, uint16_t, VEC>;
+const void *combine_bwd_kernel(int wtype, int lanes) {
+  return wtype == MXTRAIN_F32 ? combine_bwd_lanes<T, float, VEC>(lanes) : combine_bwd_lanes<T, uint16_t, VEC>(lanes);
+}
+
+template <class T, int VEC>
+const void *sort_dispatch_kernel(int64_t pairs) {
+  return pairs <= 256    ? (const void *)&k_sort_dispatch<T, VEC, 1>
+         : pairs <= 1024 ? (const void *)&k_sort_dispatch<T, VEC, 4>
+                         : (const void *)&k_sort_dispatch<T, VEC, 8>;
 }
 
 // fn<T, VEC>(...) for the rows' type and width.
@@ -170,6 +185,21 @@ mxtrain_status mxtrain_sort_dispatch(const void *x, int64_t ld_x, int dtype, con
   if (st != MXTRAIN_OK) return st;
   st = route_check(x, ld_x, xs, ld_xs, dtype, rank, T, k, H, T * k);
   if (st != MXTRAIN_OK) return st;
+  const SortPlan sp = sort_plan(T * k, G, false);
+  if (T * k > 0 && T * k <= kFewPairs && G <= kFewGroups && H > 0) {
+    SortDispatchArgs g{};
+    g.sort = sort_args(ids, ld_ids, id_type, T, k, first, G, rank, ends, order);
+    g.sort.adjacent = ld_ids == k;
+    g.sort.bits = sp.bits;
+    g.move = route_args(rank, dtype, T, k, H, T * k);
+    g.move.in = x;
+    g.move.ld_in = ld_x;
+    g.move.out = xs;
+    g.move.ld_out = ld_xs;
+    // no more workgroups than run at once: each begins with a sort
+    return launch(ROUTE_PICK(sort_dispatch_kernel, dtype, H, T * k), std::min<int64_t>((g.move.pieces.total + 255) / 256, 2048),
+                  256, g, stream);
+  }
   st = mxtrain_expert_sort(ids, ld_ids, id_type, T, k, first, G, rank, ends, order, workspace, workspace_bytes, stream);
   return st != MXTRAIN_OK ? st : mxtrain_dispatch_fwd(x, ld_x, dtype, rank, T, k, H, T * k, xs, ld_xs, stream);
 }
@@ -233,10 +263,14 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
   // (16384 x 8 rows of 2048 bf16: one wavefront 243 us, four 226.  1021 x 2 rows of
   // 2049 fp32: sixteen 18 us, four 13.)
   const int64_t per = a.pieces.per.d;
+  const int lanes = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  if (lanes < 64)
+    return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes),
+                  std::min((T * lanes + 255) / 256, kMaxGrid), 256, a, stream);
   int64_t steps = std::max<int64_t>(1, (per + 128) / 256);
   while (steps > 1 && T * ((per + 64 * steps - 1) / (64 * steps)) < 1024) steps--;
   const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (per + 64 * steps - 1) / (64 * steps)));
-  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type), std::min(T, kMaxGrid), 64 * waves, a, stream);
+  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes), std::min(T, kMaxGrid), 64 * waves, a, stream);
 }
 
 }  // extern "C"

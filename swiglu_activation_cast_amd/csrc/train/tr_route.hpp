@@ -101,12 +101,18 @@ __global__ __launch_bounds__(256) void k_combine(const RouteArgs a) {
 // Combine's gradients: a workgroup takes a token, its lanes the pieces of the
 // row, and up to 8 choices at a time.  Lane j loads choice j's rank and weight, which
 // are then uniform values: a dropped pair is a branch.
-template <class T, class W, int VEC>
-__global__ __launch_bounds__(1024) void k_combine_bwd(const RouteArgs a) {
+//
+// L < 64: rows of at most L pieces, 256 / L tokens to a workgroup (16384 tokens x
+// 8 rows of 130 bf16: 28 us with a wavefront to a token, 22 with 32 lanes).
+template <class T, class W, int VEC, int L>
+__global__ __launch_bounds__((L == 64 ? 1024 : 256)) void k_combine_bwd(const RouteArgs a) {
   constexpr int K = 8;
-  __shared__ float sm[16][K];
-  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, C = a.pieces.per.d;
-  for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+  __shared__ float sm[L == 64 ? 16 : 1][K];
+  const u32 lane = threadIdx.x % L, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, C = a.pieces.per.d;
+  const u32 step = L == 64 ? blockDim.x : L;  // pieces at a time
+  constexpr int kTokens = 256 / L;
+  const int64_t t0 = L == 64 ? blockIdx.x : (int64_t)blockIdx.x * kTokens + threadIdx.x / L;
+  for (int64_t t = t0; t < a.T; t += (int64_t)gridDim.x * (L == 64 ? 1 : kTokens)) {
     for (u32 j0 = 0; j0 < a.k; j0 += K) {
       u32 r[K];
       float w[K], dot[K] = {};
@@ -116,11 +122,17 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const RouteArgs a) {
         const float weight = route_weight<W>(a, pair);
 #pragma unroll
         for (int j = 0; j < K; j++) {
-          r[j] = j0 + j < a.k ? __builtin_amdgcn_readlane(row, j) : ~0u;
-          w[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
+          if constexpr (L == 64) {
+            r[j] = __builtin_amdgcn_readlane(row, j);
+            w[j] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(weight), j));
+          } else {
+            r[j] = __shfl(row, j, L);
+            w[j] = __shfl(weight, j, L);
+          }
+          if (j0 + j >= a.k) r[j] = ~0u;
         }
       }
-      for (u32 c = threadIdx.x; c < C; c += blockDim.x) {
+      for (u32 c = L == 64 ? threadIdx.x : lane; c < C; c += step) {
         const u32 col = piece_col<VEC>(c, a.H);
         Piece<T, VEC> d, v[K];
         d.load(static_cast<const T *>(a.other) + t * a.ld_other + col);
@@ -151,11 +163,14 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const RouteArgs a) {
       for (int j = 0; j < K; j++) {
         if (j0 + j >= a.k) break;
 #pragma unroll
-        for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, 64);
-        if (waves == 1 && lane == 0) *gptr(a.dw + t * a.k + j0 + j) = dot[j];
-        if (waves > 1 && lane == 0) sm[wave][j] = dot[j];
+        for (int o = L / 2; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o, 64);
+        if (L < 64 || waves == 1) {
+          if (lane == 0) *gptr(a.dw + t * a.k + j0 + j) = dot[j];
+        } else if (lane == 0) {
+          sm[wave][j] = dot[j];
+        }
       }
-      if (waves > 1) {
+      if (L == 64 && waves > 1) {
         __syncthreads();
         if (threadIdx.x < K && j0 + threadIdx.x < a.k) {
           float sum = 0.0f;
@@ -164,6 +179,62 @@ __global__ __launch_bounds__(1024) void k_combine_bwd(const RouteArgs a) {
         }
         __syncthreads();
       }
+    }
+  }
+}
+
+// The sort and the dispatch in one launch, for up to 2048 pairs (ITEMS for each of
+// 256 threads) of up to 255 groups: every workgroup ranks all pairs for itself, the
+// first writes the result down.  8 x 2 pairs, rows of 5120 bf16: 3.5 us (two
+// launches 6.6); 128 x 8 of 2048 5.4 (8.8); 256 x 8 8.0 (10.1).
+constexpr int kFewPairs = 2048, kFewGroups = 255;
+
+struct SortDispatchArgs {
+  SortArgs sort;
+  RouteArgs move;
+};
+
+template <class T, int VEC, int ITEMS>
+__global__ __launch_bounds__(256) void k_sort_dispatch(const SortDispatchArgs g) {
+  const SortArgs &s = g.sort;
+  const RouteArgs &a = g.move;
+  __shared__ SortShared<4> sm;
+  __shared__ uint16_t rank[ITEMS * 256];
+  const u32 lane = threadIdx.x & 63, w = threadIdx.x >> 6, each = (s.n + 255) / 256;
+  u32 item[ITEMS], key[ITEMS], digit[ITEMS], place[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) {
+    const u32 p = (w * each + i) * 64 + lane;
+    item[i] = (u32)i < each && p < s.n ? p : ~0u;
+  }
+  sort_keys<ITEMS>(s, item, key);
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) digit[i] = item[i] != ~0u ? key[i] : ~0u;
+  const u32 total = rank_tile<4, ITEMS>(sm, digit, place, s.bits), base = block_scan<4>(total, sm.wave);
+  sm.base[threadIdx.x] = base;
+  if (blockIdx.x == 0 && threadIdx.x < s.n_keys) *gptr(s.ends + threadIdx.x) = (int32_t)(base + total);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < ITEMS; i++) {
+    if (item[i] == ~0u) continue;
+    const u32 to = sm.base[digit[i]] + place[i];
+    rank[item[i]] = key[i] < s.n_keys ? (uint16_t)to : (uint16_t)0xffff;
+    if (blockIdx.x != 0) continue;
+    sort_place(s, item[i], key[i], to);
+    sort_rank(s, item[i], key[i], to);
+  }
+  __syncthreads();
+  for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
+    if (first + threadIdx.x >= a.pieces.total) continue;
+    int64_t t;
+    u32 c;
+    place_of(a.pieces, first, threadIdx.x, t, c);
+    const u32 col = piece_col<VEC>(c, a.H);
+    Piece<T, VEC> v;
+    v.load(static_cast<const T *>(a.in) + t * a.ld_in + col);
+    for (u32 j = 0; j < a.k; j++) {
+      const u32 r = rank[(u32)t * a.k + j];
+      if (r != 0xffff) v.store(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col);
     }
   }
 }

@@ -114,12 +114,15 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
 #pragma unroll
   for (int i = 0; i < ITEMS; i++) {
     const bool have = digit[i] != ~0u;
-    uint64_t same = __ballot(have);
+    uint64_t same = __ballot(have);  // the lanes with this lane's digit
     if (same == 0) break;
-    for (u32 b = 0; b < bits; b++) {
-      const int one = __builtin_amdgcn_sbfe((int)digit[i], b, 1);  // 0 or -1
-      same &= __ballot(one == 0) ^ (uint64_t)(int64_t)one;
-    }
+    // (bits past the last are zero in every lane and change nothing)
+    for (u32 b = 0; b < bits; b += 4)
+#pragma unroll
+      for (u32 e = 0; e < 4; e++) {
+        const int one = __builtin_amdgcn_sbfe((int)digit[i], b + e, 1);  // 0 or -1
+        same &= __ballot(one == 0) ^ (uint64_t)(int64_t)one;
+      }
     const u32 lower = __popcll(same & ((1ull << lane) - 1));
     if (have) {
       const u32 before = sm.count[w][digit[i]];
@@ -133,11 +136,13 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
   __syncthreads();
   u32 total = 0;
   if (threadIdx.x < bins) {
+    u32 c[W];
+#pragma unroll
+    for (int i = 0; i < W; i++) c[i] = sm.count[i][threadIdx.x];
 #pragma unroll
     for (int i = 0; i < W; i++) {
-      const u32 c = sm.count[i][threadIdx.x];
       sm.count[i][threadIdx.x] = (uint16_t)total;
-      total += c;
+      total += c[i];
     }
   }
   __syncthreads();
@@ -151,7 +156,8 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
 // and set by the second.
 __device__ __forceinline__ void sort_clear_flags(const SortArgs &a) {
   if (!a.flags) return;  // 16 bytes at a time: they begin and end on multiples of it
-  for (int64_t i = (int64_t)(blockIdx.x * kSortThreads + threadIdx.x) * 16; i < a.n_keys; i += (int64_t)gridDim.x * kSortThreads * 16)
+  const int64_t step = (int64_t)gridDim.x * kSortThreads * 16;
+  for (int64_t i = (int64_t)(blockIdx.x * kSortThreads + threadIdx.x) * 16; i < a.n_keys; i += step)
     *gptr(reinterpret_cast<u32x4_t *>(a.flags + i)) = u32x4_t{};
 }
 

@@ -298,3 +298,18 @@ def test_wrong_arguments():
             (lambda: mx.mxtrain_dispatch_bwd(rows.t(), rank, out=x.t()), ValueError)):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,k,E", [(64, 4, 255), (65, 4, 7), (128, 8, 64), (205, 5, 9), (512, 4, 200), (513, 4, 200), (100, 3, 256)])
+def test_one_call_is_the_sort_and_the_move(T, k, E, dtype):
+    """On both sides of every border of the form that sorts and moves in one launch (256, 1024 and 2048 pairs, 255
+    experts): the same bits as the two calls."""
+    g = gen(T)
+    ids = torch.randint(-1, E + 1, (T, k), generator=g, device="cuda")
+    for H in (1, 3, 40, 1031):
+        x = torch.randn((T, H), generator=g, device="cuda").to(dtype)
+        xs, *index = mx.mxtrain_sort_dispatch(x, ids, E, out=torch.zeros((T * k, H), dtype=dtype, device="cuda"))
+        want = mx.mxtrain_expert_sort(ids, E)
+        assert all(torch.equal(a, b) for a, b in zip(index, want))
+        assert torch.equal(xs, mx.mxtrain_dispatch_fwd(x, want[0], out=torch.zeros_like(xs)))

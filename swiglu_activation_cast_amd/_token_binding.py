@@ -14,7 +14,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._train_binding import (_FLOATS, _SIGNATURES, _TYPES, _call, _f32, _gpu, _i64, _int, _ld, _other_stream, _out, _p,
+from ._train_binding import (_FLOATS, _SIGNATURES, _TYPES, _call, _f32, _gpu, _i64, _int, _other_stream, _out, _p,
                              _place, _stream_of, _workspace, _workspace_bytes)
 
 _u64 = ctypes.c_uint64
@@ -42,6 +42,23 @@ _SIGNATURES.update({
 _INTS = {torch.int32: 0, torch.int64: 1}
 
 
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """_ld of a matrix, with half of its calls."""
+    rows, cols = t.shape
+    step, unit = t.stride()
+    if unit != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return step if rows > 1 else max(step, cols)
+
+
+def _matrix(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> Tuple[torch.Tensor, int]:
+    """`out`, checked, or a new matrix, and its row stride."""
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+    _out(out, "out", (rows, cols), dtype, device)
+    return out, _row_stride(out, "out")
+
+
 # ------------------------------------------------------- tokens and experts
 def _pairs(t, name: str, dtypes, device=None) -> Tuple[int, int]:
     """(T, k) of a tensor [T, k], or [T] for one expert a token."""
@@ -53,7 +70,7 @@ def _id_stride(ids: torch.Tensor) -> int:
     """Elements from one token's ids to the next's."""
     if ids.dim() == 1:
         return ids.stride(0) if ids.shape[0] > 1 else 1
-    return _ld(ids, "ids")
+    return _row_stride(ids, "ids")
 
 
 def _index_out(t: Optional[torch.Tensor], name: str, shape, device) -> torch.Tensor:
@@ -115,11 +132,11 @@ def mxtrain_dispatch_fwd(x: torch.Tensor, rank: torch.Tensor, *, rows: Optional[
         raise ValueError("x and rank must have the same tokens")
     if rows is None:
         rows = T * k if out is None else out.shape[0]
-    xs = _out(out, "out", (rows, x.shape[1]), x.dtype, dev)
+    xs, ld_out = _matrix(out, rows, x.shape[1], x.dtype, dev)
     if stream is not None:
         _other_stream(dev, stream, x, rank, xs)
-    _call("mxtrain_dispatch_fwd", dev, x.data_ptr(), _ld(x, "x"), _TYPES[x.dtype], rank.data_ptr(), T, k, x.shape[1],
-          rows, xs.data_ptr(), _ld(xs, "out"), _stream_of(dev, stream))
+    _call("mxtrain_dispatch_fwd", dev, x.data_ptr(), _row_stride(x, "x"), _TYPES[x.dtype], rank.data_ptr(), T, k,
+          x.shape[1], rows, xs.data_ptr(), ld_out, _stream_of(dev, stream))
     return xs
 
 
@@ -138,15 +155,15 @@ def mxtrain_sort_dispatch(x: torch.Tensor, ids: torch.Tensor, num_experts: int, 
     H = x.shape[1]
     if x.shape[0] != T:
         raise ValueError("x and ids must have the same tokens")
-    xs = _out(out, "out", (T * k, H), x.dtype, dev)
+    xs, ld_out = _matrix(out, T * k, H, x.dtype, dev)
     rank = _index_out(rank, "rank", ids.shape, dev)
     ends = _index_out(ends, "ends", (num_experts,), dev)
     order = _index_out(order, "order", (T * k,), dev)
     ws = _workspace(_workspace_bytes("mxtrain_expert_sort_workspace", T * k, num_experts), workspace, dev)
     if stream is not None:
         _other_stream(dev, stream, x, ids, xs, rank, ends, order, ws)
-    _call("mxtrain_sort_dispatch", dev, x.data_ptr(), _ld(x, "x"), _TYPES[x.dtype], ids.data_ptr(), _id_stride(ids),
-          _INTS[ids.dtype], T, k, first, num_experts, H, xs.data_ptr(), _ld(xs, "out"), rank.data_ptr(),
+    _call("mxtrain_sort_dispatch", dev, x.data_ptr(), _row_stride(x, "x"), _TYPES[x.dtype], ids.data_ptr(),
+          _id_stride(ids), _INTS[ids.dtype], T, k, first, num_experts, H, xs.data_ptr(), ld_out, rank.data_ptr(),
           ends.data_ptr(), order.data_ptr(), *_place(ws), _stream_of(dev, stream))
     return xs, rank, ends, order
 
@@ -158,11 +175,11 @@ def mxtrain_dispatch_bwd(dxs: torch.Tensor, rank: torch.Tensor, *, out: Optional
     dev = dxs.device
     T, k = _rank(rank, dev)
     R, H = dxs.shape
-    dx = _out(out, "out", (T, H), dxs.dtype, dev)
+    dx, ld_out = _matrix(out, T, H, dxs.dtype, dev)
     if stream is not None:
         _other_stream(dev, stream, dxs, rank, dx)
-    _call("mxtrain_dispatch_bwd", dev, dxs.data_ptr(), _ld(dxs, "dxs"), _TYPES[dxs.dtype], rank.data_ptr(), T, k, H, R,
-          dx.data_ptr(), _ld(dx, "out"), _stream_of(dev, stream))
+    _call("mxtrain_dispatch_bwd", dev, dxs.data_ptr(), _row_stride(dxs, "dxs"), _TYPES[dxs.dtype], rank.data_ptr(),
+          T, k, H, R, dx.data_ptr(), ld_out, _stream_of(dev, stream))
     return dx
 
 
@@ -183,12 +200,12 @@ def mxtrain_combine_fwd(ys: torch.Tensor, rank: torch.Tensor, weights: torch.Ten
         _gpu(residual, "residual", (ys.dtype,), 2, dev)
         if residual.shape != (T, H):
             raise ValueError(f"residual must have shape {(T, H)}, got {tuple(residual.shape)}")
-    y = _out(out, "out", (T, H), ys.dtype, dev)
+    y, ld_out = _matrix(out, T, H, ys.dtype, dev)
     if stream is not None:
         _other_stream(dev, stream, ys, rank, weights, residual, y)
-    _call("mxtrain_combine_fwd", dev, ys.data_ptr(), _ld(ys, "ys"), _TYPES[ys.dtype], rank.data_ptr(), pw,
+    _call("mxtrain_combine_fwd", dev, ys.data_ptr(), _row_stride(ys, "ys"), _TYPES[ys.dtype], rank.data_ptr(), pw,
           _TYPES[weights.dtype], None if residual is None else residual.data_ptr(),
-          0 if residual is None else _ld(residual, "residual"), T, k, H, R, y.data_ptr(), _ld(y, "out"),
+          0 if residual is None else _row_stride(residual, "residual"), T, k, H, R, y.data_ptr(), ld_out,
           _stream_of(dev, stream))
     return y
 
@@ -210,7 +227,7 @@ def mxtrain_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, rank: torch.Tensor, 
     if dy.shape != (T, H):
         raise ValueError(f"dy must have shape {(T, H)}, got {tuple(dy.shape)}")
     pw = _weights(weights, rank)
-    dys = _out(out, "out", (R, H), ys.dtype, dev)
+    dys, ld_out = _matrix(out, R, H, ys.dtype, dev)
     if dweights is None:
         dweights = torch.empty(rank.shape, dtype=torch.float32, device=dev)
     elif (dweights.dtype != torch.float32 or dweights.device != dev or dweights.shape != rank.shape
@@ -218,8 +235,8 @@ def mxtrain_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, rank: torch.Tensor, 
         raise ValueError("dweights must be a contiguous float32 tensor of rank's shape on the inputs' device")
     if stream is not None:
         _other_stream(dev, stream, dy, ys, rank, weights, dys, dweights)
-    _call("mxtrain_combine_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), ys.data_ptr(), _ld(ys, "ys"), _TYPES[ys.dtype],
-          rank.data_ptr(), pw, _TYPES[weights.dtype], T, k, H, R, dys.data_ptr(), _ld(dys, "out"),
+    _call("mxtrain_combine_bwd", dev, dy.data_ptr(), _row_stride(dy, "dy"), ys.data_ptr(), _row_stride(ys, "ys"),
+          _TYPES[ys.dtype], rank.data_ptr(), pw, _TYPES[weights.dtype], T, k, H, R, dys.data_ptr(), ld_out,
           dweights.data_ptr(), _stream_of(dev, stream))
     return dys, dweights
 
@@ -263,12 +280,15 @@ def mxtrain_embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, *, scale: flo
     dtype = out.dtype if out is not None else out_dtype or weight.dtype
     if dtype not in _TYPES:
         raise TypeError(f"results are bfloat16 or float32, not {dtype}")
-    y = _out(out, "out", (*ids.shape, H), dtype, dev)
-    rows = _rows_of(y, "out", _FLOATS, ids, dev)
+    if out is None:
+        y, ld_out = torch.empty((*ids.shape, H), dtype=dtype, device=dev), H
+    else:
+        y = _out(out, "out", (*ids.shape, H), dtype, dev)
+        ld_out = _row_stride(_rows_of(y, "out", _FLOATS, ids, dev), "out")
     if stream is not None:
         _other_stream(dev, stream, weight, ids, y)
-    _call("mxtrain_embedding_fwd", dev, weight.data_ptr(), _ld(weight, "weight"), _TYPES[weight.dtype], V, H,
-          ids.data_ptr(), step, _INTS[ids.dtype], T, first, scale, rows.data_ptr(), _ld(rows, "out"), _TYPES[dtype],
+    _call("mxtrain_embedding_fwd", dev, weight.data_ptr(), _row_stride(weight, "weight"), _TYPES[weight.dtype], V, H,
+          ids.data_ptr(), step, _INTS[ids.dtype], T, first, scale, y.data_ptr(), ld_out, _TYPES[dtype],
           _stream_of(dev, stream))
     return y
 
@@ -295,13 +315,13 @@ def mxtrain_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, num_embeddings: i
     dtype = out.dtype if out is not None else out_dtype
     if dtype not in _TYPES:
         raise TypeError(f"results are bfloat16 or float32, not {dtype}")
-    dw = _out(out, "out", (num_embeddings, H), dtype, dev)
+    dw, ld_out = _matrix(out, num_embeddings, H, dtype, dev)
     ws = _workspace(_workspace_bytes("mxtrain_embedding_bwd_workspace", T, num_embeddings, H, _TYPES[dy.dtype],
                                      _TYPES[dtype]), workspace, dev)
     if stream is not None:
         _other_stream(dev, stream, dy, ids, dw, ws)
-    _call("mxtrain_embedding_bwd", dev, rows.data_ptr(), _ld(rows, "dy"), _TYPES[dy.dtype], ids.data_ptr(), step,
-          _INTS[ids.dtype], T, first, scale, num_embeddings, H, dw.data_ptr(), _ld(dw, "out"), _TYPES[dtype],
+    _call("mxtrain_embedding_bwd", dev, rows.data_ptr(), _row_stride(rows, "dy"), _TYPES[dy.dtype], ids.data_ptr(),
+          step, _INTS[ids.dtype], T, first, scale, num_embeddings, H, dw.data_ptr(), ld_out, _TYPES[dtype],
           int(accumulate), *_place(ws), _stream_of(dev, stream))
     return dw
 
@@ -339,13 +359,14 @@ def mxtrain_dropout_fwd(x: torch.Tensor, p: float, seed: int, offset: int, *,
         _gpu(residual, "residual", (x.dtype,), 2, dev)
         if residual.shape != x.shape:
             raise ValueError("residual and x must have the same shape")
-    y = _out(out, "out", x.shape, x.dtype, dev)
+    y, ld_out = _matrix(out, M, N, x.dtype, dev)
     ps = _state(state, dev)
     if stream is not None:
         _other_stream(dev, stream, x, residual, state, y)
-    _call("mxtrain_dropout_fwd", dev, x.data_ptr(), _ld(x, "x"), None if residual is None else residual.data_ptr(),
-          0 if residual is None else _ld(residual, "residual"), _TYPES[x.dtype], M, N, p, _word(seed, "seed"),
-          _word(offset, "offset"), ps, y.data_ptr(), _ld(y, "out"), _stream_of(dev, stream))
+    _call("mxtrain_dropout_fwd", dev, x.data_ptr(), _row_stride(x, "x"),
+          None if residual is None else residual.data_ptr(),
+          0 if residual is None else _row_stride(residual, "residual"), _TYPES[x.dtype], M, N, p, _word(seed, "seed"),
+          _word(offset, "offset"), ps, y.data_ptr(), ld_out, _stream_of(dev, stream))
     return y
 
 
@@ -356,10 +377,10 @@ def mxtrain_dropout_bwd(dy: torch.Tensor, p: float, seed: int, offset: int, *, s
     _gpu(dy, "dy", _FLOATS, 2)
     dev = dy.device
     M, N = dy.shape
-    dx = _out(out, "out", dy.shape, dy.dtype, dev)
+    dx, ld_out = _matrix(out, M, N, dy.dtype, dev)
     ps = _state(state, dev)
     if stream is not None:
         _other_stream(dev, stream, dy, state, dx)
-    _call("mxtrain_dropout_bwd", dev, dy.data_ptr(), _ld(dy, "dy"), _TYPES[dy.dtype], M, N, p, _word(seed, "seed"),
-          _word(offset, "offset"), ps, dx.data_ptr(), _ld(dx, "out"), _stream_of(dev, stream))
+    _call("mxtrain_dropout_bwd", dev, dy.data_ptr(), _row_stride(dy, "dy"), _TYPES[dy.dtype], M, N, p,
+          _word(seed, "seed"), _word(offset, "offset"), ps, dx.data_ptr(), ld_out, _stream_of(dev, stream))
     return dx

@@ -197,8 +197,8 @@ mxtrain_status mxtrain_sort_dispatch(const void *x, int64_t ld_x, int dtype, con
     g.move.out = xs;
     g.move.ld_out = ld_xs;
     // no more workgroups than run at once: each begins with a sort
-    return launch(ROUTE_PICK(sort_dispatch_kernel, dtype, H, T * k), std::min<int64_t>((g.move.pieces.total + 255) / 256, 2048),
-                  256, g, stream);
+    const int64_t blocks = std::min<int64_t>((g.move.pieces.total + 255) / 256, 2048);
+    return launch(ROUTE_PICK(sort_dispatch_kernel, dtype, H, T * k), blocks, 256, g, stream);
   }
   st = mxtrain_expert_sort(ids, ld_ids, id_type, T, k, first, G, rank, ends, order, workspace, workspace_bytes, stream);
   return st != MXTRAIN_OK ? st : mxtrain_dispatch_fwd(x, ld_x, dtype, rank, T, k, H, T * k, xs, ld_xs, stream);
@@ -270,7 +270,8 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
   int64_t steps = std::max<int64_t>(1, (per + 128) / 256);
   while (steps > 1 && T * ((per + 64 * steps - 1) / (64 * steps)) < 1024) steps--;
   const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (per + 64 * steps - 1) / (64 * steps)));
-  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes), std::min(T, kMaxGrid), 64 * waves, a, stream);
+  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes), std::min(T, kMaxGrid), 64 * waves, a,
+                stream);
 }
 
 }  // extern "C"

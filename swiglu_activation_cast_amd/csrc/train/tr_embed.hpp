@@ -41,7 +41,8 @@ struct EmbedArgs {
 // or 1 where rows are shorter than that.
 template <class T, class U, int VEC, int N>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
-  for (int64_t first = (int64_t)blockIdx.x * (256 * N); first < a.pieces.total; first += (int64_t)gridDim.x * (256 * N)) {
+  const int64_t step = (int64_t)gridDim.x * (256 * N);
+  for (int64_t first = (int64_t)blockIdx.x * (256 * N); first < a.pieces.total; first += step) {
     int64_t t[N];
     u32 col[N];
     uint64_t key[N];
@@ -128,7 +129,7 @@ __device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
 
 // Part 0 of a chunk belongs to a word that began in an earlier chunk, part 1 to
 // one that begins here and goes on in the next.
-template <class T, class U, int VEC>
+template <class T, class U, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   if (blockIdx.x >= a.sum_blocks) {
     embed_zeros<U, VEC>(a);
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
 #pragma unroll
     for (int u = 0; u < N; u++) {
       const u32 token = __builtin_amdgcn_readlane(my_token, min(i0 + u, valid - 1));
-      d[u].load(dy + (int64_t)token * a.ld_in);
+      d[u].template load<NT>(dy + (int64_t)token * a.ld_in);
     }
 #pragma unroll
     for (int u = 0; u < N; u++) {
@@ -202,17 +203,22 @@ __global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
   const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const u32 lo = chunk * a.rows, next = lo + a.rows;
   if (next >= a.T) return;
-  const u32 word = *gptr(a.keys + next);
-  if (word >= a.V || *gptr(a.keys + next - 1) != word) return;  // nothing goes on
-  if (lo > 0 && *gptr(a.keys + lo) == word && *gptr(a.keys + lo - 1) == word) return;  // it began earlier
+  // all that decides, in flight together: the word at the border and its
+  // neighbours, and the first words of the 64 chunks after it
+  const u32 word = *gptr(a.keys + next), last = *gptr(a.keys + next - 1);
+  const u32 first = *gptr(a.keys + lo), before = *gptr(a.keys + max(lo, 1u) - 1);
+  auto begins = [&](u32 c) { return *gptr(a.keys + (int64_t)min(c, a.chunks - 1) * a.rows); };
+  u32 ahead = begins(chunk + 1 + lane);
+  if (word >= a.V || last != word) return;                   // nothing goes on
+  if (lo > 0 && first == word && before == word) return;     // it began earlier
   // chunks that begin with this word: those after `chunk` up to the first that does not
   u32 parts = 1;
   for (;;) {
-    const u32 c = chunk + parts + lane;
-    const uint64_t same = __ballot(c < a.chunks && *gptr(a.keys + min(c, a.chunks - 1) * a.rows) == word);
+    const uint64_t same = __ballot(chunk + parts + lane < a.chunks && ahead == word);
     const u32 n = same == ~0ull ? 64 : __builtin_ctzll(~same);
     parts += n;
     if (n < 64) break;
+    ahead = begins(chunk + parts + lane);
   }
   const u32 piece = strip * 64 + lane;
   const bool in = piece * VEC < a.H;
@@ -236,7 +242,8 @@ __global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
   __syncthreads();
   if (wave != 0 || !in) return;
 #pragma unroll
-  for (int j = 0; j < VEC; j++) sum[j] = ((sum[j] + sm[1][j * 64 + lane]) + sm[2][j * 64 + lane]) + sm[3][j * 64 + lane];
+  for (int j = 0; j < VEC; j++)
+    sum[j] = ((sum[j] + sm[1][j * 64 + lane]) + sm[2][j * 64 + lane]) + sm[3][j * 64 + lane];
   embed_write<U, VEC>(a, word, piece, sum);
 }
 

@@ -114,15 +114,20 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
 #pragma unroll
   for (int i = 0; i < ITEMS; i++) {
     const bool have = digit[i] != ~0u;
-    uint64_t same = __ballot(have);  // the lanes with this lane's digit
-    if (same == 0) break;
-    // (bits past the last are zero in every lane and change nothing)
+    const uint64_t any = __ballot(have);
+    if (any == 0) break;
+    // the lanes with this lane's digit (bits past the last are zero in every lane
+    // and change nothing); these are most of a sort's instructions
+    u32 same_lo = (u32)any, same_hi = (u32)(any >> 32);
     for (u32 b = 0; b < bits; b += 4)
 #pragma unroll
       for (u32 e = 0; e < 4; e++) {
-        const int one = __builtin_amdgcn_sbfe((int)digit[i], b + e, 1);  // 0 or -1
-        same &= __ballot(one == 0) ^ (uint64_t)(int64_t)one;
+        const u32 one = (u32)__builtin_amdgcn_sbfe((int)digit[i], b + e, 1);  // 0 or ~0
+        const uint64_t without = __ballot(one == 0);
+        same_lo &= (u32)without ^ one;
+        same_hi &= (u32)(without >> 32) ^ one;
       }
+    const uint64_t same = (uint64_t)same_hi << 32 | same_lo;
     const u32 lower = __popcll(same & ((1ull << lane) - 1));
     if (have) {
       const u32 before = sm.count[w][digit[i]];

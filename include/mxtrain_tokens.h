@@ -96,7 +96,7 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
  *   dy        : dy_type [T, H], row stride ld_dy
  *   dweight   : dw_type [V, H], row stride ld_dw
  *   workspace : at least mxtrain_embedding_bwd_workspace(T, V, H, dy_type, dw_type)
- *               bytes, 16-byte aligned
+ *               bytes (0 for few tokens, then it may be NULL), 16-byte aligned
  * Tokens are sorted by word and each word's rows summed in the order of the
  * tokens, in parts of at most 64 rows that are joined in order.  scale is finite
  * (MXTRAIN_ERR_VALUE).  T, V, H < 2^31.

@@ -55,6 +55,11 @@ const void *sum_kernel(bool nt) {
 }
 
 template <class T, class U, int VEC>
+const void *few_kernel() {
+  return (const void *)&k_embed_bwd_few<T, U, VEC>;
+}
+
+template <class T, class U, int VEC>
 const void *join_kernel() {
   return (const void *)&k_embed_join<T, U, VEC>;
 }
@@ -119,7 +124,7 @@ mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weigh
 
 int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_type, int dw_type) {
   if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0) return 0;
-  if (T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
+  if (T > INT32_MAX || V > INT32_MAX || H > INT32_MAX || T <= kEmbedFew) return 0;
   return embed_plan(sort_plan(T, V, true), T, V, H, embed_vec(dy_type, dw_type, H)).bytes;
 }
 
@@ -134,12 +139,13 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   if (V == 0 || H == 0 || (T == 0 && accumulate)) return MXTRAIN_OK;
   const SortPlan sp = sort_plan(T, V, true);
   const EmbedPlan ep = embed_plan(sp, T, V, H, embed_vec(dy_type, dw_type, H));
-  if (T > 0 && !workspace) return MXTRAIN_ERR_NULL;
-  if (T > 0 && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
-  if (T > 0 && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
+  const bool few = T <= kEmbedFew;
+  if (!few && !workspace) return MXTRAIN_ERR_NULL;
+  if (!few && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
+  if (!few && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
   const int64_t vec = embed_vec(dy_type, dw_type, H), zero_vec = vec == 1 ? 1 : 16 / size_of(dw_type);
   const int64_t zero_per = (H + zero_vec - 1) / zero_vec, zeros = accumulate ? 0 : V * zero_per;
-  const int64_t jobs = (int64_t)ep.chunks * ep.strips, sum_blocks = (jobs + 3) / 4;
+  const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips, sum_blocks = (jobs + 3) / 4;
   if (jobs > INT32_MAX / 256) return MXTRAIN_ERR_OVERFLOW;
   const int64_t zero_blocks = std::min<int64_t>((zeros + 255) / 256, INT32_MAX / 512);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -160,23 +166,26 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   a.strips = ep.strips;
   a.sum_blocks = (u32)sum_blocks;
   a.zeros = {zeros, divider((uint32_t)zero_per)};
-  a.flags = T > 0 ? ws + ep.flags : nullptr;
+  a.flags = ws + ep.flags;
   a.accumulate = accumulate;
-  if (T > 0) {
-    SortArgs s{};
-    s.ids = ids;
-    s.ld = id_stride;
-    s.first = first;
-    s.k = divider(1);
-    s.ids_i64 = id_type == MXTRAIN_I64;
-    s.n = (u32)T;
-    s.n_keys = (u32)V;
-    s.flags = accumulate ? nullptr : ws + ep.flags;
-    s.order = reinterpret_cast<int32_t *>(ws + sp.order);
-    s.key_out = reinterpret_cast<u32 *>(ws + sp.keys);
-    if ((st = sort_run(sp, s, ws, stream)) != MXTRAIN_OK) return st;
-  }
+  a.ids = ids;
+  a.id_stride = id_stride;
+  a.ids_i64 = id_type == MXTRAIN_I64;
+  a.first = first;
   const bool f = dy_type == MXTRAIN_F32, g = dw_type == MXTRAIN_F32;
+  if (few) return launch(EMBED_PICK(few_kernel, vec, f, g), sum_blocks + zero_blocks, 256, a, stream);
+  SortArgs s{};
+  s.ids = ids;
+  s.ld = id_stride;
+  s.first = first;
+  s.k = divider(1);
+  s.ids_i64 = id_type == MXTRAIN_I64;
+  s.n = (u32)T;
+  s.n_keys = (u32)V;
+  s.flags = accumulate ? nullptr : ws + ep.flags;
+  s.order = reinterpret_cast<int32_t *>(ws + sp.order);
+  s.key_out = reinterpret_cast<u32 *>(ws + sp.keys);
+  if ((st = sort_run(sp, s, ws, stream)) != MXTRAIN_OK) return st;
   // 128 MB or more (half the last-level cache) are read past the caches: 65537 rows
   // of 2048 bf16 on 4099 words 92 us so, 96 otherwise, on 65 words 76 and 82
   const bool nt = (double)T * (double)H * size_of(dy_type) >= (double)(1 << 27);

@@ -156,14 +156,16 @@ def test_embedding_checks(call):
 
 def test_embedding_own_checks():
     assert embed(T=0, tokens=None, ids=None) == OK
-    assert embed_bwd(acc=2) == VALUE and embed_bwd(ws=None) == NULL and embed_bwd(ws=A + 8) == ALIGN
+    assert embed_bwd(acc=2) == VALUE
+    assert embed_bwd(T=500, ws=None) == NULL and embed_bwd(T=500, ws=A + 8) == ALIGN
     for wt, tt in ((BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)):
-        need = mx.train_lib().mxtrain_embedding_bwd_workspace(8, 100, 64, tt, wt)
-        assert need > 0 and embed_bwd(wt=wt, tt=tt, bytes=need - 1) == WORKSPACE
+        need = mx.train_lib().mxtrain_embedding_bwd_workspace(500, 100, 64, tt, wt)
+        assert need > 0 and embed_bwd(T=500, wt=wt, tt=tt, bytes=need - 1) == WORKSPACE
+        assert mx.train_lib().mxtrain_embedding_bwd_workspace(256, 100, 64, tt, wt) == 0
     assert embed_bwd(V=0, table=None) == OK and embed_bwd(T=0, acc=1, ids=None, tokens=None, ws=None) == OK
     ws = mx.train_lib().mxtrain_embedding_bwd_workspace
     assert ws(0, 100, 64, 0, 0) == 0 and ws(8, 0, 64, 0, 0) == 0 and ws(8, 100, 0, 0, 0) == 0
-    assert ws(8, 100, 64, 2, 0) == 0 and ws(8, 100, 64, 0, 2) == 0 and ws(BIG, 100, 64, 0, 0) == 0
+    assert ws(500, 100, 64, 2, 0) == 0 and ws(500, 100, 64, 0, 2) == 0 and ws(BIG, 100, 64, 0, 0) == 0
 
 
 def dropout(**kw):

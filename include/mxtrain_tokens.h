@@ -99,7 +99,9 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
  *               bytes (0 for few tokens, then it may be NULL), 16-byte aligned
  * Tokens are sorted by word and each word's rows summed in the order of the
  * tokens, in parts of at most 64 rows that are joined in order.  scale is finite
- * (MXTRAIN_ERR_VALUE).  T, V, H < 2^31.
+ * (MXTRAIN_ERR_VALUE).  T, V, H < 2^31; in the gradient T times the strips of a
+ * row, 256 columns of fp32 into fp32, 512 otherwise, at most 2^29
+ * (MXTRAIN_ERR_OVERFLOW).
  */
 mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weight_type, int64_t V, int64_t H,
                                      const void *ids, int64_t id_stride, int id_type, int64_t T, int64_t first,

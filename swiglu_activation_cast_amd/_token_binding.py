@@ -73,6 +73,12 @@ def _id_stride(ids: torch.Tensor) -> int:
     return _row_stride(ids, "ids")
 
 
+def _first(first: int) -> int:
+    if not -(1 << 63) <= first < 1 << 63:
+        raise ValueError(f"first must fit 64 bits, got {first}")
+    return first
+
+
 def _index_out(t: Optional[torch.Tensor], name: str, shape, device) -> torch.Tensor:
     if t is None:
         return torch.empty(shape, dtype=torch.int32, device=device)
@@ -114,7 +120,7 @@ def mxtrain_expert_sort(ids: torch.Tensor, num_experts: int, *, first: int = 0, 
     ws = _workspace(_workspace_bytes("mxtrain_expert_sort_workspace", T * k, num_experts), workspace, dev)
     if stream is not None:
         _other_stream(dev, stream, ids, rank, ends, order, ws)
-    _call("mxtrain_expert_sort", dev, ids.data_ptr(), _id_stride(ids), _INTS[ids.dtype], T, k, first, num_experts,
+    _call("mxtrain_expert_sort", dev, ids.data_ptr(), _id_stride(ids), _INTS[ids.dtype], T, k, _first(first), num_experts,
           rank.data_ptr(), ends.data_ptr(), order.data_ptr(), *_place(ws), _stream_of(dev, stream))
     return rank, ends, order
 
@@ -163,7 +169,7 @@ def mxtrain_sort_dispatch(x: torch.Tensor, ids: torch.Tensor, num_experts: int, 
     if stream is not None:
         _other_stream(dev, stream, x, ids, xs, rank, ends, order, ws)
     _call("mxtrain_sort_dispatch", dev, x.data_ptr(), _row_stride(x, "x"), _TYPES[x.dtype], ids.data_ptr(),
-          _id_stride(ids), _INTS[ids.dtype], T, k, first, num_experts, H, xs.data_ptr(), ld_out, rank.data_ptr(),
+          _id_stride(ids), _INTS[ids.dtype], T, k, _first(first), num_experts, H, xs.data_ptr(), ld_out, rank.data_ptr(),
           ends.data_ptr(), order.data_ptr(), *_place(ws), _stream_of(dev, stream))
     return xs, rank, ends, order
 
@@ -288,7 +294,7 @@ def mxtrain_embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, *, scale: flo
     if stream is not None:
         _other_stream(dev, stream, weight, ids, y)
     _call("mxtrain_embedding_fwd", dev, weight.data_ptr(), _row_stride(weight, "weight"), _TYPES[weight.dtype], V, H,
-          ids.data_ptr(), step, _INTS[ids.dtype], T, first, scale, y.data_ptr(), ld_out, _TYPES[dtype],
+          ids.data_ptr(), step, _INTS[ids.dtype], T, _first(first), scale, y.data_ptr(), ld_out, _TYPES[dtype],
           _stream_of(dev, stream))
     return y
 
@@ -321,7 +327,7 @@ def mxtrain_embedding_bwd(dy: torch.Tensor, ids: torch.Tensor, num_embeddings: i
     if stream is not None:
         _other_stream(dev, stream, dy, ids, dw, ws)
     _call("mxtrain_embedding_bwd", dev, rows.data_ptr(), _row_stride(rows, "dy"), _TYPES[dy.dtype], ids.data_ptr(),
-          step, _INTS[ids.dtype], T, first, scale, num_embeddings, H, dw.data_ptr(), ld_out, _TYPES[dtype],
+          step, _INTS[ids.dtype], T, _first(first), scale, num_embeddings, H, dw.data_ptr(), ld_out, _TYPES[dtype],
           int(accumulate), *_place(ws), _stream_of(dev, stream))
     return dw
 

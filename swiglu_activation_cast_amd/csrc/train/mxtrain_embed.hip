@@ -64,6 +64,16 @@ const void *join_kernel() {
   return (const void *)&k_embed_join<T, U, VEC>;
 }
 
+// Wavefronts that sum: as many workgroups as a launch takes join their parts.
+constexpr int64_t kMaxJobs = INT32_MAX / 256;
+
+// Few enough tokens for the gradient without a sort (and every strip of each has
+// a wavefront).
+bool embed_few(int64_t T, int64_t H, int64_t vec) {
+  const int64_t strips = ((H + vec - 1) / vec + 63) / 64;
+  return T <= kEmbedFew && T * strips <= kMaxJobs;
+}
+
 // How the gradient cuts its work: chunks of 64 tokens, or fewer where that
 // leaves less than sixteen wavefronts to a compute unit.
 struct EmbedPlan {
@@ -124,8 +134,9 @@ mxtrain_status mxtrain_embedding_fwd(const void *weight, int64_t ld_w, int weigh
 
 int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_type, int dw_type) {
   if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0) return 0;
-  if (T > INT32_MAX || V > INT32_MAX || H > INT32_MAX || T <= kEmbedFew) return 0;
-  return embed_plan(sort_plan(T, V, true), T, V, H, embed_vec(dy_type, dw_type, H)).bytes;
+  if (T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
+  const int64_t vec = embed_vec(dy_type, dw_type, H);
+  return embed_few(T, H, vec) ? 0 : embed_plan(sort_plan(T, V, true), T, V, H, vec).bytes;
 }
 
 mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type, const void *ids, int64_t id_stride,
@@ -138,15 +149,16 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   if (accumulate != 0 && accumulate != 1) return MXTRAIN_ERR_VALUE;
   if (V == 0 || H == 0 || (T == 0 && accumulate)) return MXTRAIN_OK;
   const SortPlan sp = sort_plan(T, V, true);
-  const EmbedPlan ep = embed_plan(sp, T, V, H, embed_vec(dy_type, dw_type, H));
-  const bool few = T <= kEmbedFew;
+  const int64_t vec = embed_vec(dy_type, dw_type, H), zero_vec = vec == 1 ? 1 : 16 / size_of(dw_type);
+  const EmbedPlan ep = embed_plan(sp, T, V, H, vec);
+  const bool few = embed_few(T, H, vec);
   if (!few && !workspace) return MXTRAIN_ERR_NULL;
   if (!few && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
   if (!few && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
-  const int64_t vec = embed_vec(dy_type, dw_type, H), zero_vec = vec == 1 ? 1 : 16 / size_of(dw_type);
   const int64_t zero_per = (H + zero_vec - 1) / zero_vec, zeros = accumulate ? 0 : V * zero_per;
-  const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips, sum_blocks = (jobs + 3) / 4;
-  if (jobs > INT32_MAX / 256) return MXTRAIN_ERR_OVERFLOW;
+  const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips;
+  if (jobs > kMaxJobs) return MXTRAIN_ERR_OVERFLOW;
+  const int64_t sum_blocks = (jobs + 3) / 4;
   const int64_t zero_blocks = std::min<int64_t>((zeros + 255) / 256, INT32_MAX / 512);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   EmbedArgs a{};
@@ -164,6 +176,7 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   a.rows = ep.rows;
   a.chunks = ep.chunks;
   a.strips = ep.strips;
+  a.jobs = (u32)jobs;
   a.sum_blocks = (u32)sum_blocks;
   a.zeros = {zeros, divider((uint32_t)zero_per)};
   a.flags = ws + ep.flags;

@@ -109,15 +109,18 @@ const void *combine_kernel(int wtype, bool nt) {
 
 // lanes: of a token, at least its row's pieces where fewer than 64.
 template <class T, class W, int VEC>
-const void *combine_bwd_lanes(int lanes) {
-  return lanes == 16 ? (const void *)&k_combine_bwd<T, W, VEC, 16>
-         : lanes == 32 ? (const void *)&k_combine_bwd<T, W, VEC, 32>
-                       : (const void *)&k_combine_bwd<T, W, VEC, 64>;
+const void *combine_bwd_lanes(int lanes, bool nt) {
+  if (lanes == 16) return (const void *)&k_combine_bwd<T, W, VEC, 16, false>;
+  if (lanes == 32) return (const void *)&k_combine_bwd<T, W, VEC, 32, false>;
+  if constexpr (VEC > 1)
+    if (nt) return (const void *)&k_combine_bwd<T, W, VEC, 64, true>;
+  return (const void *)&k_combine_bwd<T, W, VEC, 64, false>;
 }
 
 template <class T, int VEC>
-const void *combine_bwd_kernel(int wtype, int lanes) {
-  return wtype == MXTRAIN_F32 ? combine_bwd_lanes<T, float, VEC>(lanes) : combine_bwd_lanes<T, uint16_t, VEC>(lanes);
+const void *combine_bwd_kernel(int wtype, int lanes, bool nt) {
+  return wtype == MXTRAIN_F32 ? combine_bwd_lanes<T, float, VEC>(lanes, nt)
+                              : combine_bwd_lanes<T, uint16_t, VEC>(lanes, nt);
 }
 
 template <class T, int VEC>
@@ -136,9 +139,11 @@ mxtrain_status route_launch(const void *kernel, const RouteArgs &a, void *stream
   return launch(kernel, std::min((a.pieces.total + 255) / 256, kMaxGrid), 256, a, stream);
 }
 
-// Whether combine reads past the caches: rows of 128 MB or more (half the last
-// level's 256 MB).  16384 x 8 rows of 2048 bf16 126 us otherwise, 117 so; 4096 x
-// 8 29 and 26; but 2048 x 8 13.5 and 14.0, and odd fp32 rows of 43 MB 14.0 and 15.7.
+// Whether combine and its gradients read past the caches: rows of 128 MB or more
+// (half the last level's 256 MB).  Combine of 16384 x 8 rows of 2048 bf16: 126 us
+// otherwise, 117 so; 4096 x 8 29 and 26; but 2048 x 8 13.5 and 14.0, and odd fp32
+// rows of 43 MB 14.0 and 15.7.  Gradients of 16384 x 8 rows 229 and 223, of 4096 x 8
+// 62 and 59, of 2048 x 8 26 and 30.
 bool route_past_caches(int dtype, int64_t T, int64_t k, int64_t H) {
   return (double)T * (double)k * (double)H * size_of(dtype) >= (double)(1 << 27);
 }
@@ -264,14 +269,15 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
   // 2049 fp32: sixteen 18 us, four 13.)
   const int64_t per = a.pieces.per.d;
   const int lanes = per <= 16 ? 16 : per <= 32 ? 32 : 64;
+  const bool nt = route_past_caches(dtype, T, k, H);
   if (lanes < 64)
-    return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes),
+    return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes, nt),
                   std::min((T * lanes + 255) / 256, kMaxGrid), 256, a, stream);
   int64_t steps = std::max<int64_t>(1, (per + 128) / 256);
   while (steps > 1 && T * ((per + 64 * steps - 1) / (64 * steps)) < 1024) steps--;
   const int waves = (int)std::min<int64_t>(16, std::max<int64_t>(1, (per + 64 * steps - 1) / (64 * steps)));
-  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes), std::min(T, kMaxGrid), 64 * waves, a,
-                stream);
+  return launch(ROUTE_PICK(combine_bwd_kernel, dtype, H, weight_type, lanes, nt), std::min(T, kMaxGrid), 64 * waves,
+                a, stream);
 }
 
 }  // extern "C"

@@ -3,7 +3,8 @@
 
 namespace mxt {
 
-// One workgroup sorts everything (n <= kSortTile).
+// One workgroup sorts everything (n <= kSortTile).  Bound by instructions, six for
+// each bit of each item's digit: 8192 keys of 16 bits 20 us, 1000 7.
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
   __shared__ SortShared<16> sm;
   __shared__ u32 keys[kSortTile];
@@ -20,6 +21,7 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
   }
   sort_clear_flags(a);
   sort_keys<kSortItems>(a, item, key);
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // other wavefronts set what this one cleared
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kSortItems; i++)
@@ -77,7 +79,8 @@ __device__ __forceinline__ void sort_source(const SortArgs &a, const u32 *p, u32
   }
 }
 
-// counts[b][d]: items of workgroup b's range with digit d.
+// counts[b][d]: items of workgroup b's range with digit d.  131072 pairs: 4.8 us,
+// the launch and one load's way.
 __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
   __shared__ u32 count[1 << kSortBits];
   const u32 bins = 1u << a.bits, lo = blockIdx.x * a.per, hi = min(a.n, lo + a.per);
@@ -93,7 +96,9 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
   if (threadIdx.x < bins) *gptr(a.counts + (blockIdx.x << a.bits) + threadIdx.x) = count[threadIdx.x];
 }
 
-// Moves workgroup b's range to its places.
+// Moves workgroup b's range to its places.  Bound by the way of its loads, counts
+// (128 workgroups' here) and items together, and eight barriers: 131072 pairs by 64
+// experts 7.4 us, by 256 9 (24 with the counts read one at a time).
 __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   __shared__ SortShared<16> sm;
   __shared__ u32 sums[2][4 * kSortThreads];  // [groups][bins]

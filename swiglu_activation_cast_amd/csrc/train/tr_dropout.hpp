@@ -6,8 +6,10 @@
 // columns (Salmon, Moraes, Dror and Shaw, 2011: ten rounds, each two 32 x 32 ->
 // 64 bit products and four exclusive ors, with a key that grows by two constants).
 //
-// Bound by HBM as long as the block's cost, twenty products for eight elements,
-// stays below the time of their bytes.
+// Bound by HBM: twenty products for eight elements stay below the time of their
+// bytes, also without a residual.  (32 bits an element would double the products,
+// and with them take longer than bf16's bytes.)  16384 x 8192 bf16 with the
+// residual 127 us, 6.3 TB/s; without 97 us, 5.5 TB/s; 1021 x 2049 fp32 5 us.
 #pragma once
 #include "tr_rows.hpp"
 

@@ -31,14 +31,13 @@ struct EmbedArgs {
   float *part;              // [chunks][2][strips * 64 * VEC]
   u32 rows;                 // tokens of a chunk
   u32 chunks, strips;       // and of the columns, 64 pieces each
+  u32 jobs;                 // summing wavefronts: chunks (tokens, if few) x strips
   const uint8_t *flags;     // [V], 1: the word has tokens
   Pieces zeros;             // of dW's rows, 16 bytes each
   u32 sum_blocks;           // workgroups that sum; those after them write zeros
   int32_t accumulate;
 };
 
-// VEC, here and below: columns that a thread holds, 16 bytes of the narrower type,
-// or 1 where rows are shorter than that.
 // Token t's row of the table; V where it is outside.
 __device__ __forceinline__ u32 embed_key(const EmbedArgs &a, int64_t t) {
   const int64_t at = t * a.id_stride;
@@ -48,6 +47,10 @@ __device__ __forceinline__ u32 embed_key(const EmbedArgs &a, int64_t t) {
   return key < a.V ? (u32)key : a.V;
 }
 
+// VEC, here and below: columns that a thread holds, 16 bytes of the narrower type,
+// or 1 where rows are shorter than that.  N pieces a thread, whose loads of ids and
+// then of rows are in flight together: 16640 rows of 5120 bf16 out of 65536 50 us,
+// 4.8 TB/s over the distinct rows and y; 16 of 8192 3.2 us.
 template <class T, class U, int VEC, int N>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
   const int64_t step = (int64_t)gridDim.x * (256 * N);
@@ -135,6 +138,9 @@ __device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
 
 // Part 0 of a chunk belongs to a word that began in an earlier chunk, part 1 to
 // one that begins here and goes on in the next.
+// 16384 tokens on 65536 words x 5120, bf16 into fp32: 228 us, 6.6 TB/s over dy and
+// dW, most of it zeros; 65537 on 4099 x 2050 bf16: 65 us, 4.4 TB/s (rows that
+// start at odd multiples of 4 bytes; 52 us at 2048 columns).
 template <class T, class U, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   if (blockIdx.x >= a.sum_blocks) {
@@ -143,8 +149,8 @@ __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   }
   const u32 lane = threadIdx.x & 63;
   const u32 job = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (job >= a.jobs) return;
   const u32 chunk = job / a.strips, strip = job - chunk * a.strips;
-  if (chunk >= a.chunks) return;
   const u32 lo = chunk * a.rows, count = min(a.rows, a.T - lo);
   // lane i holds token i of the chunk, and its word; those outside are sorted last
   const u32 mine = min(lane, count - 1);
@@ -238,8 +244,8 @@ __global__ __launch_bounds__(256) void k_embed_bwd_few(const EmbedArgs a) {
   }
   const u32 lane = threadIdx.x & 63;
   const u32 job = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+  if (job >= a.jobs) return;
   const u32 t = job / a.strips, strip = job - t * a.strips;
-  if (t >= a.T) return;
   const u32 word = embed_key(a, t);
   if (word >= a.V) return;
   // the tokens of this word, 64 to a mask
@@ -283,8 +289,9 @@ __global__ __launch_bounds__(256) void k_embed_bwd_few(const EmbedArgs a) {
 
 // Joins the parts of the word that begins in chunk blockIdx.x / strips and goes
 // on: part 1 there, then part 0 of the chunks after it as far as the word goes.
-// The four wavefronts take every fourth part, eight at a time, and their sums are
-// added in order.
+// The four wavefronts take every fourth part, four or eight at a time, and their
+// sums are added in order.
+// 65537 tokens on 4099 words (a twentieth of them one word): 8 us.
 template <class T, class U, int VEC>
 __global__ __launch_bounds__(256) void k_embed_join(const EmbedArgs a) {
   __shared__ float sm[4][64 * VEC];

@@ -162,6 +162,8 @@ def test_embedding_own_checks():
         need = mx.train_lib().mxtrain_embedding_bwd_workspace(500, 100, 64, tt, wt)
         assert need > 0 and embed_bwd(T=500, wt=wt, tt=tt, bytes=need - 1) == WORKSPACE
         assert mx.train_lib().mxtrain_embedding_bwd_workspace(256, 100, 64, tt, wt) == 0
+    big = dict(T=1 << 29, H=513, ld_w=513, ld_t=513, bytes=1 << 62)
+    assert embed_bwd(**big) == OVERFLOW and embed_bwd(wt=F32, tt=F32, **{**big, "H": 257}) == OVERFLOW
     assert embed_bwd(V=0, table=None) == OK and embed_bwd(T=0, acc=1, ids=None, tokens=None, ws=None) == OK
     ws = mx.train_lib().mxtrain_embedding_bwd_workspace
     assert ws(0, 100, 64, 0, 0) == 0 and ws(8, 0, 64, 0, 0) == 0 and ws(8, 100, 0, 0, 0) == 0

@@ -88,8 +88,10 @@ RouteArgs route_args(const int32_t *rank, int dtype, int64_t T, int64_t k, int64
 }
 
 template <class T, int VEC>
-const void *dispatch_kernel() {
-  return (const void *)&k_dispatch<T, VEC>;
+const void *dispatch_kernel(bool nt) {
+  if constexpr (VEC > 1)
+    if (nt) return (const void *)&k_dispatch<T, VEC, true>;
+  return (const void *)&k_dispatch<T, VEC, false>;
 }
 
 // wtype: the weights', -1: none.
@@ -179,7 +181,8 @@ mxtrain_status mxtrain_dispatch_fwd(const void *x, int64_t ld_x, int dtype, cons
   a.ld_in = ld_x;
   a.out = xs;
   a.ld_out = ld_xs;
-  return route_launch(ROUTE_PICK(dispatch_kernel, dtype, H), a, stream);
+  const bool whole_lines = aligned(xs, 64) && ld_xs * size_of(dtype) % 64 == 0;
+  return route_launch(ROUTE_PICK(dispatch_kernel, dtype, H, whole_lines), a, stream);
 }
 
 mxtrain_status mxtrain_sort_dispatch(const void *x, int64_t ld_x, int dtype, const void *ids, int64_t ld_ids,

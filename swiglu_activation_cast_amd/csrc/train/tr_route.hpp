@@ -39,9 +39,13 @@ __device__ __forceinline__ float route_weight(const RouteArgs &a, int64_t pair) 
 __device__ __forceinline__ u32 route_row(const RouteArgs &a, int64_t pair) { return (u32)*gptr(a.rank + pair); }
 
 // A piece a thread, read once and written k times.  16384 tokens x 8, rows of 2048
-// bf16: 103 us, 5.9 TB/s over x and xs (with two pieces a thread 3 us more, with
-// stores through the caches 16).
-template <class T, int VEC>
+// bf16: 103 us, 5.9 TB/s over x and xs (with two pieces a thread 3 us more).
+//
+// NT: stores past the caches, where rows begin with a line (those 103 us would be
+// 118).  Other rows share lines with their neighbours, which other workgroups write:
+// rows of 257, 513 and 1025 bf16 take 26, 37 and 93 us with the sort through the
+// caches, 39, 59 and 102 past them.
+template <class T, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_dispatch(const RouteArgs a) {
   for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
     if (first + threadIdx.x >= a.pieces.total) continue;
@@ -53,7 +57,7 @@ __global__ __launch_bounds__(256) void k_dispatch(const RouteArgs a) {
     v.load(static_cast<const T *>(a.in) + t * a.ld_in + col);
     for (u32 j = 0; j < a.k; j++) {
       const u32 r = route_row(a, t * a.k + j);
-      if (r < a.R) v.store(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col);
+      if (r < a.R) v.template store<NT>(static_cast<T *>(a.out) + (int64_t)r * a.ld_out + col);
     }
   }
 }

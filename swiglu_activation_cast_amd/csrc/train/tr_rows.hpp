@@ -37,10 +37,11 @@ struct Piece {
   // Past the caches (what is written here is larger than they are, or read next
   // by another XCD) where 16 bytes a lane fill whole lines; two such stores 32
   // bytes apart would each write half lines to memory.
+  template <bool NT = true>
   __device__ __forceinline__ void store(T *p) const {
     if constexpr (VEC == 1) {
       store(p, 0, 1);
-    } else if constexpr (kWords == 4) {
+    } else if constexpr (kWords == 4 && NT) {
       __builtin_nontemporal_store(u32x4_t{w[0], w[1], w[2], w[3]}, (glob16)p);
     } else {
 #pragma unroll

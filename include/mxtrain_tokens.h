@@ -97,8 +97,8 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
  *   dweight   : dw_type [V, H], row stride ld_dw
  *   workspace : at least mxtrain_embedding_bwd_workspace(T, V, H, dy_type, dw_type)
  *               bytes (0 for few tokens, then it may be NULL), 16-byte aligned
- * Tokens are sorted by word and each word's rows summed in the order of the
- * tokens, in parts of at most 64 rows that are joined in order.  scale is finite
+ * A word's rows are summed in a fixed order (parts of at most 64 rows, each in the
+ * order of the tokens, that are joined in order).  scale is finite
  * (MXTRAIN_ERR_VALUE).  T, V, H < 2^31; in the gradient T times the strips of a
  * row, 256 columns of fp32 into fp32, 512 otherwise, at most 2^29
  * (MXTRAIN_ERR_OVERFLOW).

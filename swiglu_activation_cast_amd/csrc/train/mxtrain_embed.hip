@@ -68,10 +68,10 @@ const void *join_kernel() {
 constexpr int64_t kMaxJobs = INT32_MAX / 256;
 
 // Few enough tokens for the gradient without a sort (and every strip of each has
-// a wavefront).
+// a workgroup).
 bool embed_few(int64_t T, int64_t H, int64_t vec) {
   const int64_t strips = ((H + vec - 1) / vec + 63) / 64;
-  return T <= kEmbedFew && T * strips <= kMaxJobs;
+  return T <= kEmbedFew && T * strips <= kMaxJobs / 2;
 }
 
 // How the gradient cuts its work: chunks of 64 tokens, or fewer where that
@@ -158,7 +158,7 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   const int64_t zero_per = (H + zero_vec - 1) / zero_vec, zeros = accumulate ? 0 : V * zero_per;
   const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips;
   if (jobs > kMaxJobs) return MXTRAIN_ERR_OVERFLOW;
-  const int64_t sum_blocks = (jobs + 3) / 4;
+  const int64_t sum_blocks = few ? jobs : (jobs + 3) / 4;
   const int64_t zero_blocks = std::min<int64_t>((zeros + 255) / 256, INT32_MAX / 512);
   uint8_t *ws = static_cast<uint8_t *>(workspace);
   EmbedArgs a{};

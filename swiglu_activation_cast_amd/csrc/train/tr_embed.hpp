@@ -31,7 +31,7 @@ struct EmbedArgs {
   float *part;              // [chunks][2][strips * 64 * VEC]
   u32 rows;                 // tokens of a chunk
   u32 chunks, strips;       // and of the columns, 64 pieces each
-  u32 jobs;                 // summing wavefronts: chunks (tokens, if few) x strips
+  u32 jobs;                 // summing wavefronts: chunks x strips
   const uint8_t *flags;     // [V], 1: the word has tokens
   Pieces zeros;             // of dW's rows, 16 bytes each
   u32 sum_blocks;           // workgroups that sum; those after them write zeros
@@ -204,11 +204,12 @@ __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   leave(word == after);
 }
 
-// The gradient for up to 256 tokens in one launch, without a sort: the wavefronts
-// of a token sum all rows of its word, unless an earlier token has that word.  256
-// tokens on 32768 words x 512 bf16: 7.8 us (16.4 with the sort), on 4099 x 8192 fp32
-// 22 (30).  A word that all 256 tokens have is one wavefront's for each 64
-// pieces: 21 us (11.6).
+// The gradient for up to 256 tokens in one launch, without a sort: a token's
+// workgroup sums the rows of its word, unless an earlier token has that word.  Each
+// wavefront looks through 64 tokens and sums what it finds there; the four sums are
+// added in order.
+// 256 tokens on 32768 words x 512 bf16: 7.9 us (16.4 with the sort), on 219 words x
+// 555 4.1 (11.6), all of them one word x 2048 8.3 (11.6).
 constexpr u32 kEmbedFew = 256;
 
 // Zeros where no token has the word, 256 pieces (of at most 256 rows) at a time.
@@ -242,49 +243,56 @@ __global__ __launch_bounds__(256) void k_embed_bwd_few(const EmbedArgs a) {
     embed_zeros_few<U, VEC>(a);
     return;
   }
-  const u32 lane = threadIdx.x & 63;
-  const u32 job = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
-  if (job >= a.jobs) return;
-  const u32 t = job / a.strips, strip = job - t * a.strips;
+  constexpr int N = 8;
+  __shared__ float sm[4][64 * VEC];
+  __shared__ u32 found[4];  // tokens of the word that a wavefront has; ~0u: it is not this token's to sum
+  const u32 lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const u32 t = blockIdx.x / a.strips, strip = blockIdx.x - t * a.strips;
   const u32 word = embed_key(a, t);
   if (word >= a.V) return;
-  // the tokens of this word, 64 to a mask
-  constexpr int M = kEmbedFew / 64;
-  uint64_t same[M];
-  uint64_t earlier = 0;
-#pragma unroll
-  for (int m = 0; m < M; m++) {
-    const u32 i = m * 64 + lane;
-    same[m] = __ballot(i < a.T && embed_key(a, min(i, a.T - 1)) == word);
-    earlier |= __ballot(i < t) & same[m];
-  }
-  if (earlier) return;
+  const u32 i = wave * 64 + lane;
+  uint64_t same = __ballot(i < a.T && embed_key(a, min(i, a.T - 1)) == word);
+  const u32 mine = __ballot(i < t) & same ? ~0u : __popcll(same);
+  if (lane == 0) found[wave] = mine;
+  __syncthreads();
+  const u32 f0 = found[0], f1 = found[1], f2 = found[2], f3 = found[3];
+  if (f0 == ~0u || f1 == ~0u || f2 == ~0u || f3 == ~0u) return;
   const u32 piece = strip * 64 + lane;
   const bool in = piece * VEC < a.H;
   const T *dy = static_cast<const T *>(a.in) + piece_col<VEC>(in ? piece : 0, a.H);
   float sum[VEC] = {};
-  constexpr int N = 8;
+  while (same) {
+    // eight rows in flight, in the order of the tokens; past the last one it is read
+    // again and counts as zero
+    const u32 count = __popcll(same);
+    u32 token = 0;
+    Piece<T, VEC> d[N];
 #pragma unroll
-  for (int m = 0; m < M; m++)
-    while (same[m]) {
-      // eight rows in flight, in the order of the tokens; past the last one it is
-      // read again and counts as zero
-      const u32 count = __popcll(same[m]);
-      u32 token = 0;
-      Piece<T, VEC> d[N];
-#pragma unroll
-      for (int u = 0; u < N; u++) {
-        token = same[m] ? m * 64 + __builtin_ctzll(same[m]) : token;
-        same[m] &= same[m] - 1;
-        d[u].load(dy + (int64_t)token * a.ld_in);
-      }
-      // (no branches, behind which the compiler would move the loads)
-#pragma unroll
-      for (int u = 0; u < N; u++)
-#pragma unroll
-        for (int j = 0; j < VEC; j++) sum[j] += (u32)u < count ? d[u].get(j) : 0.0f;
+    for (int u = 0; u < N; u++) {
+      token = same ? wave * 64 + __builtin_ctzll(same) : token;
+      same &= same - 1;
+      d[u].load(dy + (int64_t)__builtin_amdgcn_readfirstlane(token) * a.ld_in);
     }
-  if (in) embed_write<U, VEC>(a, word, piece, sum);
+    // (no branches, behind which the compiler would move the loads)
+#pragma unroll
+    for (int u = 0; u < N; u++)
+#pragma unroll
+      for (int j = 0; j < VEC; j++) sum[j] += (u32)u < count ? d[u].get(j) : 0.0f;
+  }
+  if (mine == f0 + f1 + f2 + f3) {  // all of them are this wavefront's
+    if (in) embed_write<U, VEC>(a, word, piece, sum);
+    return;
+  }
+  // (where one wavefront has all, the others leave here)
+  if ((f0 != 0) + (f1 != 0) + (f2 != 0) + (f3 != 0) < 2) return;
+#pragma unroll
+  for (int j = 0; j < VEC; j++) sm[wave][j * 64 + lane] = sum[j];
+  __syncthreads();
+  if (wave != 0 || !in) return;
+#pragma unroll
+  for (int j = 0; j < VEC; j++)
+    sum[j] = ((sum[j] + sm[1][j * 64 + lane]) + sm[2][j * 64 + lane]) + sm[3][j * 64 + lane];
+  embed_write<U, VEC>(a, word, piece, sum);
 }
 
 // Joins the parts of the word that begins in chunk blockIdx.x / strips and goes

@@ -69,7 +69,7 @@ def check(got, want, tol):
 # without a sort (up to 256 tokens); one chunk, several; one workgroup sorts (up to
 # 8192), many; one, two and three digits; vocabularies smaller and larger than the
 # tokens; odd widths
-GRADS = [(1, 1, 1), (1, 1000, 5120), (5, 3, 7), (64, 64, 64), (65, 10, 513), (200, 600, 4), (256, 31, 520), (257, 30, 3), (700, 5000, 96), (3000, 40, 1000),
+GRADS = [(1, 1, 1), (1, 1000, 5120), (5, 3, 7), (64, 64, 64), (65, 10, 513), (200, 600, 4), (256, 31, 520), (257, 30, 3), (1024, 700, 300), (1025, 600, 65), (700, 5000, 96), (3000, 40, 1000),
          (8192, 1024, 40), (8193, 1023, 40), (9001, 4099, 258), (20000, 1, 72), (30011, 70001, 33), (9000, 1100000, 24)]
 
 
@@ -198,7 +198,7 @@ def test_gradient_against_differences():
 def test_wrong_arguments():
     w, ids = torch.randn((4, 8), device="cuda"), torch.zeros((3, 2), dtype=torch.int64, device="cuda")
     dy = torch.randn((3, 2, 8), device="cuda")
-    many, more = torch.randn((300, 8), device="cuda"), torch.zeros(300, dtype=torch.int64, device="cuda")
+    many, more = torch.randn((1100, 8), device="cuda"), torch.zeros(1100, dtype=torch.int64, device="cuda")
     for call, error in (
             (lambda: mx.mxtrain_embedding_fwd(w, ids.float()), TypeError),
             (lambda: mx.mxtrain_embedding_fwd(w, [0, 1]), TypeError),

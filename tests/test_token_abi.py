@@ -157,17 +157,17 @@ def test_embedding_checks(call):
 def test_embedding_own_checks():
     assert embed(T=0, tokens=None, ids=None) == OK
     assert embed_bwd(acc=2) == VALUE
-    assert embed_bwd(T=500, ws=None) == NULL and embed_bwd(T=500, ws=A + 8) == ALIGN
+    assert embed_bwd(T=5000, ws=None) == NULL and embed_bwd(T=5000, ws=A + 8) == ALIGN
     for wt, tt in ((BF16, BF16), (F32, BF16), (BF16, F32), (F32, F32)):
-        need = mx.train_lib().mxtrain_embedding_bwd_workspace(500, 100, 64, tt, wt)
-        assert need > 0 and embed_bwd(T=500, wt=wt, tt=tt, bytes=need - 1) == WORKSPACE
+        need = mx.train_lib().mxtrain_embedding_bwd_workspace(5000, 100, 64, tt, wt)
+        assert need > 0 and embed_bwd(T=5000, wt=wt, tt=tt, bytes=need - 1) == WORKSPACE
         assert mx.train_lib().mxtrain_embedding_bwd_workspace(256, 100, 64, tt, wt) == 0
     big = dict(T=1 << 29, H=513, ld_w=513, ld_t=513, bytes=1 << 62)
     assert embed_bwd(**big) == OVERFLOW and embed_bwd(wt=F32, tt=F32, **{**big, "H": 257}) == OVERFLOW
     assert embed_bwd(V=0, table=None) == OK and embed_bwd(T=0, acc=1, ids=None, tokens=None, ws=None) == OK
     ws = mx.train_lib().mxtrain_embedding_bwd_workspace
     assert ws(0, 100, 64, 0, 0) == 0 and ws(8, 0, 64, 0, 0) == 0 and ws(8, 100, 0, 0, 0) == 0
-    assert ws(500, 100, 64, 2, 0) == 0 and ws(500, 100, 64, 0, 2) == 0 and ws(BIG, 100, 64, 0, 0) == 0
+    assert ws(5000, 100, 64, 2, 0) == 0 and ws(5000, 100, 64, 0, 2) == 0 and ws(BIG, 100, 64, 0, 0) == 0
 
 
 def dropout(**kw):

@@ -140,7 +140,7 @@ __device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
 // one that begins here and goes on in the next.
 // 16384 tokens on 65536 words x 5120, bf16 into fp32: 228 us, 6.6 TB/s over dy and
 // dW, most of it zeros; 65537 on 4099 x 2050 bf16: 65 us, 4.4 TB/s (rows that
-// start at odd multiples of 4 bytes; 52 us at 2048 columns).
+// start at odd multiples of 4 bytes; 58 us at 2048 columns).
 template <class T, class U, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
   if (blockIdx.x >= a.sum_blocks) {

@@ -4,7 +4,7 @@
 namespace mxt {
 
 // One workgroup sorts everything (n <= kSortTile).  Bound by instructions, six for
-// each bit of each item's digit: 8192 keys of 16 bits 20 us, 1000 7.
+// each bit of each item's digit: 8192 keys of 16 bits 18 us, 1000 8.
 __global__ __launch_bounds__(kSortThreads) void k_sort_small(const SortArgs a) {
   __shared__ SortShared<16> sm;
   __shared__ u32 keys[kSortTile];
@@ -97,8 +97,8 @@ __global__ __launch_bounds__(kSortThreads) void k_sort_count(const SortArgs a) {
 }
 
 // Moves workgroup b's range to its places.  Bound by the way of its loads, counts
-// (128 workgroups' here) and items together, and eight barriers: 131072 pairs by 64
-// experts 7.4 us, by 256 9 (24 with the counts read one at a time).
+// and items together, and eight barriers: 131072 pairs by 64 experts in 128
+// workgroups 7.4 us (10 with the counts read one at a time).
 __global__ __launch_bounds__(kSortThreads) void k_sort_move(const SortArgs a) {
   __shared__ SortShared<16> sm;
   __shared__ u32 sums[2][4 * kSortThreads];  // [groups][bins]

@@ -12,10 +12,10 @@
 // wavefronts' counts are then summed in order.  No order of execution enters, so
 // the result is the one stable order.
 //
-// Up to 8192 items, one workgroup does all passes in LDS.  More are dealt to
-// up to 256 workgroups in contiguous ranges, and a pass is two launches: each
-// workgroup counts its digits, and then each adds up the counts of all
-// workgroups (from L2) to know its first place for every digit, and moves
+// Up to 8192 items (4096 where one pass does), one workgroup does all passes in
+// LDS.  More are dealt to up to 256 workgroups in contiguous ranges, and a pass is
+// two launches: each workgroup counts its digits, and then each adds up the counts
+// of all workgroups (from L2) to know its first place for every digit, and moves
 // its items.
 #pragma once
 #include "tr_rows.hpp"

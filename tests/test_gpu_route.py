@@ -44,12 +44,12 @@ def check_sort(got, want):
         assert np.array_equal(g.cpu().numpy(), w), name
 
 
-# one workgroup (up to 4096 pairs, 8192 with two digits) and many; one digit (up to 1023
-# experts), two;
-# ranges that end inside a tile
+# one workgroup (up to 4096 pairs, 8192 with two digits) and many, with one tile of
+# 8192 each and several; one digit (up to 1023 experts), two; ranges that end inside
+# a tile
 SORTS = [(0, 2, 4), (1, 1, 1), (1, 8, 300), (5, 3, 7), (63, 1, 64), (200, 8, 64), (1021, 5, 33), (1024, 8, 255),
          (4096, 2, 1023), (4097, 2, 1024), (900, 9, 65535), (8193, 1, 2), (16640, 4, 16), (16384, 8, 64),
-         (20011, 3, 1023), (20011, 3, 5000), (70001, 2, 65535), (300001, 2, 96), (0, 1, 5000)]
+         (20011, 3, 1023), (20011, 3, 5000), (70001, 2, 65535), (300001, 2, 96), (2500003, 2, 40), (2300001, 1, 5000), (0, 1, 5000)]
 
 
 @pytest.mark.parametrize("T,k,E", SORTS)

@@ -170,3 +170,17 @@ def test_empty_and_wrong_arguments():
             (lambda: mx.mxtrain_dropout_bwd(x, 0.5, 1, 2, state=torch.zeros(2, device="cuda")), TypeError)):
         with pytest.raises(error):
             call()
+
+
+@gpu
+@pytest.mark.parametrize("N", [8192, 8195])
+def test_read_past_the_caches(N):
+    """128 MB and more are read past the caches: the same bits as in two parts of columns, which are not."""
+    M = 8300
+    x, res = randn(M, N, 5, torch.bfloat16), randn(M, N, 6, torch.bfloat16)
+    assert x.numel() * 2 >= 2**27
+    y = mx.mxtrain_dropout_fwd(x, 0.3, 7, 8, residual=res)
+    assert torch.equal(y[:, :4096], mx.mxtrain_dropout_fwd(x[:, :4096], 0.3, 7, 8, residual=res[:, :4096]))
+    assert torch.equal(y[:4000], mx.mxtrain_dropout_fwd(x[:4000], 0.3, 7, 8, residual=res[:4000]))
+    ref, tol, _ = want(x[:40], 0.3, 7, 8, res[:40])
+    assert bool(((y[:40].double() - ref).abs() <= tol + 2.0 ** -8 * ref.abs()).all())

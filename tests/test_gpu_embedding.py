@@ -216,3 +216,15 @@ def test_wrong_arguments():
             (lambda: mx.mxtrain_embedding_bwd(many, more, 4, workspace=torch.zeros(4, device="cuda")), ValueError)):
         with pytest.raises(error):
             call()
+
+
+@pytest.mark.parametrize("H", [2048, 2051])
+def test_gradient_read_past_the_caches(H):
+    """128 MB of dy and more are read past the caches."""
+    T, V = 33000, 2000
+    g = gen(8)
+    dy = torch.randn((T, H), generator=g, device="cuda").bfloat16()
+    assert dy.numel() * 2 >= 2**27
+    ids = words(T, V, g, "zipf")
+    want, tol = ref_grad(dy, ids, V, 0.5)
+    check(mx.mxtrain_embedding_bwd(dy, ids, V, scale=0.5), want, tol)

@@ -313,3 +313,21 @@ def test_one_call_is_the_sort_and_the_move(T, k, E, dtype):
         want = mx.mxtrain_expert_sort(ids, E)
         assert all(torch.equal(a, b) for a, b in zip(index, want))
         assert torch.equal(xs, mx.mxtrain_dispatch_fwd(x, want[0], out=torch.zeros_like(xs)))
+
+
+@pytest.mark.parametrize("H", [2048, 2053])
+def test_rows_read_past_the_caches(H):
+    """128 MB of rows and more are read past the caches: the same bits as half of the tokens at a time, which is not."""
+    T, k, E = 8300, 4, 16
+    s = routed(T, k, E, H, torch.bfloat16, 11)
+    assert T * k * H * 2 >= 2**27 > T * k * H
+    y = mx.mxtrain_combine_fwd(s["rows"], s["rank"], s["w"], residual=s["res"])
+    dx = mx.mxtrain_dispatch_bwd(s["rows"], s["rank"])
+    dys, dw = mx.mxtrain_combine_bwd(s["dy"], s["rows"], s["rank"], s["w"])
+    want = torch.empty_like(dys)
+    for part in (slice(0, T // 2), slice(T // 2, T)):
+        rank, w, dy = s["rank"][part], s["w"][part], s["dy"][part]
+        assert torch.equal(y[part], mx.mxtrain_combine_fwd(s["rows"], rank, w, residual=s["res"][part]))
+        assert torch.equal(dx[part], mx.mxtrain_dispatch_bwd(s["rows"], rank))
+        assert torch.equal(dw[part], mx.mxtrain_combine_bwd(dy, s["rows"], rank, w, out=want)[1])
+    assert torch.equal(dys, want)

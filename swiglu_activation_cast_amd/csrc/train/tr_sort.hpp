@@ -1,22 +1,25 @@
 // tr_sort.hpp -- stable sort of small integer keys (gfx950): tokens by expert,
 // tokens by word.
 //
-// A pass sorts by one digit of at most 10 bits, least significant first: an
-// item's place is the number of items with a smaller digit plus the number of
+// An item's place is the number of items with a smaller key plus the number of
 // earlier ones with the same.  A key is id - first, or n_keys where that is
-// not in [0, n_keys): dropped items come last.
-//
-// Within a wavefront, the lanes with the same digit find each other by one
-// ballot for each bit; a lane's place among them is the number of lower lanes,
-// and the lowest adds their number to the wavefront's count of that digit.  The
-// wavefronts' counts are then summed in order.  No order of execution enters, so
+// not in [0, n_keys): dropped items come last.  No order of execution enters, so
 // the result is the one stable order.
 //
-// Up to 8192 items (4096 where one pass does), one workgroup does all passes in
-// LDS.  More are dealt to up to 256 workgroups in contiguous ranges, and a pass is
-// two launches: each workgroup counts its digits, and then each adds up the counts
-// of all workgroups (from L2) to know its first place for every digit, and moves
-// its items.
+// Few items are counted by comparing (up to 4096, or 8192 whose keys have more than
+// 10 bits): every workgroup compares its items with all.  That is one launch, in which
+// no workgroup waits for another.  Up to 32768 items with such long keys are sorted so
+// in tiles of 1024, and a second launch seeks each item in the other tiles.
+//
+// Others are sorted by digits of at most 10 bits, least significant first.  Within a
+// wavefront, the lanes with the same digit find each other by one ballot for each
+// bit; a lane's place among them is the number of lower lanes, and the lowest adds
+// their number to the wavefront's count of that digit.  The wavefronts' counts are
+// then summed in order.  Items are dealt to up to 256 workgroups in contiguous
+// ranges, and a pass is two launches: each workgroup counts its digits, and then each
+// adds up the counts of all workgroups (from L2) to know its first place for every
+// digit, and moves its items.  Up to 16384 items of one digit, each counts all of
+// them itself, in one launch.
 #pragma once
 #include "tr_rows.hpp"
 
@@ -27,6 +30,7 @@ constexpr int kSortThreads = 1024;          // and, one digit a thread, of most 
 constexpr int kSortItems = 8;               // items a thread in one tile
 constexpr int kSortTile = kSortThreads * kSortItems;
 constexpr int kSortBlocks = 256;
+constexpr int kSortMerge = 32768;           // most items that sorted tiles are merged of, all keys in LDS
 
 struct SortArgs {
   const void *ids;  // the keys' source in the first pass: [n / k, k] with row stride ld
@@ -38,9 +42,9 @@ struct SortArgs {
   u32 *key_out, *item_out;      // the next pass's source; in the last pass the sorted keys, or NULL
   int32_t *order, *rank, *ends;  // written by the last pass, each may be NULL; ends only where one pass does
   uint8_t *flags;                // [n_keys], 1 where an item has that key; may be NULL
-  u32 *counts;                   // [blocks][1 << bits]
-  u32 shift, bits, blocks, per;  // this pass's digit; workgroups and items of each (a multiple of 1024)
-  u32 passes;                    // one workgroup: passes of `bits` bits each
+  u32 *counts;                   // [blocks][1 << bits]; NULL: every workgroup counts all items
+  u32 shift, bits, blocks, per;  // this pass's digit; workgroups and items of each
+  u32 tile, flag_range;          // without digits: items of a tile (0: all); words whose flags a workgroup writes
   int32_t is_first, is_last;
 };
 
@@ -157,12 +161,12 @@ __device__ __forceinline__ u32 rank_tile(SortShared<W> &sm, const u32 *digit, u3
   return total;
 }
 
-// The flags are cleared by the first kernel (the first part of one workgroup's)
-// and set by the second.
+// The flags are cleared by the first kernel and set by the second (where one kernel
+// sorts, it does both).
 __device__ __forceinline__ void sort_clear_flags(const SortArgs &a) {
   if (!a.flags) return;  // 16 bytes at a time: they begin and end on multiples of it
   const int64_t step = (int64_t)gridDim.x * kSortThreads * 16;
-  for (int64_t i = (int64_t)(blockIdx.x * kSortThreads + threadIdx.x) * 16; i < a.n_keys; i += step)
+  for (int64_t i = ((int64_t)blockIdx.x * kSortThreads + threadIdx.x) * 16; i < a.n_keys; i += step)
     *gptr(reinterpret_cast<u32x4_t *>(a.flags + i)) = u32x4_t{};
 }
 

@@ -66,11 +66,12 @@ def check(got, want, tol):
     assert not bad.any(), f"{int(bad.sum())} of {bad.numel()} off"
 
 
-# without a sort (up to 256 tokens); one chunk, several; one workgroup sorts (up to
-# 8192), many; one, two and three digits; vocabularies smaller and larger than the
+# without a sort (up to 256 tokens); one chunk, several; sorts by comparing (up to 4096,
+# or 8192), in tiles (up to 32768), by one, two and three digits; vocabularies smaller and larger than the
 # tokens; odd widths
 GRADS = [(1, 1, 1), (1, 1000, 5120), (5, 3, 7), (64, 64, 64), (65, 10, 513), (200, 600, 4), (256, 31, 520), (257, 30, 3), (1024, 700, 300), (1025, 600, 65), (700, 5000, 96), (3000, 40, 1000),
-         (8192, 1024, 40), (8193, 1023, 40), (9001, 4099, 258), (20000, 1, 72), (30011, 70001, 33), (9000, 1100000, 24)]
+         (8192, 1024, 40), (8193, 1023, 40), (9001, 4099, 258), (20000, 1, 72), (30011, 70001, 33), (9000, 1100000, 24),
+         (32768, 1500, 16), (32769, 1500, 24), (40007, 1100000, 8)]
 
 
 @pytest.mark.parametrize("dt", TYPES)

@@ -44,12 +44,15 @@ def check_sort(got, want):
         assert np.array_equal(g.cpu().numpy(), w), name
 
 
-# one workgroup (up to 4096 pairs, 8192 with two digits) and many, with one tile of
-# 8192 each and several; one digit (up to 1023 experts), two; ranges that end inside
-# a tile
+# up to 4096 pairs (8192 of more than 1023 experts, fewer of very many), compared in one
+# launch, with 32 places a workgroup, or 128 from 16385 pairs and experts; up to 32768 of
+# more than 1023 experts, in tiles of 1024; up to 16384 of fewer, where every workgroup counts all; more, by digits:
+# one or two, with a tile of 8192 a workgroup and several; ranges that end inside a tile
 SORTS = [(0, 2, 4), (1, 1, 1), (1, 8, 300), (5, 3, 7), (63, 1, 64), (200, 8, 64), (1021, 5, 33), (1024, 8, 255),
          (4096, 2, 1023), (4097, 2, 1024), (900, 9, 65535), (8193, 1, 2), (16640, 4, 16), (16384, 8, 64),
-         (20011, 3, 1023), (20011, 3, 5000), (70001, 2, 65535), (300001, 2, 96), (2500003, 2, 40), (2300001, 1, 5000), (0, 1, 5000)]
+         (20011, 3, 1023), (20011, 3, 5000), (70001, 2, 65535), (300001, 2, 96), (2500003, 2, 40), (2300001, 1, 5000), (0, 1, 5000),
+         (31, 1, 33), (65, 1, 3), (2731, 3, 9), (8192, 1, 17000), (3000, 1, 65535), (9, 1, 40000), (4107, 2, 6), (12289, 1, 3000),
+         (8192, 2, 64), (16385, 1, 128), (10923, 3, 65535), (16384, 2, 7), (32769, 1, 7), (2048, 2, 64), (4097, 1, 1023), (16384, 2, 2000), (32769, 1, 1024), (5000, 1, 20000)]
 
 
 @pytest.mark.parametrize("T,k,E", SORTS)

@@ -204,8 +204,9 @@ mxtrain_status mxtrain_sort_dispatch(const void *x, int64_t ld_x, int dtype, con
     g.move.ld_in = ld_x;
     g.move.out = xs;
     g.move.ld_out = ld_xs;
-    // no more workgroups than run at once: each begins with a sort
-    const int64_t blocks = std::min<int64_t>((g.move.pieces.total + 255) / 256, 2048);
+    // half as many workgroups as run at once, since each begins with a sort: 1000 x 2
+    // rows of 4096 bf16 9.0 us, 12.1 with 2048; 2000 x 1 of 8192 fp32 25.4 and 25.0
+    const int64_t blocks = std::min<int64_t>((g.move.pieces.total + 255) / 256, 1024);
     return launch(ROUTE_PICK(sort_dispatch_kernel, dtype, H, T * k), blocks, 256, g, stream);
   }
   st = mxtrain_expert_sort(ids, ld_ids, id_type, T, k, first, G, rank, ends, order, workspace, workspace_bytes, stream);

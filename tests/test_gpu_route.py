@@ -318,6 +318,20 @@ def test_one_call_is_the_sort_and_the_move(T, k, E, dtype):
         assert torch.equal(xs, mx.mxtrain_dispatch_fwd(x, want[0], out=torch.zeros_like(xs)))
 
 
+@pytest.mark.parametrize("T,k,H", [(1024, 2, 4099), (2048, 1, 1030)])
+def test_one_call_with_several_steps(T, k, H):
+    """The form that sorts and moves in one launch, with more pieces than its workgroups take in one step."""
+    g = gen(H)
+    ids = torch.randint(-1, 12, (T, k), generator=g, device="cuda")
+    x = torch.randn((T, H), generator=g, device="cuda")
+    assert T * ((H + 3) // 4) > 1024 * 256
+    xs, rank, ends, order = mx.mxtrain_sort_dispatch(x, ids, 11)
+    check_sort((rank, ends, order), ref_sort(ids, 11, 0))
+    for j in range(k):
+        kept = rank[:, j] >= 0
+        assert torch.equal(xs[rank[kept, j].long()], x[kept])
+
+
 @pytest.mark.parametrize("H", [2048, 2053])
 def test_rows_read_past_the_caches(H):
     """128 MB of rows and more are read past the caches: the same bits as half of the tokens at a time, which is not."""

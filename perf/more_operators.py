@@ -142,9 +142,11 @@ def prepare(case, seed):
             s["rows"] = torch.zeros((n, H), dtype=dt, device=dev) if case["shards"] > 1 else None
         return s
     V = case["vocab"]
-    # words by falling frequency (Zipf), spread over the vocabulary
-    p = 1.0 / (torch.arange(V, device=dev) + 2.7)
-    words = torch.multinomial(p, T, replacement=True, generator=g)
+    # words by falling frequency (Zipf), spread over the vocabulary.  Drawn by whole numbers, whose running sums are
+    # the same every time: those of floating-point numbers are not on a GPU, and would move words from run to run
+    shares = (2.0 ** 40 / (torch.arange(V, dtype=torch.float64, device=dev) + 2.7)).long()
+    sums = torch.cumsum(shares, 0)
+    words = torch.searchsorted(sums, torch.randint(int(sums[-1]), (T,), generator=g, device=dev), right=True)
     s["t"] = torch.randperm(V, generator=g, device=dev)[words].to(IDS[case["ids"]])
     s["scale"] = math.sqrt(H)
     if case["op"] == "embed":

@@ -136,7 +136,9 @@ int64_t mxtrain_embedding_bwd_workspace(int64_t T, int64_t V, int64_t H, int dy_
   if (!type_ok(dy_type) || !type_ok(dw_type) || T <= 0 || V <= 0 || H <= 0) return 0;
   if (T > INT32_MAX || V > INT32_MAX || H > INT32_MAX) return 0;
   const int64_t vec = embed_vec(dy_type, dw_type, H);
-  return embed_few(T, H, vec) ? 0 : embed_plan(sort_plan(T, V, true), T, V, H, vec).bytes;
+  if (embed_few(T, H, vec)) return 0;
+  const EmbedPlan p = embed_plan(sort_plan(T, V, true), T, V, H, vec);
+  return (int64_t)p.chunks * p.strips > kMaxJobs ? 0 : p.bytes;
 }
 
 mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type, const void *ids, int64_t id_stride,
@@ -152,12 +154,12 @@ mxtrain_status mxtrain_embedding_bwd(const void *dy, int64_t ld_dy, int dy_type,
   const int64_t vec = embed_vec(dy_type, dw_type, H), zero_vec = vec == 1 ? 1 : 16 / size_of(dw_type);
   const EmbedPlan ep = embed_plan(sp, T, V, H, vec);
   const bool few = embed_few(T, H, vec);
+  const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips;
+  if (jobs > kMaxJobs) return MXTRAIN_ERR_OVERFLOW;
   if (!few && !workspace) return MXTRAIN_ERR_NULL;
   if (!few && !aligned(workspace, 16)) return MXTRAIN_ERR_ALIGN;
   if (!few && workspace_bytes < ep.bytes) return MXTRAIN_ERR_WORKSPACE;
   const int64_t zero_per = (H + zero_vec - 1) / zero_vec, zeros = accumulate ? 0 : V * zero_per;
-  const int64_t jobs = (few ? T : (int64_t)ep.chunks) * ep.strips;
-  if (jobs > kMaxJobs) return MXTRAIN_ERR_OVERFLOW;
   const int64_t sum_blocks = few ? jobs : (jobs + 3) / 4;
   const int64_t zero_blocks = std::min<int64_t>((zeros + 255) / 256, INT32_MAX / 512);
   uint8_t *ws = static_cast<uint8_t *>(workspace);

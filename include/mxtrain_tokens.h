@@ -98,8 +98,8 @@ mxtrain_status mxtrain_combine_bwd(const void *dy, int64_t ld_dy, const void *ys
  *   workspace : at least mxtrain_embedding_bwd_workspace(T, V, H, dy_type, dw_type)
  *               bytes (0 for few tokens, then it may be NULL, and for sizes that are
  *               refused), 16-byte aligned
- * A word's rows are summed in a fixed order (parts of at most 64 rows, each in the
- * order of the tokens, that are joined in order).
+ * A word's rows are summed in a fixed order: parts of at most 64 rows, each in the
+ * order of the tokens, then every fourth part, then the four sums, each in order.
  * scale is finite (MXTRAIN_ERR_VALUE).  T, V, H < 2^31; in the gradient
  * ceil(T / 64) times the strips of a row, 256 columns of fp32 into fp32, 512
  * otherwise, at most 2^23 - 1 (MXTRAIN_ERR_OVERFLOW).

@@ -8,7 +8,7 @@
 // are cut into chunks of at most 64; a wavefront takes a chunk and 64 pieces of the
 // columns, keeps the running sum in registers and writes it where the word
 // changes.  A word whose rows lie in several chunks leaves an fp32 part in each,
-// and a second kernel joins them in order.  Words without tokens (the sort
+// and a second kernel joins them in a fixed order.  Words without tokens (the sort
 // flags those that have some) get their zeros from further workgroups of the first
 // launch.
 #pragma once

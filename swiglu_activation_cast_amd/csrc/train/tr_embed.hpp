@@ -48,9 +48,10 @@ __device__ __forceinline__ u32 embed_key(const EmbedArgs &a, int64_t t) {
 }
 
 // VEC, here and below: columns that a thread holds, 16 bytes of the narrower type,
-// or 1 where rows are shorter than that.  N pieces a thread, whose loads of ids and
-// then of rows are in flight together: 16640 rows of 5120 bf16 out of 65536 50 us,
-// 4.8 TB/s over the distinct rows and y; 16 of 8192 3.2 us.
+// or 1 where rows are shorter than that.  N pieces a thread, whose loads of rows are
+// in flight together (those of ids are not: embed_key branches on their type, and
+// the compiler waits for each before the next): 16640 rows of 5120 bf16 out of 65536
+// 50 us, 4.8 TB/s over the distinct rows and y; 16 of 8192 3.2 us.
 template <class T, class U, int VEC, int N>
 __global__ __launch_bounds__(256) void k_embed(const EmbedArgs a) {
   const int64_t step = (int64_t)gridDim.x * (256 * N);

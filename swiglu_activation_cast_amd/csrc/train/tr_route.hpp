@@ -41,10 +41,12 @@ __device__ __forceinline__ u32 route_row(const RouteArgs &a, int64_t pair) { ret
 // A piece a thread, read once and written k times.  16384 tokens x 8, rows of 2048
 // bf16: 103 us, 5.9 TB/s over x and xs (with two pieces a thread 3 us more).
 //
-// NT: stores past the caches, where rows begin with a line (those 103 us would be
-// 118).  Other rows share lines with their neighbours, which other workgroups write:
-// rows of 257, 513 and 1025 bf16 take 26, 37 and 93 us with the sort through the
-// caches, 39, 59 and 102 past them.
+// NT: stores past the caches, where rows begin at multiples of 64 bytes (those 103 us
+// would be 118; rows of 544, 1056 and 2080 bf16, odd multiples of 64 bytes, take 30, 58
+// and 109 us so, 36, 68 and 129 through the caches).  Other rows share such pieces
+// of memory with their neighbours, which other workgroups write: rows of 257, 513 and
+// 1025 bf16 take 26, 37 and 93 us with the sort through the caches, 39, 59 and 102 past
+// them.
 template <class T, int VEC, bool NT>
 __global__ __launch_bounds__(256) void k_dispatch(const RouteArgs a) {
   for (int64_t first = (int64_t)blockIdx.x * 256; first < a.pieces.total; first += (int64_t)gridDim.x * 256) {
@@ -114,6 +116,10 @@ __global__ __launch_bounds__(256) void k_combine(const RouteArgs a) {
 // before the first is used.  16384 tokens x 8, rows of 2048 bf16: 221 us, 5.2 TB/s
 // over dy, ys and dys (at most as many bytes read as written, where a copy moves
 // 4.6); with a wavefront to a token 243 us.
+//
+// Stores past the caches whatever the rows' alignment: rows of 257, 513, 1024, 1025
+// and 2048 bf16 take 35, 72, 107, 132 and 220 us so, 43, 66, 113, 136 and 228 through
+// the caches.
 //
 // L < 64: rows of at most L pieces, 256 / L tokens to a workgroup (16384 tokens x
 // 8 rows of 130 bf16: 28 us with a wavefront to a token, 22 with 32 lanes).
@@ -198,8 +204,13 @@ __global__ __launch_bounds__((L == 64 ? 1024 : 256)) void k_combine_bwd(const Ro
 
 // The sort and the dispatch in one launch, for up to 2048 pairs (ITEMS for each of
 // 256 threads) of up to 255 groups: every workgroup ranks all pairs for itself, the
-// first writes the result down.  8 x 2 pairs, rows of 5120 bf16: 3.4 us (two
-// launches 5.5); 128 x 8 of 2048 5.4 (8.0); 256 x 8 7.5 (8.9).
+// first writes the result down.  8 x 2 pairs, rows of 5120 bf16: 4.0 us (two
+// launches 6.1); 128 x 8 of 2048 5.9 (8.4); 256 x 8 8.0 (9.3); 1000 x 2 of 4096 10.8
+// (9.4, and 3 us more of the host's time).
+//
+// Stores past the caches whatever the rows' alignment: 256 x 8 rows of 513, 1024 and
+// 1025 bf16 take 7.9, 7.5 and 8.2 us so, 7.7, 7.7 and 7.9 through the caches, 2000
+// rows of 4096 and 4099 12.2 and 12.8, 12.9 and 13.4.
 constexpr int kFewPairs = 2048, kFewGroups = 255;
 
 struct SortDispatchArgs {

@@ -118,9 +118,10 @@ __device__ __forceinline__ float *embed_part(const EmbedArgs &a, u32 chunk, u32 
 }
 
 // Zeros in the rows of words without tokens.  One store a thread, workgroup after
-// workgroup: 16384 tokens on 65536 words x 5120 fp32 take 267 us so, 325 where
-// wavefronts walk rows of their own (a front of single stores fills 1.3 GB at
-// 6.5-6.8 TB/s, such rows at 5.3) and 374 with stores through the caches.
+// workgroup: 16384 tokens on 65536 words x 5120 fp32 take 250 us so with the sort and
+// the join, 58 more where wavefronts walk rows of their own (a front of single stores
+// fills 1.3 GB at 6.5-6.8 TB/s, such rows at 5.3) and 107 more with stores through
+// the caches.
 template <class U, int VEC>
 __device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
   constexpr int Z = VEC == 1 ? 1 : 16 / (int)sizeof(U);
@@ -139,7 +140,7 @@ __device__ __forceinline__ void embed_zeros(const EmbedArgs &a) {
 
 // Part 0 of a chunk belongs to a word that began in an earlier chunk, part 1 to
 // one that begins here and goes on in the next.
-// 16384 tokens on 65536 words x 5120, bf16 into fp32: 228 us, 6.6 TB/s over dy and
+// 16384 tokens on 65536 words x 5120, bf16 into fp32: 230 us, 6.6 TB/s over dy and
 // dW, most of it zeros; 65537 on 4099 x 2050 bf16: 65 us, 4.4 TB/s (rows that
 // start at odd multiples of 4 bytes; 58 us at 2048 columns).
 template <class T, class U, int VEC, bool NT>
